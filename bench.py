@@ -121,6 +121,7 @@ def roofline(wl, name: str, ms: float, nbytes: dict, flops: dict) -> dict:
 def algorithmic_bytes(wl, idx: np.ndarray) -> dict:
     """Bytes the path must move per step, by phase (the metric's definition:
     indexer keys + key scales + selected KV rows + outputs)."""
+    from indexed_sparse_attention_lightning_b200 import workloads as W
     sp = wl.spec
     V = wl.visible.astype(np.int64)
     key_b = sp.d_index * {"e4m3": 1, "mxfp8": 1, "bf16": 2, "f32": 4}[sp.index_dtype]
@@ -137,6 +138,9 @@ def algorithmic_bytes(wl, idx: np.ndarray) -> dict:
             sel = idx[t][idx[t] >= 0]
             tiles += np.unique(sel // tile_t).size * (sp.d_latent // tile_d)
         rows = int((n_sel * row_b).sum()) + 4 * tiles
+    elif sp.kv_dtype in W.FP4_GROUP:
+        row_b = sp.d_latent // 2 + sp.d_latent // W.FP4_GROUP[sp.kv_dtype] + 2 * sp.d_rope
+        rows = int((n_sel * row_b).sum())
     else:
         row_b = (sp.d_latent + sp.d_rope) * (2 if sp.kv_dtype == "bf16" else 4)
         rows = int((n_sel * row_b).sum())
@@ -324,6 +328,7 @@ def input_prep_bytes(wl, with_kv: bool) -> int:
     read, its e4m3 codes and scales written; per new token the bf16 key read and
     its code row and scale written, and (with_kv) the bf16 latent row read and
     its stored form written."""
+    from indexed_sparse_attention_lightning_b200 import workloads as W
     sp = wl.spec
     n, h, d = wl.n_q, sp.h_index, sp.d_index
     b = n * h * d * 2 + n * h * d + n * h * 4
@@ -332,6 +337,8 @@ def input_prep_bytes(wl, with_kv: bool) -> int:
         D = sp.d_latent + sp.d_rope
         if sp.kv_dtype == "e4m3":
             stored = sp.d_latent + 2 * sp.d_rope + 4 * (sp.d_latent // sp.kv_tile[1])
+        elif sp.kv_dtype in W.FP4_GROUP:
+            stored = sp.d_latent // 2 + sp.d_latent // W.FP4_GROUP[sp.kv_dtype] + 2 * sp.d_rope
         else:
             stored = D * (2 if sp.kv_dtype == "bf16" else 4)
         b += n * (D * 2 + stored)
@@ -414,6 +421,7 @@ def serving_inputs(wl) -> dict:
     (``k_new``/``kv_new``, None where the pool takes no single tokens: a bf16
     index pool, or a latent cache with one scale per page)."""
     import torch
+    from indexed_sparse_attention_lightning_b200 import workloads as W
     sp = wl.spec
     out = {k: torch.from_numpy(getattr(wl, k)) for k in ("q_seq", "q_pos", "w", "q")}
     ps = sp.page_size
@@ -436,6 +444,12 @@ def serving_inputs(wl) -> dict:
     elif sp.kv_dtype == "bf16":
         kv = torch.from_numpy(wl.kv.reshape(-1, sp.d_qk)[rows].view(np.int16))
         out["kv_new"] = kv.view(torch.bfloat16)
+    elif sp.kv_dtype in W.FP4_GROUP:
+        lat = W.fp4_value(wl.kv.reshape(-1, sp.d_latent // 2)[rows],
+                          wl.kv_scale.reshape(wl.num_pages * ps, -1)[rows], sp.kv_dtype)
+        rope = torch.from_numpy(wl.kv_rope.reshape(-1, sp.d_rope)[rows].view(np.int16))
+        out["kv_new"] = torch.cat([torch.from_numpy(lat).bfloat16(), rope.view(torch.bfloat16)],
+                                  dim=1)
     elif sp.kv_tile[0] == 1:
         st, sd = sp.kv_tile
         codes = torch.from_numpy(wl.kv.reshape(-1, sp.d_latent)[rows]).view(torch.float8_e4m3fn)

@@ -19,7 +19,12 @@
  * Inference" §4): index keys as e4m3 with one fp32 scale per token, the latent
  * as e4m3 with one fp32 scale per tile of tokens x latent dims (a whole page
  * by default; rope stays bf16).  Input preparation quantises the query and
- * appends new tokens in these formats.
+ * appends new tokens in these formats.  The latent may also be held in 4 bits
+ * (e2m1 codes with one small scale per 32 or 16 dims): a row then takes about
+ * a third of its bf16 size ("Long-Context LLM Inference Optimization": a cache
+ * footprint below a quarter of the original).  A cache that outgrows its
+ * memory is shrunk by the attention its positions received: see
+ * sa_accumulate_weights and sa_evict_tokens.
  *
  * Conventions for every entry point
  *  - All pointers marked "device" are CUDA device pointers owned by the
@@ -69,9 +74,13 @@ typedef enum sa_dtype {
     SA_F32 = 0,
     SA_BF16 = 1,
     SA_E4M3 = 2,              /* OCP e4m3fn code bytes, always paired with fp32 scales */
-    SA_MXFP8 = 3              /* index query and keys only: e4m3fn code bytes with one E8M0
+    SA_MXFP8 = 3,             /* index query and keys only: e4m3fn code bytes with one E8M0
                                * scale byte per 32 consecutive values (the OCP MX format:
                                * scale = 2^(byte - 127); byte 255 is NaN) */
+    SA_MXFP4 = 4,             /* latent cache only: e2m1 codes, two to a byte (dim 2i in the
+                               * low half of byte i), with one E8M0 scale byte per 32 dims */
+    SA_NVFP4 = 5              /* latent cache only: e2m1 codes as above with one e4m3fn scale
+                               * byte per 16 dims */
 } sa_dtype;
 
 /* Paged caches of one attention layer.
@@ -104,12 +113,18 @@ typedef struct sa_cache {
     int32_t d_index;
 
     /* MLA latent KV rows */
-    sa_dtype kv_dtype;           /* SA_BF16, SA_E4M3 or SA_F32 */
+    sa_dtype kv_dtype;           /* SA_BF16, SA_E4M3, SA_MXFP4, SA_NVFP4 or SA_F32 */
     const void *kv;              /* SA_F32/SA_BF16: [num_pages, page_size, d_latent + d_rope]
-                                  * SA_E4M3: latent codes [num_pages, page_size, d_latent] */
-    const void *kv_rope;         /* SA_E4M3 only: bf16 [num_pages, page_size, d_rope] */
-    const float *kv_scale;       /* SA_E4M3 only: fp32 [num_pages, page_size / kv_scale_tokens,
-                                  * d_latent / kv_scale_dims], one scale per tile */
+                                  * SA_E4M3: latent codes [num_pages, page_size, d_latent]
+                                  * SA_MXFP4/SA_NVFP4: [num_pages, page_size, d_latent / 2]
+                                  * bytes of two codes; d_latent a multiple of 32 */
+    const void *kv_rope;         /* SA_E4M3, SA_MXFP4, SA_NVFP4: bf16 [num_pages, page_size,
+                                  * d_rope]; d_rope a multiple of 8 for the 4-bit formats */
+    const float *kv_scale;       /* SA_E4M3: fp32 [num_pages, page_size / kv_scale_tokens,
+                                  * d_latent / kv_scale_dims], one scale per tile;
+                                  * SA_MXFP4: E8M0 bytes [num_pages, page_size, d_latent / 32],
+                                  * SA_NVFP4: e4m3fn bytes [num_pages, page_size,
+                                  * d_latent / 16] (pass the byte array's address) */
     int32_t d_latent;            /* 512 (production) */
     int32_t d_rope;              /* 64 (production) */
     /* SA_E4M3 scale tile: one fp32 scale per kv_scale_tokens tokens of a page
@@ -119,7 +134,8 @@ typedef struct sa_cache {
      * "Long-Context LLM Inference Optimization", Layered Quantization): that is
      * (1, 128).  kv_scale_tokens divides page_size; kv_scale_dims divides
      * d_latent and is a multiple of 16.  0 and 0 mean one scale per page
-     * (page_size x d_latent). */
+     * (page_size x d_latent).  The 4-bit formats fix their own: both must be 0
+     * with them. */
     int32_t kv_scale_tokens;
     int32_t kv_scale_dims;
 } sa_cache;
@@ -162,7 +178,10 @@ enum {
     SA_WS_TOPK = 2,
     SA_WS_ATTN = 4,
     SA_WS_DECODE = 8,
-    SA_WS_APPEND = 16             /* sa_append_tokens alone: `query` may be NULL */
+    SA_WS_APPEND = 16,            /* sa_append_tokens or sa_read_tokens alone: `query` may be
+                                   * NULL */
+    SA_WS_WEIGHTS = 32,           /* sa_accumulate_weights */
+    SA_WS_EVICT = 64              /* sa_evict_tokens alone: `query` may be NULL, top_k = budget */
 };
 
 /* Bytes of device workspace the entry points in `uses` (an OR of SA_WS_*)
@@ -320,6 +339,13 @@ SA_API sa_status sa_combine_partials(const float *o_part, const float *lse_part,
  * FP8 rule, per group of values, in fp32: amax = max |x|, scale = amax / 448
  * (1 for an all-zero group), code = e4m3(x / scale) with an IEEE
  * round-to-nearest division, rounded to nearest even and saturated to +-448.
+ * 4-bit rules, per group, in fp32:
+ *   SA_MXFP4 (OCP MX, 32 values): scale = 2^(floor(log2 amax) - 2), at least
+ *     2^-127 (1 for an all-zero group);
+ *   SA_NVFP4 (16 values): scale = e4m3(min(amax / 6, 448)) rounded to nearest
+ *     even (1 for an all-zero group); where that rounds to 0 every code is +0;
+ *   code = e2m1(x / scale) with an IEEE round-to-nearest division, rounded to
+ *     nearest (ties to the even code) and saturated to +-6.
  * Inputs must be finite: a NaN or infinity gives unspecified codes. */
 
 /* Indexer query -> e4m3 codes + one fp32 scale per (token, head): the form
@@ -353,6 +379,8 @@ typedef struct sa_new_tokens {
  *    kv_scale_dims values with its scales, the rope as bf16.  An SA_E4M3 pool
  *    needs kv_scale_tokens == 1: a scale shared by several tokens would force
  *    the others to be requantised, so other tiles return SA_ERR_UNSUPPORTED.
+ *    SA_MXFP4 / SA_NVFP4 pool -> the latent quantised in the format's groups
+ *    with its scale bytes, the rope as bf16.
  * The pools named by `cache` (k_index, k_index_scale, kv, kv_rope, kv_scale)
  * are written in place and must be writable device memory; seq_len is neither
  * read nor changed (the caller advances it), so a position is not checked
@@ -370,13 +398,94 @@ typedef struct sa_new_tokens {
 SA_API sa_status sa_append_tokens(const sa_cache *cache, const sa_new_tokens *tokens,
                                   void *workspace, size_t workspace_bytes, void *stream);
 
+/* The reverse of the latent half of sa_append_tokens: the latent + rope row of
+ * each token (seq[i], pos[i]) as the values the pool stands for, into out
+ * (device [n, d_latent + d_rope] in out_dtype, SA_BF16 or SA_F32; 4-bit
+ * values are exact in bf16 unless they leave its range, SA_E4M3 and SA_F32
+ * pools are rounded to nearest even).  The same token may be asked for more than
+ * once.  A token that sa_append_tokens would skip is recorded in the same way
+ * and its output row is set to zero.  An SA_E4M3 pool may have any scale tile.
+ * workspace: as for sa_append_tokens (SA_WS_APPEND). */
+SA_API sa_status sa_read_tokens(const sa_cache *cache, int32_t n, const int32_t *seq,
+                                const int32_t *pos, void *out, sa_dtype out_dtype,
+                                void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Shrinking a cache by the attention its positions received -----------
+ * A long-lived sequence keeps a running sum of the attention weight that each
+ * of its positions received (sa_accumulate_weights, after a step's attention)
+ * and, when it outgrows its budget, keeps its first tokens, its last tokens
+ * and the positions of the largest sums (sa_evict_tokens). */
+
+/* Attention weights of one step, added to per-sequence running sums:
+ *   acc_out[b * ld_acc + s] = decay * acc_in[b * ld_acc + s]
+ *       + sum over queries t with q_seq[t] = b and entries k with idx[t][k] = s of
+ *         sum over heads h of exp(sm_scale * q[t,h,:] . kv[s,:] - lse[t,h])
+ * for 0 <= s < seq_len[b] of every sequence b; the rest of acc_out is left as
+ * it was.  idx (device int32 [n_q, top_k]) and lse (device fp32 [n_q, heads])
+ * are what sa_sparse_mla_attn or sa_decode took and returned (for a cache
+ * split over GPUs: the rank's local positions with the combined lse), so that
+ * a query's weights sum to `heads`; -1 entries are skipped, an entry that
+ * occurs twice counts twice, as it does in the attention, and a head with
+ * lse = -inf (nothing selected) adds nothing.  acc_in may be NULL (zeros) or
+ * equal to acc_out; otherwise the two must not overlap.  decay must be finite.
+ * ld_acc >= query->max_visible; a sequence longer than ld_acc, or than its
+ * page-table row, is reported (SA_DETAIL_BAD_POSITION) and written up to there.
+ * Sums are fp32, taken in the order of t, so results do not change from run
+ * to run.  Only the latent cache and the attention query are read: the
+ * query's index fields may be NULL.  Workspace: SA_WS_WEIGHTS. */
+SA_API sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *query,
+                                       const int32_t *idx, int32_t top_k, const float *lse,
+                                       const float *acc_in, float decay, float *acc_out,
+                                       int64_t ld_acc, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* Keeps at most `budget` tokens of every sequence of `src` and moves them, in
+ * order, to the pages that `dst` names.
+ * A sequence of n = src->seq_len[b] <= budget tokens keeps all of them.  A
+ * longer one keeps positions [0, keep_first), [n - keep_last, n) and, of those
+ * between, the budget - keep_first - keep_last with the largest acc[b * ld_acc
+ * + s] (device fp32 [batch, ld_acc]; ties to the lower position; a NaN counts
+ * as the largest).  keep_first + keep_last <= budget.
+ * The i-th kept token (ascending) moves to position i of sequence b in dst:
+ * its index key and scale, its latent row, rope and scales, byte for byte.
+ * dst has src's batch, formats, dims and page size and its own page table
+ * (dst->max_pages * page_size >= budget); its pools may be src's own, with
+ * the destination pages disjoint from every page that src reads -- except
+ * that a sequence which keeps all its tokens may keep its own pages, in the
+ * same order.  src's seq_len and page table are not changed: afterwards the
+ * caller frees the old pages.  src and dst must not share seq_len.
+ * Written besides the pools:
+ *   dst->seq_len[b]  the kept count;
+ *   src_pos          device int32 [batch, budget], or NULL: the original
+ *                    positions, ascending, padded with -1;
+ *   acc_out          device fp32 [batch, ld_out], ld_out >= budget, or NULL: the
+ *                    kept tokens' acc, zeros behind them up to ld_out.  May not
+ *                    overlap acc.
+ * Positions in dst are cache positions: rope phases stay as they were stored,
+ * so a caller that rotates by position keeps its own count of tokens.
+ * A sequence whose length is negative or past max_pages * page_size or ld_acc
+ * (SA_DETAIL_BAD_POSITION), or with a page id outside [0, num_pages) among the
+ * pages of its n tokens in src or of its kept tokens in dst
+ * (SA_DETAIL_BAD_PAGE), is skipped whole: nothing of it is moved, its dst
+ * length is 0, its src_pos -1 and its acc_out zero.
+ * An SA_E4M3 latent needs kv_scale_tokens == 1 (a scale shared by several
+ * tokens cannot move with one of them): other tiles return
+ * SA_ERR_UNSUPPORTED.  Workspace: sa_workspace_size(src, NULL, budget,
+ * SA_WS_EVICT). */
+SA_API sa_status sa_evict_tokens(const sa_cache *src, const float *acc, int64_t ld_acc,
+                                 int32_t budget, int32_t keep_first, int32_t keep_last,
+                                 const sa_cache *dst, float *acc_out, int64_t ld_out,
+                                 int32_t *src_pos, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+
 /* Device-side status of the most recent call that used `workspace`.
  * Synchronises `stream`.  Returns SA_OK, SA_ERR_DEVICE_FAULT or
  * SA_ERR_TIMEOUT; *detail (may be NULL) receives an SA_DETAIL_* code. */
 enum {
     SA_DETAIL_NONE = 0,
     SA_DETAIL_BAD_PAGE = 1,       /* page id outside [0, num_pages) */
-    SA_DETAIL_BAD_POSITION = 2,   /* q_pos >= seq_len, or q_seq outside [0, batch) */
+    SA_DETAIL_BAD_POSITION = 2,   /* q_pos >= seq_len, q_seq outside [0, batch), or a length
+                                   * that does not fit */
     SA_DETAIL_BAD_INDEX = 3,      /* selected index outside [0, q_pos] */
     SA_DETAIL_WAIT_TIMEOUT = 4    /* a bounded wait inside a kernel gave up */
 };

@@ -64,6 +64,25 @@ def _need_rows(t, name: str, n_rows: int, min_cols: int) -> None:
         raise SaError(_abi.SA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}")
 
 
+def _need_sums(t, name: str, batch: int, min_cols: int) -> int:
+    """Per-sequence running sums: a contiguous CUDA fp32 matrix of `batch` rows
+    (they are written up to their ends).  Returns the row length."""
+    _need(t, name, torch.float32)
+    if t.dim() != 2 or t.shape[0] != batch or t.shape[1] < max(1, min_cols):
+        raise SaError(_abi.SA_ERR_INVALID_ARG, f"{name} has shape {tuple(t.shape)}, expected "
+                                               f"({batch}, >= {max(1, min_cols)})")
+    return int(t.shape[1])
+
+
+def _need_here(where: str, *tensors) -> None:
+    """The kernels run on the current device: refuse tensors of another one."""
+    here = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != here:
+            raise SaError(_abi.SA_ERR_INVALID_ARG, f"{where}: a tensor is on {t.device}, the "
+                                                   f"current device is cuda:{here}")
+
+
 def _stream(stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream()
@@ -194,9 +213,12 @@ def host_queries(wl, pin: bool = True) -> dict:
 
 # ---------------------------------------------------------------- workspace ---
 
-def workspace_size(cache: DeviceCache, queries: DeviceQueries, top_k: int, uses: int) -> int:
-    c, q = cache.struct(), queries.struct()
-    n = _abi.lib().sa_workspace_size(ctypes.byref(c), ctypes.byref(q), top_k, uses)
+def workspace_size(cache: DeviceCache, queries: Optional[DeviceQueries], top_k: int,
+                   uses: int) -> int:
+    """``queries`` may be None for SA_WS_APPEND and SA_WS_EVICT (top_k = the budget)."""
+    c = cache.struct()
+    q = None if queries is None else ctypes.byref(queries.struct())
+    n = _abi.lib().sa_workspace_size(ctypes.byref(c), q, top_k, uses)
     if n == 0:
         raise SaError(_abi.SA_ERR_INVALID_ARG, "sa_workspace_size")
     return int(n)
@@ -435,3 +457,87 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
                                       _stream(stream)),
           "sa_append_tokens")
     return ws
+
+
+def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=None,
+                out_dtype: str = "bf16", ws=None, stream=None):
+    """Latent + rope rows of tokens (sequence, position) as the values the pool
+    stands for: [n, d_latent + d_rope] in ``out_dtype`` ("bf16" or "f32"; taken
+    from ``out`` when given).  Returns (out, ws): the workspace's status word
+    records tokens that do not exist, whose rows are zero."""
+    n = int(seq.numel())
+    _need(seq, "seq", torch.int32, (n,))
+    _need(pos, "pos", torch.int32, (n,))
+    if out is None:
+        dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+        out = torch.empty((n, cache.d_latent + cache.d_rope), dtype=dt, device=seq.device)
+    _need(out, "out", (torch.bfloat16, torch.float32), (n, cache.d_latent + cache.d_rope))
+    if ws is None:
+        ws = workspace(workspace_size(cache, None, 0, _abi.SA_WS_APPEND), seq.device)
+    _need(ws, "ws")
+    _need_here("read_tokens", cache.kv, seq, pos, out, ws)
+    c = cache.struct()
+    check(_abi.lib().sa_read_tokens(ctypes.byref(c), n, _ptr(seq), _ptr(pos), _ptr(out),
+                                    _in_dtype(out), _ptr(ws), ws.numel(), _stream(stream)),
+          "sa_read_tokens")
+    return out, ws
+
+
+# -------------------------------------- shrinking a cache by its attention ---
+
+def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
+                       lse: torch.Tensor, acc: Optional[torch.Tensor], decay: float = 1.0,
+                       out=None, ws=None, stream=None) -> torch.Tensor:
+    """Attention weight that each cached position received from these queries,
+    summed over heads and queries, on top of ``decay * acc``: fp32 rows [batch,
+    >= max_visible] per sequence.  ``idx`` and ``lse`` are the attention's own.
+    ``acc`` may be None (zeros); ``out`` defaults to ``acc`` (in place), or to a
+    new zero-filled [batch, max_visible].  Both are contiguous, with rows of the
+    same length; only positions below each sequence's length are written."""
+    batch = int(cache.page_table.shape[0])
+    if out is None:
+        out = acc if acc is not None else torch.zeros(
+            (batch, max(1, queries.max_visible)), dtype=torch.float32, device=idx.device)
+    _need(idx, "idx", torch.int32, (queries.n_q, top_k))
+    _need(lse, "lse", torch.float32, (queries.n_q, queries.heads))
+    ld = _need_sums(out, "out", batch, queries.max_visible)
+    if acc is not None and _need_sums(acc, "acc", batch, queries.max_visible) != ld:
+        raise SaError(_abi.SA_ERR_INVALID_ARG, "accumulate_weights: acc and out rows differ")
+    if ws is None:
+        ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_WEIGHTS), idx.device)
+    _need(ws, "ws")
+    _need_here("accumulate_weights", cache.kv, queries.q, idx, lse, acc, out, ws)
+    c, q = cache.struct(), queries.struct()
+    check(_abi.lib().sa_accumulate_weights(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
+                                           _ptr(lse), _ptr(acc), decay, _ptr(out), ld, _ptr(ws),
+                                           ws.numel(), _stream(stream)),
+          "sa_accumulate_weights")
+    return out
+
+
+def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: DeviceCache,
+                 keep_first: int = 0, keep_last: int = 0, acc_out=None, src_pos=None, ws=None,
+                 stream=None) -> torch.Tensor:
+    """Keep at most ``budget`` tokens of every sequence -- the first
+    ``keep_first``, the last ``keep_last`` and those of the largest ``acc``
+    between -- and move them, in order, to the pages of ``dst`` (a cache of the
+    same formats with its own page table and lengths, which are written; its
+    pools may be the same).  ``acc_out`` [batch, >= budget] receives the kept
+    sums, zeros behind them.  Returns the kept tokens' original positions,
+    int32 [batch, budget], ascending, padded with -1."""
+    batch = int(cache.page_table.shape[0])
+    ld = _need_sums(acc, "acc", batch, 1)
+    if src_pos is None:
+        src_pos = torch.empty((batch, budget), dtype=torch.int32, device=acc.device)
+    _need(src_pos, "src_pos", torch.int32, (batch, budget))
+    ld_out = 0 if acc_out is None else _need_sums(acc_out, "acc_out", batch, budget)
+    if ws is None:
+        ws = workspace(workspace_size(cache, None, budget, _abi.SA_WS_EVICT), acc.device)
+    _need(ws, "ws")
+    _need_here("evict_tokens", cache.kv, dst.kv, dst.seq_len, acc, acc_out, src_pos, ws)
+    c, d = cache.struct(), dst.struct()
+    check(_abi.lib().sa_evict_tokens(
+        ctypes.byref(c), _ptr(acc), ld, budget, keep_first, keep_last, ctypes.byref(d),
+        _ptr(acc_out), ld_out, _ptr(src_pos), _ptr(ws), ws.numel(), _stream(stream)),
+        "sa_evict_tokens")
+    return src_pos

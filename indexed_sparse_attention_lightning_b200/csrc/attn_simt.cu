@@ -4,7 +4,7 @@
 // ("Optimizing Next-Gen LLM Inference" §3.3: attention on the selected
 // positions only, reading the cache by index):
 //     z_s = sm_scale * q[t,h,:] . kv[s,:],   out = sum_s softmax(z)_s kv[s,0:dl]
-// An e4m3 latent is dequantised with its page-tile scale while it is staged
+// An e4m3 or 4-bit latent is dequantised with its scales while it is staged
 // ("Optimizing Next-Gen LLM Inference" §4: dequantisation fused into attention,
 // no dequantised cache is materialised).  Rows are staged through shared
 // memory 32 at a time and shared by a group of heads; softmax is online in
@@ -23,21 +23,6 @@ constexpr int kMaxOut = 2;    // output columns per thread: d_latent <= 512
 __device__ __forceinline__ float load_q(const PathParams &p, int64_t i) {
     if (p.q_dtype == SA_BF16) return bf16_bits_to_float(static_cast<const uint16_t *>(p.q)[i]);
     return static_cast<const float *>(p.q)[i];
-}
-
-__device__ __forceinline__ float load_kv(const PathParams &p, int64_t row, int dd) {
-    const int D = p.d_latent + p.d_rope;
-    switch (p.kv_dtype) {
-    case SA_F32: return static_cast<const float *>(p.kv)[row * D + dd];
-    case SA_BF16: return bf16_bits_to_float(static_cast<const uint16_t *>(p.kv)[row * D + dd]);
-    default:
-        if (dd < p.d_latent) {
-            uint8_t c = static_cast<const uint8_t *>(p.kv)[row * p.d_latent + dd];
-            return e4m3x2_to_float2(c).x * kv_scale_at(p, row, dd);
-        }
-        return bf16_bits_to_float(
-            static_cast<const uint16_t *>(p.kv_rope)[row * p.d_rope + (dd - p.d_latent)]);
-    }
 }
 
 template <int HG>
@@ -92,7 +77,7 @@ attn_simt_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K,
         for (int e = tid; e < kRows * D; e += kThreads) {
             const int r = e / D, dd = e - r * D;
             const int64_t row = row_s[r];
-            rows_s[r * ldr + dd] = row >= 0 ? load_kv(p, row, dd) : 0.f;
+            rows_s[r * ldr + dd] = row >= 0 ? kv_value(p, row, dd) : 0.f;
         }
         __syncthreads();
         for (int pr = tid; pr < HG * kRows; pr += kThreads) {

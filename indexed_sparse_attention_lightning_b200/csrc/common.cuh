@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_fp4.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -39,10 +40,30 @@ __device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t two) {
     return __half22float2(hh);
 }
 
+// One byte of two e2m1 codes (low half first) -> two floats, exact.
+__device__ __forceinline__ float2 e2m1x2_to_float2(uint32_t byte) {
+    __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+    __half2 hh = *reinterpret_cast<__half2 *>(&h);
+    return __half22float2(hh);
+}
+
+// The 4-bit latent formats: dims per scale byte, and the byte's value.
+__host__ __device__ constexpr bool is_fp4(int32_t dtype) {
+    return dtype == SA_MXFP4 || dtype == SA_NVFP4;
+}
+__host__ __device__ constexpr int32_t fp4_group(int32_t dtype) {
+    return dtype == SA_MXFP4 ? 32 : 16;
+}
+
 // E8M0 scale byte (OCP MX) -> its value 2^(b - 127), exactly; 255 is NaN.
 __device__ __forceinline__ float e8m0_to_float(uint32_t b) {
     if (b == 255u) return __int_as_float(0x7FC00000);
     return b == 0u ? __int_as_float(0x00400000) : __int_as_float(static_cast<int>(b << 23));
+}
+
+__device__ __forceinline__ float fp4_scale_value(int32_t dtype, uint32_t byte) {
+    return dtype == SA_MXFP4 ? e8m0_to_float(byte)
+                             : e4m3x2_to_float2(static_cast<uint16_t>(byte)).x;
 }
 
 // ---------------------------------------------------------------------------

@@ -50,7 +50,7 @@ struct PathParams {
     const float *kv_scale;
     int32_t d_latent, d_rope;
     int32_t kv_dtype;  // sa_dtype
-    int32_t kv_scale_tokens, kv_scale_dims;  // e4m3 scale tile (resolved, > 0)
+    int32_t kv_scale_tokens, kv_scale_dims;  // scale tile (resolved, > 0; 4 bits: 1 x group)
     // queries
     int32_t n_q;
     const int32_t *q_seq, *q_pos;
@@ -145,6 +145,18 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                            int32_t out_dtype, float *lse, float *o_part, float *lse_part,
                            cudaStream_t s);
 
+// Accumulated attention weights (weights.cu): the rows kernel compacts each
+// query's selection (rows, kept positions, n_valid; ascending[t] tells whether
+// the kept positions ascend), a weights kernel writes one weight per kept
+// entry (w, same layout), and the sum kernel adds them to the sequences' rows.
+// Leading dimension of rows, kept and w: weights_ld(K).
+int32_t weights_ld(int32_t top_k);
+cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, int32_t top_k,
+                                      const float *lse, const float *acc_in, float decay,
+                                      float *acc_out, int64_t ld_acc, int32_t *rows,
+                                      int32_t *kept, int32_t *n_valid, int32_t *ascending,
+                                      float *w, cudaStream_t s);
+
 // Context-parallel decode steps (cp.cu).
 int32_t cp_merge_max_candidates();
 int32_t cp_combine_max_parts();
@@ -187,14 +199,35 @@ __device__ __forceinline__ float kv_scale_at(const PathParams &p, int64_t row, i
                  d / p.kv_scale_dims);
 }
 
+// Latent dim or rope dim dd of physical row `row`, as fp32, from any cache format.
+__device__ __forceinline__ float kv_value(const PathParams &p, int64_t row, int dd) {
+    const int D = p.d_latent + p.d_rope;
+    if (p.kv_dtype == SA_F32) return static_cast<const float *>(p.kv)[row * D + dd];
+    if (p.kv_dtype == SA_BF16)
+        return bf16_bits_to_float(static_cast<const uint16_t *>(p.kv)[row * D + dd]);
+    if (dd >= p.d_latent)
+        return bf16_bits_to_float(
+            static_cast<const uint16_t *>(p.kv_rope)[row * p.d_rope + (dd - p.d_latent)]);
+    if (p.kv_dtype == SA_E4M3) {
+        const uint8_t c = static_cast<const uint8_t *>(p.kv)[row * p.d_latent + dd];
+        return e4m3x2_to_float2(c).x * kv_scale_at(p, row, dd);
+    }
+    const uint32_t two = static_cast<const uint8_t *>(p.kv)[(row * p.d_latent + dd) >> 1];
+    const uint32_t sb = reinterpret_cast<const uint8_t *>(
+        p.kv_scale)[(row * p.d_latent + dd) / p.kv_scale_dims];
+    return e2m1x2_to_float2((dd & 1) ? two >> 4 : two & 15u).x * fp4_scale_value(p.kv_dtype, sb);
+}
+
 // Physical cache rows of query t's selected positions sel[0, K): list order,
 // -1 entries dropped, out-of-range positions and bad page ids skipped and
 // reported; then padded with the first row up to a multiple of `tile`.
-// Writes rows[0, padded) and *n_valid.  Called by every thread of a CTA
-// (blockDim.x a multiple of 32); `scratch` is shared memory of 33 ints.
+// Writes rows[0, padded) and *n_valid, and with `kept` the positions behind
+// rows[0, *n_valid).  Called by every thread of a CTA (blockDim.x a multiple
+// of 32); `scratch` is shared memory of 33 ints.
 __device__ __forceinline__ void compact_rows(const PathParams &p, int32_t t, const int32_t *sel,
                                              int32_t K, int32_t tile, int32_t *rows,
-                                             int32_t *n_valid, int32_t *scratch) {
+                                             int32_t *n_valid, int32_t *scratch,
+                                             int32_t *kept = nullptr) {
     const int nwarps = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t V = visible_len(p, t);
     const int32_t seq = __ldg(p.q_seq + t);
@@ -221,6 +254,7 @@ __device__ __forceinline__ void compact_rows(const PathParams &p, int32_t t, con
         const int32_t pos = off + __popc(bal & ((1u << lane) - 1u));
         if (v >= 0) {
             rows[pos] = v;
+            if (kept != nullptr) kept[pos] = s;
             if (pos == 0) scratch[32] = v;
         }
         __syncthreads();

@@ -9,8 +9,12 @@
 // so the largest magnitude of a group lands on e4m3's largest finite value.
 // The division is IEEE round-to-nearest (__fdiv_rn): the codes depend on it.
 //
-// Both kernels are memory-bound: one warp per quantised row of the query
-// (d_index values), one CTA per appended token.
+// A 4-bit latent takes, per group of 32 (MXFP4) or 16 values (NVFP4), a scale
+// byte that puts the largest magnitude near e2m1's 6: 2^(floor(log2 amax) - 2),
+// or e4m3(amax / 6); code = e2m1(x / scale), nearest even, saturated to +-6.
+//
+// The kernels are memory-bound: one warp per quantised row of the query
+// (d_index values), one CTA per appended or read token.
 #include "common.cuh"
 #include "internal.h"
 #include "prep.h"
@@ -147,6 +151,47 @@ __device__ void quantize_groups(const void *src, int64_t s0, bool bf16, int32_t 
     __syncthreads();  // gmax is reused by the next call
 }
 
+// amax of a group -> its scale byte of a 4-bit latent and that byte's value.
+__device__ __forceinline__ uint32_t fp4_scale_byte(int32_t dtype, float amax) {
+    if (dtype == SA_MXFP4) {
+        if (!(amax > 0.0f)) return 127u;
+        // floor(log2 amax): the exponent field of a normal number; of a subnormal
+        // one the scale is clamped to 2^-127 either way
+        const int e = static_cast<int>((__float_as_uint(amax) >> 23) & 255u) - 2;
+        return static_cast<uint32_t>(max(e, 0));
+    }
+    const float s = amax > 0.0f ? fminf(__fdiv_rn(amax, 6.0f), kE4m3Max) : 1.0f;
+    return static_cast<uint32_t>(__nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3));
+}
+
+// Two values of a group -> one byte of two codes.
+__device__ __forceinline__ uint32_t to_e2m1x2(float a, float b, float scale) {
+    if (!(scale > 0.0f)) return 0u;  // an e4m3 scale that rounded to 0
+    return __nv_cvt_float2_to_fp4x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)),
+                                    __NV_E2M1, cudaRoundNearest);
+}
+
+// n values starting at element s0 of src -> two codes a byte at dst[0..n/2)
+// and one scale byte per group of g values.  Every thread of the CTA calls it.
+__device__ void quantize_fp4(const void *src, int64_t s0, bool bf16, int32_t n, int32_t dtype,
+                             uint8_t *dst, uint8_t *scl, int32_t *gmax) {
+    const int32_t g = fp4_group(dtype), groups = n / g;
+    for (int32_t i = threadIdx.x; i < groups; i += blockDim.x) gmax[i] = 0;
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < n; i += blockDim.x)
+        atomicMax(&gmax[i / g], __float_as_int(fabsf(load_value(src, s0 + i, bf16))));
+    __syncthreads();
+    for (int32_t i = threadIdx.x; i < n / 2; i += blockDim.x) {
+        const uint32_t byte = fp4_scale_byte(dtype, __int_as_float(gmax[2 * i / g]));
+        dst[i] = static_cast<uint8_t>(to_e2m1x2(load_value(src, s0 + 2 * i, bf16),
+                                                load_value(src, s0 + 2 * i + 1, bf16),
+                                                fp4_scale_value(dtype, byte)));
+    }
+    for (int32_t i = threadIdx.x; i < groups; i += blockDim.x)
+        scl[i] = static_cast<uint8_t>(fp4_scale_byte(dtype, __int_as_float(gmax[i])));
+    __syncthreads();  // gmax is reused by the next call
+}
+
 __device__ __forceinline__ uint16_t to_bf16_bits(const void *src, int64_t i, bool bf16) {
     if (bf16) return static_cast<const uint16_t *>(src)[i];
     return __bfloat16_as_ushort(__float2bfloat16_rn(static_cast<const float *>(src)[i]));
@@ -193,6 +238,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
                 uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
                 for (int32_t i = threadIdx.x; i < p.d_rope; i += blockDim.x)
                     rope[i] = to_bf16_bits(p.kv_new, s0 + p.d_latent + i, bf16);
+            } else if (is_fp4(p.kv_dtype)) {
+                const int32_t groups = p.d_latent / p.kv_scale_dims;
+                quantize_fp4(p.kv_new, s0, bf16, p.d_latent, p.kv_dtype,
+                             static_cast<uint8_t *>(p.kv) + row * (p.d_latent / 2),
+                             reinterpret_cast<uint8_t *>(p.kv_scale) + row * groups, gmax);
+                uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
+                for (int32_t i = threadIdx.x; i < p.d_rope; i += blockDim.x)
+                    rope[i] = to_bf16_bits(p.kv_new, s0 + p.d_latent + i, bf16);
             } else if (p.kv_dtype == SA_BF16) {
                 uint16_t *dst = static_cast<uint16_t *>(p.kv) + row * D;
                 for (int32_t i = threadIdx.x; i < D; i += blockDim.x)
@@ -206,7 +259,41 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
 }
 
+// Rows back out of the latent pool: one CTA per token (grid-stride).
+__global__ void __launch_bounds__(kAppendThreads)
+read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
+            const int32_t *__restrict__ pos_of, void *out, int32_t out_dtype) {
+    const int32_t D = p.d_latent + p.d_rope;
+    for (int32_t t = blockIdx.x; t < n; t += gridDim.x) {
+        const int32_t seq = __ldg(seq_of + t), pos = __ldg(pos_of + t);
+        int64_t row = -1;
+        if (seq < 0 || seq >= p.batch || pos < 0 || (pos >> 6) >= p.max_pages) {
+            if (threadIdx.x == 0) report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
+        } else {
+            row = phys_row(p.page_table, p.max_pages, p.num_pages, seq, pos);
+            if (row < 0 && threadIdx.x == 0)
+                report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+        }
+        for (int32_t i = threadIdx.x; i < D; i += blockDim.x) {
+            const float v = row >= 0 ? kv_value(p, row, i) : 0.0f;
+            if (out_dtype == SA_BF16)
+                static_cast<__nv_bfloat16 *>(out)[(int64_t)t * D + i] = __float2bfloat16_rn(v);
+            else
+                static_cast<float *>(out)[(int64_t)t * D + i] = v;
+        }
+    }
+}
+
 }  // namespace
+
+cudaError_t launch_read(const PathParams &p, int32_t n, const int32_t *seq, const int32_t *pos,
+                        void *out, int32_t out_dtype, cudaStream_t s) {
+    if (n <= 0) return cudaSuccess;
+    const int grid = std::min(n, num_sms() * 16);
+    count_launch();
+    read_kernel<<<grid, kAppendThreads, 0, s>>>(p, n, seq, pos, out, out_dtype);
+    return cudaGetLastError();
+}
 
 cudaError_t launch_quantize_rows(const void *in, sa_dtype in_dtype, int64_t n_rows, int32_t d,
                                  uint8_t *codes, float *scales, cudaStream_t s) {

@@ -1,11 +1,12 @@
 // prep.h -- launchers of the input-preparation kernels (prep.cu): FP8
-// quantisation of the indexer query and the append of new tokens to the paged
-// caches.  Not part of the public ABI.
+// quantisation of the indexer query, the append of new tokens to the paged
+// caches and the reading back of latent rows.  Not part of the public ABI.
 #pragma once
 
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "internal.h"
 #include "sa.h"
 
 namespace sa {
@@ -36,11 +37,16 @@ struct AppendParams {
     float *kv_scale;
     int32_t d_latent, d_rope;
     int32_t kv_dtype;  // sa_dtype
-    int32_t kv_scale_dims;  // e4m3: latent dims per scale (one token per scale)
+    int32_t kv_scale_dims;  // e4m3, 4 bits: latent dims per scale (one token per scale)
     // status word
     int32_t *status;
 };
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
+
+// Latent + rope rows of tokens (seq[i], pos[i]) of the cache in `p` (its query
+// fields are unused) -> out [n, d_latent + d_rope], bf16 or fp32.
+cudaError_t launch_read(const PathParams &p, int32_t n, const int32_t *seq, const int32_t *pos,
+                        void *out, int32_t out_dtype, cudaStream_t s);
 
 }  // namespace sa

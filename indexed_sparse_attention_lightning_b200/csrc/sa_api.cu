@@ -8,6 +8,7 @@
 #include <cstring>
 
 #include "common.cuh"
+#include "evict.h"
 #include "internal.h"
 #include "prep.h"
 #include "sa.h"
@@ -45,7 +46,8 @@ sa_status check_cache(const sa_cache *c) {
     if (c->d_index <= 0 || c->d_index % 16 != 0) return SA_ERR_INVALID_ARG;
     if (c->index_dtype == SA_MXFP8 && c->d_index % 32 != 0) return SA_ERR_INVALID_ARG;
     if (c->d_index > 256) return SA_ERR_UNSUPPORTED;
-    if (c->kv_dtype != SA_F32 && c->kv_dtype != SA_BF16 && c->kv_dtype != SA_E4M3)
+    if (c->kv_dtype != SA_F32 && c->kv_dtype != SA_BF16 && c->kv_dtype != SA_E4M3 &&
+        !is_fp4(c->kv_dtype))
         return SA_ERR_UNSUPPORTED;  // SA_MXFP8 names index data only
     if (c->d_latent <= 0 || c->d_rope < 0) return SA_ERR_INVALID_ARG;
     if (c->d_latent > 512 || c->d_latent + c->d_rope > 1024) return SA_ERR_UNSUPPORTED;
@@ -60,7 +62,26 @@ sa_status check_cache(const sa_cache *c) {
                 return SA_ERR_UNSUPPORTED;
         }
     }
+    if (is_fp4(c->kv_dtype)) {
+        if (!c->kv_scale || (c->d_rope > 0 && !c->kv_rope)) return SA_ERR_INVALID_ARG;
+        if (!aligned16(c->kv_scale) || (c->kv_rope && !aligned16(c->kv_rope)))
+            return SA_ERR_INVALID_ARG;
+        if (c->kv_scale_tokens != 0 || c->kv_scale_dims != 0) return SA_ERR_INVALID_ARG;
+        // whole groups, and rows of codes and rope that are whole 16-byte pieces
+        if (c->d_latent % 32 != 0 || c->d_rope % 8 != 0) return SA_ERR_INVALID_ARG;
+    }
     return SA_OK;
+}
+
+// Cache scale tile as the kernels use it (0, 0 resolved; 4 bits: the format's group).
+void resolve_scale_tile(const sa_cache *c, int32_t *tokens, int32_t *dims) {
+    const bool page_tile = c->kv_scale_tokens == 0 && c->kv_scale_dims == 0;
+    *tokens = page_tile ? c->page_size : c->kv_scale_tokens;
+    *dims = page_tile ? c->d_latent : c->kv_scale_dims;
+    if (is_fp4(c->kv_dtype)) {
+        *tokens = 1;
+        *dims = fp4_group(c->kv_dtype);
+    }
 }
 
 sa_status check_query(const sa_query *q, const sa_cache *c, bool need_index, bool need_attn) {
@@ -86,7 +107,7 @@ sa_status check_query(const sa_query *q, const sa_cache *c, bool need_index, boo
     return SA_OK;
 }
 
-PathParams make_params(const sa_cache *c, const sa_query *q, void *ws) {
+PathParams cache_params(const sa_cache *c, void *ws) {
     PathParams p{};
     p.page_table = c->page_table;
     p.seq_len = c->seq_len;
@@ -103,9 +124,13 @@ PathParams make_params(const sa_cache *c, const sa_query *q, void *ws) {
     p.d_latent = c->d_latent;
     p.d_rope = c->d_rope;
     p.kv_dtype = c->kv_dtype;
-    const bool page_tile = c->kv_scale_tokens == 0 && c->kv_scale_dims == 0;
-    p.kv_scale_tokens = page_tile ? c->page_size : c->kv_scale_tokens;
-    p.kv_scale_dims = page_tile ? c->d_latent : c->kv_scale_dims;
+    resolve_scale_tile(c, &p.kv_scale_tokens, &p.kv_scale_dims);
+    p.status = static_cast<int32_t *>(ws);
+    return p;
+}
+
+PathParams make_params(const sa_cache *c, const sa_query *q, void *ws) {
+    PathParams p = cache_params(c, ws);
     p.n_q = q->n_q;
     p.q_seq = q->q_seq;
     p.q_pos = q->q_pos;
@@ -119,7 +144,6 @@ PathParams make_params(const sa_cache *c, const sa_query *q, void *ws) {
     p.heads = q->heads;
     p.sm_scale = q->sm_scale;
     p.q_group = q->q_group;
-    p.status = static_cast<int32_t *>(ws);
     return p;
 }
 
@@ -136,6 +160,9 @@ struct Layout {
         lse_part;
     size_t indexer_total, decode_total;
     size_t attn_rows, attn_n_valid, attn_o_part, attn_lse_part, attn_total;
+    // accumulated weights: status | rows | kept | w [n_q, weights_ld] each |
+    // n_valid [n_q] | ascending [n_q]
+    size_t wt_rows, wt_kept, wt_w, wt_n_valid, wt_ascending, wt_total;
 };
 
 size_t part_bytes(size_t nq, int32_t splits, size_t per) {
@@ -171,7 +198,34 @@ Layout make_layout(const sa_query *q, int32_t top_k) {
     l.attn_o_part = align_up(l.attn_n_valid + sizeof(int32_t) * nq);
     l.attn_lse_part = align_up(l.attn_o_part + o_bytes);
     l.attn_total = align_up(l.attn_lse_part + lse_bytes);
+    const size_t wt_bytes = 4 * nq * (size_t)weights_ld(top_k);
+    l.wt_rows = align_up(kStatusBytes);
+    l.wt_kept = align_up(l.wt_rows + wt_bytes);
+    l.wt_w = align_up(l.wt_kept + wt_bytes);
+    l.wt_n_valid = align_up(l.wt_w + wt_bytes);
+    l.wt_ascending = align_up(l.wt_n_valid + sizeof(int32_t) * nq);
+    l.wt_total = align_up(l.wt_ascending + sizeof(int32_t) * nq);
     return l;
+}
+
+// sa_evict_tokens: status | physical source rows [batch, budget] | kept [batch]
+size_t evict_workspace(const sa_cache *c, int32_t budget) {
+    if (budget <= 0) return 0;
+    return align_up(evict_kept_offset(c->batch, budget) + sizeof(int32_t) * (size_t)c->batch);
+}
+
+// Physical rows and positions that fit 32 bits (with room for a block's step).
+bool rows_fit_32(const sa_cache *c) {
+    constexpr int64_t kLimit = (int64_t(1) << 31) - 8192;
+    return (int64_t)c->num_pages * kPageSize < kLimit && (int64_t)c->max_pages * kPageSize < kLimit;
+}
+
+// Whether two caches hold rows of the same formats and sizes.
+bool same_format(const sa_cache *a, const sa_cache *b) {
+    return a->batch == b->batch && a->index_dtype == b->index_dtype &&
+           a->d_index == b->d_index && a->kv_dtype == b->kv_dtype &&
+           a->d_latent == b->d_latent && a->d_rope == b->d_rope &&
+           a->kv_scale_tokens == b->kv_scale_tokens && a->kv_scale_dims == b->kv_scale_dims;
 }
 
 // Sparse attention: the tensor-core kernel for its shape, CUDA cores otherwise.
@@ -240,16 +294,20 @@ size_t sa_workspace_size(const sa_cache *cache, const sa_query *query, int32_t t
                          int32_t uses) {
     if (check_cache(cache) != SA_OK) return 0;
     if (uses == SA_WS_APPEND) return align_up(kStatusBytes);
+    if (uses == SA_WS_EVICT) return evict_workspace(cache, top_k);
     const bool idx = (uses & (SA_WS_INDEXER | SA_WS_DECODE)) != 0;
-    const bool att = (uses & (SA_WS_ATTN | SA_WS_DECODE)) != 0;
+    const bool att = (uses & (SA_WS_ATTN | SA_WS_DECODE | SA_WS_WEIGHTS)) != 0;
     if (check_query(query, cache, idx, att) != SA_OK) return 0;
-    if ((uses & (SA_WS_TOPK | SA_WS_DECODE | SA_WS_ATTN)) && (top_k <= 0 || top_k > kMaxTopK))
+    if ((uses & (SA_WS_TOPK | SA_WS_DECODE | SA_WS_ATTN | SA_WS_WEIGHTS)) &&
+        (top_k <= 0 || top_k > kMaxTopK))
         return 0;
     const Layout l = make_layout(query, top_k);
     size_t need = kStatusBytes;
     if (uses & SA_WS_INDEXER) need = std::max(need, l.indexer_total);
     if (uses & SA_WS_ATTN) need = std::max(need, l.attn_total);
     if (uses & SA_WS_DECODE) need = std::max(need, l.decode_total);
+    if (uses & SA_WS_WEIGHTS) need = std::max(need, l.wt_total);
+    if (uses & SA_WS_EVICT) need = std::max(need, evict_workspace(cache, top_k));
     return align_up(need);
 }
 
@@ -479,9 +537,74 @@ sa_status sa_append_tokens(const sa_cache *cache, const sa_new_tokens *tokens, v
     p.d_latent = cache->d_latent;
     p.d_rope = cache->d_rope;
     p.kv_dtype = cache->kv_dtype;
-    p.kv_scale_dims = page_tile ? cache->d_latent : cache->kv_scale_dims;
+    int32_t scale_tokens;
+    resolve_scale_tile(cache, &scale_tokens, &p.kv_scale_dims);
     p.status = static_cast<int32_t *>(workspace);
     return cuda_status(launch_append(p, s));
+}
+
+sa_status sa_read_tokens(const sa_cache *cache, int32_t n, const int32_t *seq, const int32_t *pos,
+                         void *out, sa_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                         void *stream) {
+    sa_status st = check_cache(cache);
+    if (st != SA_OK) return st;
+    if (n < 0) return SA_ERR_INVALID_ARG;
+    if (out_dtype != SA_BF16 && out_dtype != SA_F32) return SA_ERR_UNSUPPORTED;
+    if (n > 0 && (!seq || !pos || !out || !aligned16(out))) return SA_ERR_INVALID_ARG;
+    if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes)) != SA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = clear_status(workspace, s)) != SA_OK) return st;
+    return cuda_status(launch_read(cache_params(cache, workspace), n, seq, pos, out, out_dtype, s));
+}
+
+sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *query, const int32_t *idx,
+                                int32_t top_k, const float *lse, const float *acc_in, float decay,
+                                float *acc_out, int64_t ld_acc, void *workspace,
+                                size_t workspace_bytes, void *stream) {
+    sa_status st = check_cache(cache);
+    if (st != SA_OK) return st;
+    if ((st = check_query(query, cache, false, true)) != SA_OK) return st;
+    if (top_k <= 0 || top_k > kMaxTopK || !std::isfinite(decay)) return SA_ERR_INVALID_ARG;
+    if (query->n_q > 0 && (!idx || !lse)) return SA_ERR_INVALID_ARG;
+    if (!acc_out || ld_acc <= 0 || (query->n_q > 0 && ld_acc < query->max_visible))
+        return SA_ERR_INVALID_ARG;
+    if (!rows_fit_32(cache) || (int64_t)cache->batch * cache->max_pages >= (int64_t(1) << 31))
+        return SA_ERR_UNSUPPORTED;
+    const Layout l = make_layout(query, top_k);
+    if ((st = check_workspace(workspace, workspace_bytes, l.wt_total)) != SA_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = clear_status(workspace, s)) != SA_OK) return st;
+    char *base = static_cast<char *>(workspace);
+    return cuda_status(launch_accumulate_weights(
+        make_params(cache, query, workspace), idx, top_k, lse, acc_in, decay, acc_out, ld_acc,
+        reinterpret_cast<int32_t *>(base + l.wt_rows),
+        reinterpret_cast<int32_t *>(base + l.wt_kept),
+        reinterpret_cast<int32_t *>(base + l.wt_n_valid),
+        reinterpret_cast<int32_t *>(base + l.wt_ascending),
+        reinterpret_cast<float *>(base + l.wt_w), s));
+}
+
+sa_status sa_evict_tokens(const sa_cache *src, const float *acc, int64_t ld_acc, int32_t budget,
+                          int32_t keep_first, int32_t keep_last, const sa_cache *dst,
+                          float *acc_out, int64_t ld_out, int32_t *src_pos, void *workspace,
+                          size_t workspace_bytes, void *stream) {
+    sa_status st = check_cache(src);
+    if (st != SA_OK) return st;
+    if ((st = check_cache(dst)) != SA_OK) return st;
+    if (!same_format(src, dst)) return SA_ERR_INVALID_ARG;
+    if (src->kv_dtype == SA_E4M3 && src->kv_scale_tokens != 1) return SA_ERR_UNSUPPORTED;
+    if (!acc || ld_acc <= 0 || budget <= 0 || keep_first < 0 || keep_last < 0 ||
+        (int64_t)keep_first + keep_last > budget ||
+        (int64_t)dst->max_pages * dst->page_size < budget || src->seq_len == dst->seq_len)
+        return SA_ERR_INVALID_ARG;
+    if (acc_out && (acc_out == acc || ld_out < budget)) return SA_ERR_INVALID_ARG;
+    if (!rows_fit_32(src) || !rows_fit_32(dst)) return SA_ERR_UNSUPPORTED;
+    if ((st = check_workspace(workspace, workspace_bytes, evict_workspace(src, budget))) != SA_OK)
+        return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if ((st = clear_status(workspace, s)) != SA_OK) return st;
+    return cuda_status(launch_evict(src, acc, ld_acc, budget, keep_first, keep_last, dst, acc_out,
+                                    ld_out, src_pos, workspace, s));
 }
 
 sa_status sa_device_status(const void *workspace, size_t workspace_bytes, void *stream,

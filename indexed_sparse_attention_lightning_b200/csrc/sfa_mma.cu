@@ -34,7 +34,8 @@
 //              written -- and commits them to mbarriers;
 //   warps 1-7  copy the selected rows (16-byte cp.async, the swizzle applied
 //              in the addresses) into a 3-stage ring freed by each tile's P V;
-//              random 1152-byte rows reach shared memory fastest this way;
+//              random 1152-byte rows reach shared memory fastest this way (an
+//              e4m3 or 4-bit latent is loaded, decoded to bf16 and stored);
 //   warps 8-11 move Q into TMEM, then run the online softmax.  Warp 8 + j
 //              owns heads 16j .. 16j + 15 and reads their S rows with 16-lane
 //              loads: thread i holds heads 16j + i/4 and 16j + i/4 + 8, keys
@@ -109,7 +110,6 @@ struct SfaArgs {
     const int32_t *n_valid;  // [n_q]
     int32_t ld_rows;
     int32_t splits;
-    int32_t fp8;             // e4m3 latent + fp32 page scale + bf16 rope (else bf16 rows)
     void *out;               // [n_q, 128, 512] (splits == 1)
     int32_t out_dtype;
     float *lse;              // [n_q, 128] or null (splits == 1)
@@ -159,6 +159,7 @@ sfa_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, 
                  n_valid_out + t, scratch);
 }
 
+template <int kKv>  // sa_dtype of the latent cache
 __global__ void __launch_bounds__(kThreads, 1)
 sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     extern __shared__ uint8_t smem_raw[];
@@ -441,11 +442,12 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         const int32_t *tile_rows = rows + (int64_t)j0 * kTile;
         const uint8_t *rope = static_cast<const uint8_t *>(p.kv_rope);
         auto prefetch_row = [&](int32_t r) {
-            if (a.fp8) {
-                prefetch_l2(kv + (int64_t)r * kDl, kDl);
-                prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
-            } else {
+            if constexpr (kKv == SA_BF16) {
                 prefetch_l2(kv + (int64_t)r * (kD * 2), kD * 2);
+            } else {
+                constexpr int kRowBytes = is_fp4(kKv) ? kDl / 2 : kDl;
+                prefetch_l2(kv + (int64_t)r * kRowBytes, kRowBytes);
+                prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
             }
         };
         if (prefetcher) {
@@ -471,7 +473,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             const int32_t hi_next = more ? __ldg(tile_rows + (n + 1) * kTile + 32 + lane) : 0;
             if (!warp_wait(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1, abort_flag, status)) break;
             if (n == 2 && !warp_wait(&sm.q_ready, 0, abort_flag, status)) break;
-            if (!a.fp8) {
+            if constexpr (kKv == SA_BF16) {
                 const uint32_t dst0 = smem_u32(sm.kv[st]);
 #pragma unroll 1  // measured faster than unrolling by 2 or 4 (32K decode: 0.087 against 0.095 ms)
                 for (int k = pw; k < kTile; k += kProducerWarps) {
@@ -487,6 +489,43 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                     }
                 }
                 cp_async_arrive(&sm.kv_full[st]);
+            } else if constexpr (is_fp4(kKv)) {
+                // 4-bit latent: lane c decodes dims 16c .. 16c + 15 of a row and
+                // applies its group's scale (e2m1 x E8M0 or e4m3 has at most 6
+                // significant bits, so bf16 holds the product exactly)
+                constexpr int kGroup = fp4_group(kKv);
+                const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale);
+                uint8_t *stage = sm.kv[st];
+#pragma unroll 2
+                for (int k = pw; k < kTile; k += kProducerWarps) {
+                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? r_lo : r_hi, k & 31);
+                    const uint2 x =
+                        __ldg(reinterpret_cast<const uint2 *>(kv + (int64_t)r * (kDl / 2)) + lane);
+                    const uint32_t sb =
+                        __ldg(scales + (int64_t)r * (kDl / kGroup) + lane * 16 / kGroup);
+                    uint4 rp = make_uint4(0, 0, 0, 0);
+                    if (lane < 8)
+                        rp = __ldg(reinterpret_cast<const uint4 *>(rope + (int64_t)r * (kDr * 2)) + lane);
+                    const float sc = fp4_scale_value(kKv, sb);
+                    const uint32_t xw[2] = {x.x, x.y};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float2 f = e2m1x2_to_float2((xw[i >> 2] >> (8 * (i & 3))) & 255u);
+                        __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+                        o[i] = *reinterpret_cast<uint32_t *>(&b2);
+                    }
+                    uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
+                    const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
+                    *reinterpret_cast<uint4 *>(dk + b * 1024 + ((c0 ^ sw) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(dk + b * 1024 + (((c0 + 1) ^ sw) << 4)) =
+                        make_uint4(o[4], o[5], o[6], o[7]);
+                    if (lane < 8)
+                        *reinterpret_cast<uint4 *>(dk + 8 * 1024 + ((lane ^ sw) << 4)) = rp;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&sm.kv_full[st]);
             } else {
                 // e4m3 latent: lane c dequantises dims 16c .. 16c + 15 of a row
                 // (x its page's scale, rounded to bf16) into the same swizzled
@@ -667,7 +706,8 @@ sfa_combine_kernel(const float *__restrict__ o_part, const float *__restrict__ l
 
 bool sfa_mma_supported(const PathParams &p, int32_t top_k) {
     const bool kv_ok = p.kv_dtype == SA_BF16 ||
-                       (p.kv_dtype == SA_E4M3 && p.kv_rope != nullptr && p.kv_scale != nullptr);
+                       ((p.kv_dtype == SA_E4M3 || is_fp4(p.kv_dtype)) && p.kv_rope != nullptr &&
+                        p.kv_scale != nullptr);
     return kv_ok && p.q_dtype == SA_BF16 && p.heads == 128 &&
            p.d_latent == kDl && p.d_rope == kDr && top_k <= kMaxK &&
            (int64_t)p.num_pages * 64 < (int64_t(1) << 31);
@@ -698,16 +738,17 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
     CUtensorMap tq;
     if (!encode_tmap_2d(&tq, 2, p.q, kD, (uint64_t)p.n_q * 128, kD * 2, 64, kHeadsCta, true))
         return cudaErrorInvalidValue;
-    SfaArgs a{p,         rows,   n_valid,  ld_rows,  splits, p.kv_dtype == SA_E4M3,
-              out,       out_dtype, lse,    o_part,   lse_part};
+    SfaArgs a{p, rows, n_valid, ld_rows, splits, out, out_dtype, lse, o_part, lse_part};
     const size_t smem = sizeof(SfaSmem) + 1024;
-    e = cudaFuncSetAttribute(sfa_mma_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+    const auto kernel = p.kv_dtype == SA_BF16    ? sfa_mma_kernel<SA_BF16>
+                        : p.kv_dtype == SA_E4M3  ? sfa_mma_kernel<SA_E4M3>
+                        : p.kv_dtype == SA_MXFP4 ? sfa_mma_kernel<SA_MXFP4>
+                                                 : sfa_mma_kernel<SA_NVFP4>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int64_t grid = 2 * (int64_t)p.n_q * splits;
     count_launch();
-    e = launch_pdl(sfa_mma_kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, tq,
-                   a);
+    e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, tq, a);
     if (e != cudaSuccess || splits == 1) return e;
     count_launch();
     return launch_pdl(sfa_combine_kernel, dim3(static_cast<unsigned>(p.n_q * 128)), dim3(128), 0,

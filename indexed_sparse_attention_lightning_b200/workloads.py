@@ -20,7 +20,10 @@ indexer and the sparse attention kernel -- "Optimizing Next-Gen LLM Inference"
 * MLA latent rows ``kv[P, 64, d_latent + d_rope]`` (fp32 or bf16), or for the
   FP8 cache ``kv[P, 64, d_latent]`` e4m3 codes, ``kv_scale[P, 64 / ts, d_latent / td]``
   (one fp32 scale per tile of ts tokens x td latent dims of a page; the default
-  (64, d_latent) is one per page) and ``kv_rope[P, 64, d_rope]`` bf16.
+  (64, d_latent) is one per page) and ``kv_rope[P, 64, d_rope]`` bf16; for the
+  4-bit caches ("mxfp4", "nvfp4") ``kv[P, 64, d_latent / 2]`` bytes of two e2m1
+  codes (dim 2i in the low half of byte i), ``kv_scale[P, 64, d_latent / g]``
+  uint8 (g = 32: E8M0 bytes, or 16: e4m3 bytes) and the same rope.
 
 Slots past a sequence's end and pages no sequence owns are filled with NaN, so
 that any read outside the visible range shows up as NaN in a result.
@@ -32,6 +35,10 @@ MXFP8 (OCP MX rule, power-of-two scales): per group of 32 values
 value), stored as the E8M0 byte ``127 + floor(log2 amax) - 8``; codes as above
 (values that land in [448, 512) of the scale saturate to 448); an all-zero
 group stores byte 127 (scale 1).
+4-bit latent: MXFP4 takes the same rule with e2m1's largest exponent 2; NVFP4
+takes ``scale = e4m3(min(amax / 6, 448))`` per 16 values (1 when amax is 0);
+codes are the nearest e2m1 value of x / scale, ties to the even code, saturated
+to +-6.
 """
 from __future__ import annotations
 
@@ -71,7 +78,7 @@ class WorkloadSpec:
     heads: int = 128
     d_latent: int = 512
     d_rope: int = 64
-    kv_dtype: str = "bf16"         # "f32", "bf16" or "e4m3"
+    kv_dtype: str = "bf16"         # "f32", "bf16", "e4m3", "mxfp4" or "nvfp4"
     q_dtype: str = "bf16"          # "f32" or "bf16"
     page_size: int = 64
     paging: str = "permuted"       # "identity" or "permuted"
@@ -146,8 +153,13 @@ DECODE_B64_MXFP8_INDEX = WorkloadSpec(
     name="decode_b64_16k_32k_mxfp8_index", seed=2, batch=64, seq_len=("uniform", 16384, 32768),
     keys=("planted", 0.05, 3.0), index_dtype="mxfp8")
 
+# the headline decode over a latent cache held in 4 bits
+DECODE_B64_MXFP4_KV = WorkloadSpec(
+    name="decode_b64_16k_32k_mxfp4_kv", seed=2, batch=64, seq_len=("uniform", 16384, 32768),
+    keys=("planted", 0.05, 3.0), kv_dtype="mxfp4")
+
 EXTRA = (PROFILE_B64_16K, DECODE_B64_BF16_INDEX, DECODE_B2_1M_FP8KV_TILE_1X128,
-         DECODE_B64_MXFP8_INDEX)
+         DECODE_B64_MXFP8_INDEX, DECODE_B64_MXFP4_KV)
 
 
 def spec(which) -> WorkloadSpec:
@@ -178,9 +190,11 @@ class Workload:
     q_index: np.ndarray          # f32, uint16 (bf16) or uint8 (e4m3) [n_q, h_index, d_index]
     q_index_scale: Optional[np.ndarray]  # f32 [n_q, h_index] (or [n_q, h_index, d_index / group])
     w: np.ndarray                # f32 [n_q, h_index]
-    kv: np.ndarray               # f32/uint16(bf16) [P, ps, d_qk] or uint8 [P, ps, d_latent]
-    kv_rope: Optional[np.ndarray]  # uint16 (bf16) [P, ps, d_rope] for the e4m3 cache
-    kv_scale: Optional[np.ndarray]  # f32 [P, 64 / tile tokens, d_latent / tile dims] (e4m3)
+    # f32/uint16(bf16) [P, ps, d_qk], uint8 [P, ps, d_latent], or [P, ps, d_latent / 2] (4 bits)
+    kv: np.ndarray
+    kv_rope: Optional[np.ndarray]  # uint16 (bf16) [P, ps, d_rope] for the e4m3 and 4-bit caches
+    # f32 [P, 64 / tile tokens, d_latent / tile dims] (e4m3), uint8 [P, 64, d_latent / group] (4 bits)
+    kv_scale: Optional[np.ndarray]
     q: np.ndarray                # f32 or uint16 (bf16) [n_q, heads, d_qk]
     planted: dict = field(default_factory=dict)  # seq -> sorted planted positions
     clusters: dict = field(default_factory=dict)  # seq -> list of (start, len)
@@ -256,11 +270,56 @@ def quantize_mxfp8(x: np.ndarray):
     return codes.reshape(x.shape), byte
 
 
+FP4_GROUP = {"mxfp4": 32, "nvfp4": 16}
+
+
+def to_e2m1_codes(x: np.ndarray) -> np.ndarray:
+    """fp32 -> 4-bit codes: nearest e2m1 value (0, .5, 1, 1.5, 2, 3, 4, 6), ties to
+    the even code, saturated to +-6."""
+    a = np.abs(np.asarray(x, dtype=np.float32))
+    c = ((a > 0.25).astype(np.uint8) + (a >= 0.75) + (a > 1.25) + (a >= 1.75) + (a > 2.5)
+         + (a >= 3.5) + (a > 5.0))
+    return (c + 8 * np.signbit(x)).astype(np.uint8)
+
+
+def quantize_fp4(x: np.ndarray, kv_dtype: str):
+    """Rows of the last axis -> (bytes of two codes, scale bytes) of a 4-bit latent."""
+    grp = FP4_GROUP[kv_dtype]
+    g = x.reshape(x.shape[:-1] + (x.shape[-1] // grp, grp)).astype(np.float32)
+    amax = np.abs(g).max(axis=-1)
+    if kv_dtype == "mxfp4":
+        _, ex = np.frexp(amax)
+        byte = np.where(amax > 0, np.clip(ex.astype(np.int64) - 1 - 2 + 127, 0, 254), 127)
+        byte = byte.astype(np.uint8)
+        scale = np.ldexp(np.float32(1.0), byte.astype(np.int64) - 127).astype(np.float32)
+    else:
+        s = np.where(amax > 0, amax / np.float32(6.0), np.float32(1.0)).astype(np.float32)
+        byte = to_e4m3_codes(s)
+        scale = torch.from_numpy(byte).view(torch.float8_e4m3fn).float().numpy()
+    s = scale[..., None]
+    codes = to_e2m1_codes(np.where(s > 0, g / np.where(s > 0, s, np.float32(1.0)),
+                                   np.float32(0.0))).reshape(x.shape)
+    return codes[..., ::2] + 16 * codes[..., 1::2], byte
+
+
 def e8m0_value(byte: np.ndarray) -> np.ndarray:
     """E8M0 bytes -> their fp32 values 2^(b - 127) (255 -> NaN); storage decode only."""
     b = np.asarray(byte).astype(np.int64)
     v = np.ldexp(np.float64(1.0), b - 127)
     return np.where(b == 255, np.nan, v).astype(np.float32)
+
+
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0], dtype=np.float32)
+
+
+def fp4_value(codes: np.ndarray, scale_bytes: np.ndarray, kv_dtype: str) -> np.ndarray:
+    """Bytes of two codes and scale bytes -> fp32 values; storage decode only."""
+    two = np.stack([codes & 15, codes >> 4], axis=-1).reshape(codes.shape[:-1] + (-1,))
+    v = E2M1_VALUES[two & 7] * np.where(two & 8, np.float32(-1), np.float32(1))
+    sc = (e8m0_value(scale_bytes) if kv_dtype == "mxfp4" else
+          torch.from_numpy(np.ascontiguousarray(scale_bytes)).view(torch.float8_e4m3fn)
+          .float().numpy())
+    return v * np.repeat(sc, FP4_GROUP[kv_dtype], axis=-1)
 
 
 def _quantize_index(x: np.ndarray, group: int, mx: bool = False):
@@ -463,6 +522,11 @@ def make_workload(sp: WorkloadSpec) -> Workload:
         if ps % st or dl % sd:
             raise ValueError("scale tiles must divide the page and the latent dims")
         kv_scale = np.full((num_pages, ps // st, dl // sd), np.nan, dtype=np.float32)
+    elif sp.kv_dtype in FP4_GROUP:
+        kv = np.full((rows, dl // 2), 0x77, dtype=np.uint8)
+        kv_rope = np.full((rows, dr), BF16_NAN, dtype=np.uint16)
+        kv_scale = np.full((rows, dl // FP4_GROUP[sp.kv_dtype]),     # NaN scales
+                           255 if sp.kv_dtype == "mxfp4" else E4M3_NAN, dtype=np.uint8)
     else:
         raise ValueError(sp.kv_dtype)
     for b in range(sp.batch):
@@ -476,6 +540,9 @@ def make_workload(sp: WorkloadSpec) -> Workload:
                 kv[dst] = x
             elif sp.kv_dtype == "bf16":
                 kv[dst] = to_bf16_bits(x)
+            elif sp.kv_dtype in FP4_GROUP:
+                kv[dst], kv_scale[dst] = quantize_fp4(x[:, :dl], sp.kv_dtype)
+                kv_rope[dst] = to_bf16_bits(x[:, dl:])
             else:
                 # one scale per (st tokens x sd dims) tile of each page's
                 # latent part; the chunk is a multiple of the page size, so
@@ -495,6 +562,8 @@ def make_workload(sp: WorkloadSpec) -> Workload:
     kv = kv.reshape(num_pages, ps, -1)
     if kv_rope is not None:
         kv_rope = kv_rope.reshape(num_pages, ps, dr)
+    if sp.kv_dtype in FP4_GROUP:
+        kv_scale = kv_scale.reshape(num_pages, ps, -1)
 
     # attention queries (absorbed MLA: latent part + rope part)
     qx = _normal(rng, (n_q, sp.heads, D))

@@ -111,6 +111,53 @@ def e8m0_decode(b: np.ndarray) -> np.ndarray:
     return out
 
 
+# 4-bit latent rows: e2m1 codes, two to a byte (even dim in the low half), one
+# scale byte per group of dims.
+FP4_GROUP = {"mxfp4": 32, "nvfp4": 16}
+_E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+_E2M1 = np.concatenate([_E2M1, -_E2M1])
+
+
+def fp4_scale_decode(kv_dtype: str, b: np.ndarray) -> np.ndarray:
+    """Scale bytes of a 4-bit latent -> their values in float64."""
+    if kv_dtype == "mxfp4":
+        return e8m0_decode(b).astype(np.float64)
+    return decode("e4m3", b)
+
+
+def fp4_decode(kv_dtype: str, codes: np.ndarray, scales: np.ndarray) -> np.ndarray:
+    """(bytes [..., d / 2], scale bytes [..., d / group]) -> values [..., d] in fp32,
+    exactly (2 significant bits times at most 4)."""
+    two = np.stack([codes & 15, codes >> 4], axis=-1).reshape(codes.shape[:-1] + (-1,))
+    sc = np.repeat(fp4_scale_decode(kv_dtype, scales), FP4_GROUP[kv_dtype], axis=-1)
+    return (_E2M1[two] * sc).astype(np.float32)
+
+
+def quantize_fp4(x: np.ndarray, kv_dtype: str):
+    """fp32 rows -> (bytes of two codes, scale bytes): the quotients are taken in
+    fp32 and the nearest e2m1 value is found by search, ties to the even code."""
+    x = np.ascontiguousarray(x, dtype=np.float32)
+    g = x.reshape(x.shape[:-1] + (-1, FP4_GROUP[kv_dtype]))
+    amax = np.abs(g).max(axis=-1)
+    byte = np.full(amax.shape, 127, dtype=np.uint8)
+    if kv_dtype == "mxfp4":
+        some = amax > 0
+        e = np.floor(np.log2(amax[some].astype(np.float64))) - 2
+        byte[some] = np.clip(e + 127, 0, 254).astype(np.uint8)
+    else:
+        s = np.where(amax > 0, amax / np.float32(6), np.float32(1)).astype(np.float32)
+        byte = e4m3_encode(np.minimum(s, np.float32(448)))
+    sc = fp4_scale_decode(kv_dtype, byte).astype(np.float32)[..., None]
+    quot = np.where(sc > 0, g / np.where(sc > 0, sc, np.float32(1)), np.float32(0))
+    # (past 8 everything is nearest to 6; the cut keeps the differences exact)
+    dist = np.abs(np.minimum(np.abs(quot).astype(np.float64), 8.0)[..., None] - _E2M1[:8])
+    # among the nearest codes the even one: order them 0, 2, 4, 6, 1, 3, 5, 7
+    order = np.array([0, 2, 4, 6, 1, 3, 5, 7])
+    code = order[np.argmin(dist[..., order], axis=-1)] + 8 * np.signbit(quot)
+    code = code.reshape(x.shape).astype(np.uint8)
+    return code[..., ::2] | (code[..., 1::2] << 4), byte
+
+
 def _index_dtype(wl):
     return wl.spec.index_dtype
 
@@ -163,12 +210,18 @@ def sparse_attn(wl, idx: np.ndarray, nthreads: int | None = None):
     q = np.ascontiguousarray(wl.q)
     kv = np.ascontiguousarray(wl.kv)
     rope = None if wl.kv_rope is None else np.ascontiguousarray(wl.kv_rope)
-    ksc = _c(wl.kv_scale, np.float32)
+    kv_dt = sp.kv_dtype
+    if kv_dt in FP4_GROUP:  # exact in fp32: attend over the decoded rows
+        kv = np.concatenate([fp4_decode(kv_dt, kv, np.ascontiguousarray(wl.kv_scale)),
+                             widen("bf16", rope)], axis=-1)
+        kv_dt, rope, ksc = "f32", None, None
+    else:
+        ksc = _c(wl.kv_scale, np.float32)
     q_seq, q_pos = _c(wl.q_seq, np.int32), _c(wl.q_pos, np.int32)
     pt = _c(wl.page_table, np.int32)
     rc = _load().oracle_sparse_attn(
         n_q, _ptr(q_seq), _ptr(q_pos), sp.heads, sp.d_latent, sp.d_rope,
-        _DT[sp.q_dtype], _ptr(q), sp.softmax_scale, _DT[sp.kv_dtype], _ptr(kv), _ptr(rope),
+        _DT[sp.q_dtype], _ptr(q), sp.softmax_scale, _DT[kv_dt], _ptr(kv), _ptr(rope),
         _ptr(ksc), sp.kv_tile[0], sp.kv_tile[1],
         _ptr(pt), pt.shape[1], sp.page_size, wl.num_pages, _ptr(idx), K,
         _ptr(out), _ptr(lse), nthreads or threads())
@@ -232,7 +285,8 @@ def append_tokens(pools: dict, layout: dict, seq, pos, k_new=None, kv_new=None):
     pools: ``k_index``, ``k_index_scale``, ``kv``, ``kv_rope``, ``kv_scale`` (numpy
     arrays shaped as the cache stores them; absent entries are None).
     layout: ``page_table`` [batch, max_pages], ``page_size``, ``num_pages``,
-    ``index_dtype`` ("e4m3"/"bf16"/"f32"), ``kv_dtype`` ("e4m3"/"bf16"/"f32"), ``d_latent``,
+    ``index_dtype`` ("e4m3"/"bf16"/"f32"), ``kv_dtype`` ("e4m3"/"mxfp4"/"nvfp4"/"bf16"/"f32"),
+    ``d_latent``,
     ``kv_scale_dims`` (latent dims per scale; one token per scale).
     k_new [n, d_index], kv_new [n, d_latent + d_rope]: fp32 values.
     Token i goes to physical row page_table[seq, pos // page_size] * page_size +
@@ -265,6 +319,11 @@ def append_tokens(pools: dict, layout: dict, seq, pos, k_new=None, kv_new=None):
             row = np.asarray(kv_new[i], dtype=np.float32)
             if layout["kv_dtype"] == "e4m3":
                 codes, sc = quantize_e4m3(row[:dl], layout["kv_scale_dims"])
+                out["kv"][page, slot] = codes
+                out["kv_scale"][page, slot] = sc
+                out["kv_rope"][page, slot] = to_bf16(row[dl:])
+            elif layout["kv_dtype"] in FP4_GROUP:
+                codes, sc = quantize_fp4(row[:dl], layout["kv_dtype"])
                 out["kv"][page, slot] = codes
                 out["kv_scale"][page, slot] = sc
                 out["kv_rope"][page, slot] = to_bf16(row[dl:])
