@@ -1,0 +1,308 @@
+// sfa_gather.cuh -- the selected latent rows of a query, gathered into a
+// shared-memory ring of 64-row tiles as tensor-core operands: used by the
+// sparse attention (sfa_mma.cu) and the accumulated weights (weights.cu).
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+
+namespace sa {
+namespace sfa {
+using namespace sm100;
+
+constexpr int kDl = 512, kDr = 64, kD = kDl + kDr;
+constexpr int kBlocks = kD / 64;  // 64-dim (128-byte) column blocks of a row
+constexpr int kTile = 64;         // selected keys per tile
+constexpr int kStages = 3;
+// tiles of rows prefetched into L2 ahead of the copies (1 measured faster
+// than 2, 3, 4 or 6 on the 32K decode: 0.0945 against 0.0977 ms at 4)
+constexpr int kPrefetch = 1;
+constexpr int kProducerWarps = 7;
+constexpr int kChunksPerRow = kD * 2 / 16;  // 72 sixteen-byte pieces of a row
+// Stage layout: key k of a tile, 64-dim block b -> byte (k/8)*kGroupBytes +
+// b*1024 + (k%8)*128 (+ the 16-byte swizzle): the S view (K-major, 8-key
+// groups kGroupBytes apart) and the P V view (MN-major, 64-dim atoms 1024
+// bytes apart, 8-key groups kGroupBytes apart) read the same bytes.
+constexpr uint32_t kGroupBytes = kBlocks * 1024;             // 9216
+constexpr uint32_t kStageBytes = (kTile / 8) * kGroupBytes;  // 73728
+
+// Arrivals that fill a stage: every producer lane once, and once more for the
+// asynchronous rope copies next to a 4-bit latent's stores.
+template <int kKv>
+constexpr uint32_t kFullArrivals = (is_fp4(kKv) ? 2 : 1) * 32 * kProducerWarps;
+
+// The latent dims of a 4-bit row lie in the stage with each group of eight
+// reordered: place 2i holds dim i, place 2i + 1 dim i + 4 (i < 4), the order in
+// which nibbles i and i + 4 of a word become one bf16 pair.  Q is reordered
+// the same way and the output back; scores do not depend on it.
+__device__ __forceinline__ uint4 fp4_order(const uint4 x) {
+    return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
+                      __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
+}
+__host__ __device__ constexpr int fp4_place(int dim) {
+    return (dim & ~7) + 2 * (dim & 3) + ((dim >> 2) & 1);
+}
+
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 r = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                     *reinterpret_cast<const __nv_bfloat162 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
+// Eight codes of one word times a scale -> eight bf16 in fp4_order.  The sign,
+// exponent and mantissa bits of an e2m1 code, put at bits 15 and 8..6, are a
+// bf16 of the code's value times 2^-126 (its two subnormals are bf16's too);
+// that times 2^126 and the scale has at most 6 significant bits, so both
+// products are exact unless they leave bf16's range.
+__device__ __forceinline__ uint4 fp4_to_bf16(uint32_t w, uint32_t scale2) {
+    constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
+    constexpr uint32_t kUp = 0x7E807E80u;  // 2^126, twice
+    const uint32_t p0 = ((w << 12) & kSign) | ((w << 6) & kMag);
+    const uint32_t p1 = ((w << 8) & kSign) | ((w << 2) & kMag);
+    const uint32_t p2 = ((w << 4) & kSign) | ((w >> 2) & kMag);
+    const uint32_t p3 = (w & kSign) | ((w >> 6) & kMag);
+    return make_uint4(bf16x2_mul(bf16x2_mul(p0, kUp), scale2),
+                      bf16x2_mul(bf16x2_mul(p1, kUp), scale2),
+                      bf16x2_mul(bf16x2_mul(p2, kUp), scale2),
+                      bf16x2_mul(bf16x2_mul(p3, kUp), scale2));
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
+    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
+}
+
+// 2^x on the special-function unit (ex2.approx: relative error ~2^-22, -inf -> 0).
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Tiles [j0, j1) of the compacted key list handled by this split.
+template <int kKeys = kTile>
+__device__ __forceinline__ void split_range(int32_t n_valid, int32_t split, int32_t splits,
+                                            int32_t &j0, int32_t &j1) {
+    const int32_t tiles = (n_valid + kKeys - 1) / kKeys;
+    j0 = (int32_t)((int64_t)tiles * split / splits);
+    j1 = (int32_t)((int64_t)tiles * (split + 1) / splits);
+}
+
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
+                                          int32_t *status) {
+    bool ok = true;
+    if (lane_id() == 0) ok = mbar_wait(bar, parity, abort_flag, status);
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+    __syncwarp();
+    return ok;
+}
+
+// Row producers (kProducerWarps warps, pw = 0 .. kProducerWarps - 1): tiles
+// 0 .. T - 1 of tile_rows (physical rows, whole tiles) go through the ring.
+// Stage `q_stage` and those behind it hold Q until q_ready completes.
+//
+// The ring holds about one tile in flight per SM, too little to cover the
+// latency of random row reads from HBM; so the rows of the next tile are on
+// their way while a tile is written: pulled into L2 (bf16, e4m3: one bulk
+// prefetch per row), or already loaded into registers (4 bits: a lane's eight
+// bytes of codes and its scale byte).  Row indices are loaded one iteration
+// before they are used, so no global load latency sits between a freed stage
+// and its copies.
+template <int kKv>
+__device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t *tile_rows, int T,
+                                             int pw, uint8_t (*stages)[kStageBytes],
+                                             uint64_t *kv_full, uint64_t *kv_empty,
+                                             uint64_t *q_ready, int q_stage,
+                                             volatile int *abort_flag, int32_t *status) {
+    const int lane = lane_id();
+    const uint8_t *kv = static_cast<const uint8_t *>(p.kv);
+    const uint8_t *rope = static_cast<const uint8_t *>(p.kv_rope);
+    auto stage_free = [&](int n) -> bool {
+        if (!warp_wait(&kv_empty[n % kStages], ((n / kStages) & 1) ^ 1, abort_flag, status))
+            return false;
+        return n != q_stage || warp_wait(q_ready, 0, abort_flag, status);
+    };
+    if constexpr (is_fp4(kKv)) {
+        constexpr int kGroup = fp4_group(kKv);
+        constexpr int kSlots = (kTile + kProducerWarps - 1) / kProducerWarps;
+        const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale);
+        uint2 code[kSlots];
+        uint32_t sb[kSlots];
+        // warp pw takes keys pw, pw + 7, ...; lane c dims 16c .. 16c + 15
+        auto load = [&](int32_t lo, int32_t hi, uint2 *c, uint32_t *s) {
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                const int k = pw + kProducerWarps * i;
+                if (k < kTile) {
+                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? lo : hi, k & 31);
+                    c[i] = __ldg(reinterpret_cast<const uint2 *>(kv + (int64_t)r * (kDl / 2)) +
+                                 lane);
+                    s[i] = __ldg(scales + (int64_t)r * (kDl / kGroup) + lane * 16 / kGroup);
+                }
+            }
+        };
+        auto row_pair = [&](int n, int32_t &lo, int32_t &hi) {
+            lo = n < T ? __ldg(tile_rows + n * kTile + lane) : 0;
+            hi = n < T ? __ldg(tile_rows + n * kTile + 32 + lane) : 0;
+        };
+        const int pk = pw * 32 + lane;
+        int32_t lo, hi, lo1, hi1;
+        row_pair(0, lo, hi);
+        row_pair(1, lo1, hi1);
+        if (T > 0) load(lo, hi, code, sb);
+        for (int n = 0; n < T; ++n) {
+            const int st = n % kStages;
+            uint2 next_code[kSlots];
+            uint32_t next_sb[kSlots];
+            int32_t lo2, hi2;
+            row_pair(n + 2, lo2, hi2);
+            if (n + 1 < T) {
+                load(lo1, hi1, next_code, next_sb);
+                if (pk < kTile) {
+                    const int32_t r = pw == 0 ? lo1 : hi1;
+                    prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
+                }
+            }
+            if (!stage_free(n)) break;
+            uint8_t *stage = stages[st];
+            const uint32_t stage_u = smem_u32(stage);
+#pragma unroll
+            for (int i = 0; i < (kTile * 8 + 32 * kProducerWarps - 1) / (32 * kProducerWarps); ++i) {
+                const int c = pk + i * 32 * kProducerWarps;  // 16-byte piece of a rope row
+                const int k = c >> 3;
+                const int32_t rl = __shfl_sync(0xffffffffu, lo, k & 31);
+                const int32_t rh = __shfl_sync(0xffffffffu, hi, k & 31);
+                if (c < kTile * 8) {
+                    const int32_t r = k < 32 ? rl : rh;
+                    cp_async16(stage_u + (k >> 3) * kGroupBytes + (kBlocks - 1) * 1024 +
+                                   (k & 7) * 128 + (((c & 7) ^ (k & 7)) << 4),
+                               rope + (int64_t)r * (kDr * 2) + (c & 7) * 16);
+                }
+            }
+            cp_async_arrive(&kv_full[st]);
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                const int k = pw + kProducerWarps * i;
+                if (k < kTile) {
+                    const __nv_bfloat162 s2 = __float2bfloat162_rn(fp4_scale_value(kKv, sb[i]));
+                    const uint32_t scale2 = *reinterpret_cast<const uint32_t *>(&s2);
+                    uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
+                    const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
+                    *reinterpret_cast<uint4 *>(dk + b * 1024 + ((c0 ^ sw) << 4)) =
+                        fp4_to_bf16(code[i].x, scale2);
+                    *reinterpret_cast<uint4 *>(dk + b * 1024 + (((c0 + 1) ^ sw) << 4)) =
+                        fp4_to_bf16(code[i].y, scale2);
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&kv_full[st]);
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                code[i] = next_code[i];
+                sb[i] = next_sb[i];
+            }
+            lo = lo1;
+            hi = hi1;
+            lo1 = lo2;
+            hi1 = hi2;
+        }
+    } else {
+        const int pk = pw * 32 + lane;  // key prefetched by this thread
+        const bool prefetcher = pk < kTile;
+        auto prefetch_row = [&](int32_t r) {
+            if constexpr (kKv == SA_BF16) {
+                prefetch_l2(kv + (int64_t)r * (kD * 2), kD * 2);
+            } else {
+                prefetch_l2(kv + (int64_t)r * kDl, kDl);
+                prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
+            }
+        };
+        if (prefetcher) {
+            int32_t r0[kPrefetch];
+#pragma unroll
+            for (int n = 0; n < kPrefetch; ++n) r0[n] = n < T ? __ldg(tile_rows + n * kTile + pk) : 0;
+#pragma unroll
+            for (int n = 0; n < kPrefetch; ++n)
+                if (n < T) prefetch_row(r0[n]);
+        }
+        int32_t pf_row =
+            (prefetcher && kPrefetch < T) ? __ldg(tile_rows + kPrefetch * kTile + pk) : 0;
+        int32_t r_lo = T > 0 ? __ldg(tile_rows + lane) : 0;
+        int32_t r_hi = T > 0 ? __ldg(tile_rows + 32 + lane) : 0;
+        for (int n = 0; n < T; ++n) {
+            const int st = n % kStages;
+            if (prefetcher && n + kPrefetch < T) prefetch_row(pf_row);
+            const bool more = n + 1 < T;
+            const int32_t pf_next = (prefetcher && n + 1 + kPrefetch < T)
+                                        ? __ldg(tile_rows + (n + 1 + kPrefetch) * kTile + pk)
+                                        : 0;
+            const int32_t lo_next = more ? __ldg(tile_rows + (n + 1) * kTile + lane) : 0;
+            const int32_t hi_next = more ? __ldg(tile_rows + (n + 1) * kTile + 32 + lane) : 0;
+            if (!stage_free(n)) break;
+            // warp pw copies keys pw, pw + 7, ... of each tile
+            if constexpr (kKv == SA_BF16) {
+                // a key's 72 sixteen-byte pieces go to lanes (piece % 32) in three steps
+                const uint32_t dst0 = smem_u32(stages[st]);
+#pragma unroll 1  // measured faster than unrolling by 2 or 4 (32K decode: 0.087 against 0.095 ms)
+                for (int k = pw; k < kTile; k += kProducerWarps) {
+                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? r_lo : r_hi, k & 31);
+                    const uint8_t *src = kv + (int64_t)r * (kD * 2);
+                    const uint32_t dk = dst0 + (k >> 3) * kGroupBytes + (k & 7) * 128;
+                    const int sw = k & 7;
+#pragma unroll
+                    for (int i = 0; i < 3; ++i) {
+                        const int c = lane + 32 * i;
+                        if (c < kChunksPerRow)
+                            cp_async16(dk + (c >> 3) * 1024 + (((c & 7) ^ sw) << 4), src + c * 16);
+                    }
+                }
+                cp_async_arrive(&kv_full[st]);
+            } else {
+                // e4m3 latent: lane c dequantises dims 16c .. 16c + 15 of a row
+                // (x its tile's scale, rounded to bf16) into the same swizzled
+                // layout; lanes 0-7 copy the bf16 rope.  Plain stores, so a
+                // proxy fence and an ordinary arrive publish them.
+                uint8_t *stage = stages[st];
+#pragma unroll 2  // measured faster than no unrolling here (1M decode: 0.0327 against 0.0337 ms)
+                for (int k = pw; k < kTile; k += kProducerWarps) {
+                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? r_lo : r_hi, k & 31);
+                    const float sc = kv_scale_at(p, r, 16 * lane);  // this lane's 16 dims
+                    const uint4 x =
+                        __ldg(reinterpret_cast<const uint4 *>(kv + (int64_t)r * kDl) + lane);
+                    uint4 rp = make_uint4(0, 0, 0, 0);
+                    if (lane < 8)
+                        rp = __ldg(reinterpret_cast<const uint4 *>(rope + (int64_t)r * (kDr * 2)) +
+                                   lane);
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint16_t two = static_cast<uint16_t>(xw[i >> 1] >> (16 * (i & 1)));
+                        const float2 f = e4m3x2_to_float2(two);
+                        __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
+                        o[i] = *reinterpret_cast<uint32_t *>(&b2);
+                    }
+                    uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
+                    const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
+                    *reinterpret_cast<uint4 *>(dk + b * 1024 + ((c0 ^ sw) << 4)) =
+                        make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(dk + b * 1024 + (((c0 + 1) ^ sw) << 4)) =
+                        make_uint4(o[4], o[5], o[6], o[7]);
+                    if (lane < 8)
+                        *reinterpret_cast<uint4 *>(dk + 8 * 1024 + ((lane ^ sw) << 4)) = rp;
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&kv_full[st]);
+            }
+            pf_row = pf_next;
+            r_lo = lo_next;
+            r_hi = hi_next;
+        }
+    }
+    cp_async_wait_all();
+}
+
+}  // namespace sfa
+}  // namespace sa

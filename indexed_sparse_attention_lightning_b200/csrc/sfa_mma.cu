@@ -50,21 +50,14 @@
 // the workspace status word.
 #include "common.cuh"
 #include "internal.h"
+#include "sfa_gather.cuh"
 #include "sm100.cuh"
 
 namespace sa {
 namespace {
-using namespace sm100;
+using namespace sfa;
 
 constexpr int kHeadsCta = 64;
-constexpr int kDl = 512, kDr = 64, kD = kDl + kDr;
-constexpr int kBlocks = kD / 64;  // 64-dim (128-byte) column blocks of a row
-constexpr int kTile = 64;         // selected keys per tile
-constexpr int kStages = 3;
-// tiles of rows prefetched into L2 ahead of the copies (1 measured faster
-// than 2, 3, 4 or 6 on the 32K decode: 0.0945 against 0.0977 ms at 4)
-constexpr int kPrefetch = 1;
-constexpr int kProducerWarps = 7;
 constexpr int kSoftmaxWarp0 = 8;  // warps 8-11, one per TMEM subpartition
 constexpr int kThreads = 384;
 constexpr int kMaxK = 2048;
@@ -72,20 +65,12 @@ constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColQ = 0;    // lower half-lanes: Q, 288 columns
 constexpr uint32_t kColS = 288;  // lower half-lanes: two S buffers of 64 columns
 constexpr uint32_t kLaneO = 16;  // O: upper half-lanes, columns [0, 512)
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescaleLog2 = 8.0f;
-constexpr int kChunksPerRow = kD * 2 / 16;  // 72 sixteen-byte pieces of a row
-// Stage layout: key k of a tile, 64-dim block b -> byte (k/8)*kGroupBytes +
-// b*1024 + (k%8)*128 (+ the 16-byte swizzle): the S view (K-major, 8-key
-// groups kGroupBytes apart) and the P V view (MN-major, 64-dim atoms 1024
-// bytes apart, 8-key groups kGroupBytes apart) read the same bytes.  After S,
-// block 8 (the rope) holds P: head h's 64 keys at (h/8)*kGroupBytes + 8*1024 +
-// (h%8)*128 (+ swizzle), the K-major A operand of P V with 8-head groups
-// kGroupBytes apart.
-constexpr uint32_t kGroupBytes = kBlocks * 1024;             // 9216
-constexpr uint32_t kStageBytes = (kTile / 8) * kGroupBytes;  // 73728
-constexpr uint32_t kPOffset = (kBlocks - 1) * 1024;          // the rope block
+// After S, block 8 of a stage (the rope) holds P: head h's 64 keys at
+// (h/8)*kGroupBytes + 8*1024 + (h%8)*128 (+ swizzle), the K-major A operand of
+// P V with 8-head groups kGroupBytes apart.
+constexpr uint32_t kPOffset = (kBlocks - 1) * 1024;  // the rope block
 
 struct SfaSmem {
     // ring stage: 8 groups of 8 rows; a group holds the 9 column blocks of its
@@ -117,34 +102,6 @@ struct SfaArgs {
     float *lse_part;         // [n_q, splits, 128]      (splits > 1)
 };
 
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p) {
-    return reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
-}
-
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
-                                          int32_t *status) {
-    bool ok = true;
-    if (lane_id() == 0) ok = mbar_wait(bar, parity, abort_flag, status);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    __syncwarp();
-    return ok;
-}
-
-// 2^x on the special-function unit (ex2.approx: relative error ~2^-22, -inf -> 0).
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// Tiles [j0, j1) of the compacted key list handled by this split.
-__device__ __forceinline__ void split_range(int32_t n_valid, int32_t split, int32_t splits,
-                                            int32_t &j0, int32_t &j1) {
-    const int32_t tiles = (n_valid + kTile - 1) / kTile;
-    j0 = (int32_t)((int64_t)tiles * split / splits);
-    j1 = (int32_t)((int64_t)tiles * (split + 1) / splits);
-}
-
 // Query t's selected positions -> physical cache rows (compact_rows): one
 // CTA per query.  The fused decode path gets the rows from the top-K kernel.
 constexpr int kRowsThreads = 512;
@@ -172,7 +129,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.kv_full[s], 32 * kProducerWarps);  // one cp.async arrival per lane
+            mbar_init(&sm.kv_full[s], kFullArrivals<kKv>);
             mbar_init(&sm.kv_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[b], 1);
@@ -227,7 +184,8 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                     uint32_t v[32];
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(qr + ((c ^ (h & 7)) << 4));
+                        uint4 x = *reinterpret_cast<const uint4 *>(qr + ((c ^ (h & 7)) << 4));
+                        if (is_fp4(kKv) && b < kBlocks - 1) x = fp4_order(x);
                         v[4 * c] = x.x;
                         v[4 * c + 1] = x.y;
                         v[4 * c + 2] = x.z;
@@ -375,6 +333,13 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
             }
             if (!o_lane) continue;
+            if constexpr (is_fp4(kKv)) {  // back into the order of dims
+                float u[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = v[fp4_place(i)];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] = u[i];
+            }
             const int dv = 32 * c;
             if (a.splits == 1) {
                 if (a.out_dtype == SA_BF16) {
@@ -425,147 +390,9 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         }
     } else if (warp >= 1) {
         // ---------------------------------------------- row producers ---
-        // warp 1 + w copies keys w, w + 7, ... of each tile; a key's 72
-        // sixteen-byte pieces go to lanes (piece % 32) in three steps.  Ring
-        // stage 2 holds Q until the softmax warps have moved it to TMEM.
-        const int pw = warp - 1;
-        const uint8_t *kv = static_cast<const uint8_t *>(p.kv);
-        const int32_t *rows = a.rows + (int64_t)t * a.ld_rows;
-        // The ring holds about one tile in flight per SM, too little to cover
-        // the latency of random row reads from HBM; so the rows of tile
-        // n + kPrefetch are pulled into L2 (one bulk prefetch per row, by
-        // warps 1-2) while tile n is copied, and the next copies start from L2.
-        // Row indices are loaded one iteration before they are used, so no
-        // global load latency sits between a freed stage and its copies.
-        const int pk = pw * 32 + lane;  // key prefetched by this thread
-        const bool prefetcher = pk < kTile;
-        const int32_t *tile_rows = rows + (int64_t)j0 * kTile;
-        const uint8_t *rope = static_cast<const uint8_t *>(p.kv_rope);
-        auto prefetch_row = [&](int32_t r) {
-            if constexpr (kKv == SA_BF16) {
-                prefetch_l2(kv + (int64_t)r * (kD * 2), kD * 2);
-            } else {
-                constexpr int kRowBytes = is_fp4(kKv) ? kDl / 2 : kDl;
-                prefetch_l2(kv + (int64_t)r * kRowBytes, kRowBytes);
-                prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
-            }
-        };
-        if (prefetcher) {
-            int32_t r0[kPrefetch];
-#pragma unroll
-            for (int n = 0; n < kPrefetch; ++n) r0[n] = n < T ? __ldg(tile_rows + n * kTile + pk) : 0;
-#pragma unroll
-            for (int n = 0; n < kPrefetch; ++n)
-                if (n < T) prefetch_row(r0[n]);
-        }
-        int32_t pf_row =
-            (prefetcher && kPrefetch < T) ? __ldg(tile_rows + kPrefetch * kTile + pk) : 0;
-        int32_t r_lo = T > 0 ? __ldg(tile_rows + lane) : 0;
-        int32_t r_hi = T > 0 ? __ldg(tile_rows + 32 + lane) : 0;
-        for (int n = 0; n < T; ++n) {
-            const int st = n % kStages;
-            if (prefetcher && n + kPrefetch < T) prefetch_row(pf_row);
-            const bool more = n + 1 < T;
-            const int32_t pf_next = (prefetcher && n + 1 + kPrefetch < T)
-                                        ? __ldg(tile_rows + (n + 1 + kPrefetch) * kTile + pk)
-                                        : 0;
-            const int32_t lo_next = more ? __ldg(tile_rows + (n + 1) * kTile + lane) : 0;
-            const int32_t hi_next = more ? __ldg(tile_rows + (n + 1) * kTile + 32 + lane) : 0;
-            if (!warp_wait(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1, abort_flag, status)) break;
-            if (n == 2 && !warp_wait(&sm.q_ready, 0, abort_flag, status)) break;
-            if constexpr (kKv == SA_BF16) {
-                const uint32_t dst0 = smem_u32(sm.kv[st]);
-#pragma unroll 1  // measured faster than unrolling by 2 or 4 (32K decode: 0.087 against 0.095 ms)
-                for (int k = pw; k < kTile; k += kProducerWarps) {
-                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? r_lo : r_hi, k & 31);
-                    const uint8_t *src = kv + (int64_t)r * (kD * 2);
-                    const uint32_t dk = dst0 + (k >> 3) * kGroupBytes + (k & 7) * 128;
-                    const int sw = k & 7;
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const int c = lane + 32 * i;
-                        if (c < kChunksPerRow)
-                            cp_async16(dk + (c >> 3) * 1024 + (((c & 7) ^ sw) << 4), src + c * 16);
-                    }
-                }
-                cp_async_arrive(&sm.kv_full[st]);
-            } else if constexpr (is_fp4(kKv)) {
-                // 4-bit latent: lane c decodes dims 16c .. 16c + 15 of a row and
-                // applies its group's scale (e2m1 x E8M0 or e4m3 has at most 6
-                // significant bits, so bf16 holds the product exactly)
-                constexpr int kGroup = fp4_group(kKv);
-                const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale);
-                uint8_t *stage = sm.kv[st];
-#pragma unroll 2
-                for (int k = pw; k < kTile; k += kProducerWarps) {
-                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? r_lo : r_hi, k & 31);
-                    const uint2 x =
-                        __ldg(reinterpret_cast<const uint2 *>(kv + (int64_t)r * (kDl / 2)) + lane);
-                    const uint32_t sb =
-                        __ldg(scales + (int64_t)r * (kDl / kGroup) + lane * 16 / kGroup);
-                    uint4 rp = make_uint4(0, 0, 0, 0);
-                    if (lane < 8)
-                        rp = __ldg(reinterpret_cast<const uint4 *>(rope + (int64_t)r * (kDr * 2)) + lane);
-                    const float sc = fp4_scale_value(kKv, sb);
-                    const uint32_t xw[2] = {x.x, x.y};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = e2m1x2_to_float2((xw[i >> 2] >> (8 * (i & 3))) & 255u);
-                        __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-                        o[i] = *reinterpret_cast<uint32_t *>(&b2);
-                    }
-                    uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
-                    const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
-                    *reinterpret_cast<uint4 *>(dk + b * 1024 + ((c0 ^ sw) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(dk + b * 1024 + (((c0 + 1) ^ sw) << 4)) =
-                        make_uint4(o[4], o[5], o[6], o[7]);
-                    if (lane < 8)
-                        *reinterpret_cast<uint4 *>(dk + 8 * 1024 + ((lane ^ sw) << 4)) = rp;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&sm.kv_full[st]);
-            } else {
-                // e4m3 latent: lane c dequantises dims 16c .. 16c + 15 of a row
-                // (x its page's scale, rounded to bf16) into the same swizzled
-                // layout; lanes 0-7 copy the bf16 rope.  Plain stores, so a
-                // proxy fence and an ordinary arrive publish them.
-                uint8_t *stage = sm.kv[st];
-#pragma unroll 2  // measured faster than no unrolling here (1M decode: 0.0327 against 0.0337 ms)
-                for (int k = pw; k < kTile; k += kProducerWarps) {
-                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? r_lo : r_hi, k & 31);
-                    const float sc = kv_scale_at(p, r, 16 * lane);  // this lane's 16 dims
-                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(kv + (int64_t)r * kDl) + lane);
-                    uint4 rp = make_uint4(0, 0, 0, 0);
-                    if (lane < 8)
-                        rp = __ldg(reinterpret_cast<const uint4 *>(rope + (int64_t)r * (kDr * 2)) + lane);
-                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint16_t two = static_cast<uint16_t>(xw[i >> 1] >> (16 * (i & 1)));
-                        const float2 f = e4m3x2_to_float2(two);
-                        __nv_bfloat162 b2 = __floats2bfloat162_rn(f.x * sc, f.y * sc);
-                        o[i] = *reinterpret_cast<uint32_t *>(&b2);
-                    }
-                    uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
-                    const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
-                    *reinterpret_cast<uint4 *>(dk + b * 1024 + ((c0 ^ sw) << 4)) =
-                        make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(dk + b * 1024 + (((c0 + 1) ^ sw) << 4)) =
-                        make_uint4(o[4], o[5], o[6], o[7]);
-                    if (lane < 8)
-                        *reinterpret_cast<uint4 *>(dk + 8 * 1024 + ((lane ^ sw) << 4)) = rp;
-                }
-                fence_proxy_async_smem();
-                mbar_arrive(&sm.kv_full[st]);
-            }
-            pf_row = pf_next;
-            r_lo = lo_next;
-            r_hi = hi_next;
-        }
-        cp_async_wait_all();
+        // ring stage 2 holds Q until the softmax warps have moved it to TMEM
+        produce_rows<kKv>(p, a.rows + (int64_t)t * a.ld_rows + (int64_t)j0 * kTile, T, warp - 1,
+                          sm.kv, sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
     } else if (lane == 0 && T > 0) {
         // ------------------------------------------------- MMA issuer ---
         constexpr uint32_t id_s = instr_desc(64, kTile, 1 /*bf16*/, 0, 0);

@@ -5,17 +5,19 @@
 //     w[t,s] = sum_h exp(sm_scale * q[t,h,:] . kv[s,:] - lse[t,h])
 //     acc_out[b,s] = decay * acc_in[b,s] + sum_{t of b} w[t,s]
 // Three kernels: rows (each query's selection as physical rows and positions),
-// weights (one fp32 w per selected entry) and sum.  Sums over queries are taken
+// weights (one fp32 w per selected entry; on the tensor cores for the
+// attention's production shape, on CUDA cores otherwise) and sum.  Sums over queries are taken
 // in the order of t without atomics between CTAs, so results are reproducible:
 // in the sum kernel each warp owns a range of one sequence's positions, keeps
 // its sums in shared memory and walks the queries in order.
 #include "common.cuh"
 #include "internal.h"
+#include "sfa_gather.cuh"
+#include "sm100.cuh"
 
 namespace sa {
 namespace {
-
-constexpr int kTile = 64;  // selected entries per tile: rows are padded to it
+using namespace sfa;
 
 // ------------------------------------------------------------------- rows ---
 constexpr int kRowsThreads = 512;
@@ -91,6 +93,360 @@ weights_simt_kernel(const PathParams p, const float *__restrict__ lse, int32_t l
         for (int i = 1; i < kSimtHeads; ++i) sum += sum_s[i * kSimtRows + lane];
         w[(int64_t)t * ld + k0 + lane] = sum;
     }
+}
+
+cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t ld,
+                                const int32_t *rows, const int32_t *n_valid, float *w,
+                                cudaStream_t s) {
+    const int D = p.d_latent + p.d_rope;
+    const size_t smem = sizeof(float) * ((size_t)kSimtRows * (D + 1) + (size_t)kSimtHeads * D +
+                                         kSimtHeads * kSimtRows);
+    const cudaError_t e = cudaFuncSetAttribute(
+        weights_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    count_launch();
+    return launch_pdl(weights_simt_kernel, dim3((unsigned)(ld / kSimtRows), (unsigned)p.n_q),
+                      dim3(kSimtThreads), smem, s, p, lse, ld, rows, n_valid, w);
+}
+
+// ---------------------------------------- weights on the tensor cores ---
+// 128 heads x 512 + 64 dims.  One CTA takes all heads of one query and a split
+// of its tiles: S = Q K^T with M = 128 heads, N = 64 keys, K = 576, Q in TMEM
+// (288 columns), two S buffers behind it.  There is no P V, so a row is gathered
+// once per query, and a stage is free again as soon as its S is done.
+//   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2,
+//               before the wait on the rows kernel), then issues the MMAs;
+//   warps 1-7   gather the rows (sfa_gather.cuh);
+//   warps 8-11  move Q into TMEM (warp 8 + j: heads 32j .. 32j + 31, one per
+//               lane), then read S: thread = head, 64 keys, exp2 of the logits
+//               minus its head's lse, summed over the 32 heads of the warp by
+//               halving exchanges (62 shuffles leave each lane two keys) and
+//               over the four warps through shared memory, in a fixed order.
+// All waits are bounded; a timeout is reported in the workspace status word.
+// An e4m3 latent value is code x fp32 scale, 24 significant bits: rounded to one
+// bf16 its logits, and with them the fp32 weights, would be off by 2^-9 of
+// every product.  Such a row goes into the stage as two: row k the value's
+// nearest bf16, row k + 32 the nearest bf16 of what that left (2^-18 is left
+// then), and the epilogue adds the two columns; a tile holds 32 keys.  The
+// bf16 and 4-bit rows are exact in bf16: 64 keys.
+template <int kKv>
+constexpr int kKeysOf = kKv == SA_E4M3 ? 32 : kTile;
+
+constexpr int kHeads = 128;
+constexpr int kMmaThreads = 384;
+constexpr int kEpiWarp0 = 8;
+constexpr uint32_t kWTmemCols = 512;
+constexpr uint32_t kWColS = 288;
+
+struct WeightsSmem {
+    uint8_t kv[kStages][kStageBytes];
+    float part[2][4][kTile];  // per tile parity: each warp's sums over its 32 heads
+    uint64_t kv_full[kStages], kv_empty[kStages];
+    uint64_t s_full[2], s_empty[2], q_full, q_ready, done;
+    uint32_t tmem_base;
+    int abort;
+};
+static_assert(sizeof(WeightsSmem) + 1024 <= 232448, "shared memory budget of one CTA");
+
+// Sums v[i] over the warp's lanes: afterwards v[0 .. N/32) hold the totals of
+// entries N/32 * (lane read with its bits reversed) and those behind it.
+template <int N>
+__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+#pragma unroll
+    for (int half = N / 2, bit = 1; bit < 32; half >>= 1, bit <<= 1) {
+        const bool up = (lane & bit) != 0;
+#pragma unroll
+        for (int i = 0; i < half; ++i) {
+            const float send = up ? v[i] : v[i + half];
+            const float keep = up ? v[i + half] : v[i];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
+        }
+    }
+}
+
+// Row producers of an e4m3 latent: tiles of 32 keys as 64 rows (see kKeysOf).
+// As in produce_rows, a tile's codes and scales are in registers before its
+// stage is free.
+__device__ __forceinline__ void produce_e4m3_pairs(const PathParams &p, const int32_t *tile_rows,
+                                                   int T, int pw, WeightsSmem &sm,
+                                                   volatile int *abort_flag, int32_t *status) {
+    constexpr int kKeys = kKeysOf<SA_E4M3>;
+    constexpr int kSlots = (kKeys + kProducerWarps - 1) / kProducerWarps;
+    const int lane = lane_id();
+    const uint8_t *kv = static_cast<const uint8_t *>(p.kv);
+    const uint8_t *rope = static_cast<const uint8_t *>(p.kv_rope);
+    uint4 code[kSlots], rp[kSlots];
+    float sc[kSlots];
+    auto load = [&](int32_t rows, uint4 *c, uint4 *r4, float *s) {
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            const int k = pw + kProducerWarps * i;
+            if (k < kKeys) {
+                const int32_t r = __shfl_sync(0xffffffffu, rows, k);
+                c[i] = __ldg(reinterpret_cast<const uint4 *>(kv + (int64_t)r * kDl) + lane);
+                s[i] = kv_scale_at(p, r, 16 * lane);
+                if (lane < 8)
+                    r4[i] = __ldg(reinterpret_cast<const uint4 *>(rope + (int64_t)r * (kDr * 2)) +
+                                  lane);
+            }
+        }
+    };
+    auto rows_of = [&](int n) { return n < T ? __ldg(tile_rows + n * kKeys + lane) : 0; };
+    int32_t rows1 = rows_of(1);
+    if (T > 0) load(rows_of(0), code, rp, sc);
+    for (int n = 0; n < T; ++n) {
+        const int st = n % kStages;
+        uint4 next_code[kSlots], next_rp[kSlots];
+        float next_sc[kSlots];
+        const int32_t rows2 = rows_of(n + 2);
+        if (n + 1 < T) load(rows1, next_code, next_rp, next_sc);
+        if (!warp_wait(&sm.kv_empty[st], ((n / kStages) & 1) ^ 1, abort_flag, status)) break;
+        if (n == 1 && !warp_wait(&sm.q_ready, 0, abort_flag, status)) break;
+        uint8_t *stage = sm.kv[st];
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            const int k = pw + kProducerWarps * i;
+            if (k < kKeys) {
+                const uint32_t xw[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+                uint32_t near[8], left[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f =
+                        e4m3x2_to_float2(static_cast<uint16_t>(xw[j >> 1] >> (16 * (j & 1))));
+                    const float x = f.x * sc[i], y = f.y * sc[i];
+                    const __nv_bfloat162 a = __floats2bfloat162_rn(x, y);
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(
+                        x - __low2float(a), y - __high2float(a));
+                    near[j] = *reinterpret_cast<const uint32_t *>(&a);
+                    left[j] = *reinterpret_cast<const uint32_t *>(&b);
+                }
+                const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
+                uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
+                uint8_t *dl = dk + (kKeys / 8) * kGroupBytes;
+                const uint32_t o0 = b * 1024 + ((c0 ^ sw) << 4);
+                const uint32_t o1 = b * 1024 + (((c0 + 1) ^ sw) << 4);
+                *reinterpret_cast<uint4 *>(dk + o0) = make_uint4(near[0], near[1], near[2], near[3]);
+                *reinterpret_cast<uint4 *>(dk + o1) = make_uint4(near[4], near[5], near[6], near[7]);
+                *reinterpret_cast<uint4 *>(dl + o0) = make_uint4(left[0], left[1], left[2], left[3]);
+                *reinterpret_cast<uint4 *>(dl + o1) = make_uint4(left[4], left[5], left[6], left[7]);
+                if (lane < 8) {
+                    const uint32_t o = (kBlocks - 1) * 1024 + ((lane ^ sw) << 4);
+                    *reinterpret_cast<uint4 *>(dk + o) = rp[i];
+                    *reinterpret_cast<uint4 *>(dl + o) = make_uint4(0, 0, 0, 0);
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.kv_full[st]);
+#pragma unroll
+        for (int i = 0; i < kSlots; ++i) {
+            code[i] = next_code[i];
+            rp[i] = next_rp[i];
+            sc[i] = next_sc[i];
+        }
+        rows1 = rows2;
+    }
+}
+
+template <int kKv>  // sa_dtype of the latent cache
+__global__ void __launch_bounds__(kMmaThreads, 1)
+weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p, int32_t splits,
+                   const float *__restrict__ lse, int32_t ld, const int32_t *__restrict__ rows,
+                   const int32_t *__restrict__ n_valid_of, float *__restrict__ w) {
+    extern __shared__ uint8_t smem_raw[];
+    WeightsSmem &sm = *reinterpret_cast<WeightsSmem *>(align1024(smem_raw));
+    const int t = blockIdx.x / splits, split = blockIdx.x % splits;
+    const int warp = warp_id(), lane = lane_id();
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&sm.kv_full[s], kFullArrivals<kKv>);
+            mbar_init(&sm.kv_empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&sm.s_full[b], 1);
+            mbar_init(&sm.s_empty[b], 4);  // the four epilogue warps
+        }
+        mbar_init(&sm.q_full, 1);
+        mbar_init(&sm.q_ready, 4);
+        mbar_init(&sm.done, 1);
+        sm.abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == 0) tmem_alloc(&sm.tmem_base, kWTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_trigger();  // after the TMEM allocation: a waiting successor holds none
+    if (warp == 0 && lane == 0) {
+        mbar_arrive_expect_tx(&sm.q_full, kBlocks * kHeads * 128);
+        for (int half = 0; half < 2; ++half)
+            for (int b = 0; b < kBlocks; ++b)
+                tma_load_2d(sm.kv[1 + half] + b * (64 * 128), &tm_q, 64 * b,
+                            t * kHeads + 64 * half, &sm.q_full);
+    }
+    pdl_wait();  // rows and counts come from the rows kernel
+    const uint32_t tmem = sm.tmem_base;
+    volatile int *abort_flag = &sm.abort;
+    int32_t *status = p.status;
+    const int32_t n_valid = n_valid_of[t];
+    int32_t j0, j1;
+    constexpr int kKeys = kKeysOf<kKv>;
+    split_range<kKeys>(n_valid, split, splits, j0, j1);
+    const int T = j1 - j0;
+
+    if (warp >= kEpiWarp0) {
+        const int j = warp & 3;  // TMEM subpartition of this warp
+        const int h = 32 * j + lane;
+        const uint32_t lanes = static_cast<uint32_t>(32 * j) << 16;
+        bool ok = true;
+        if (T > 0) {
+            ok = warp_wait(&sm.q_full, 0, abort_flag, status);
+            if (ok) {
+                const int hr = h & 63;  // row within its half
+#pragma unroll 1
+                for (int b = 0; b < kBlocks; ++b) {
+                    const uint8_t *qr = sm.kv[1 + (h >> 6)] + b * (64 * 128) + hr * 128;
+                    uint32_t v[32];
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        uint4 x = *reinterpret_cast<const uint4 *>(qr + ((c ^ (hr & 7)) << 4));
+                        if (is_fp4(kKv) && b < kBlocks - 1) x = fp4_order(x);
+                        v[4 * c] = x.x;
+                        v[4 * c + 1] = x.y;
+                        v[4 * c + 2] = x.z;
+                        v[4 * c + 3] = x.w;
+                    }
+                    tmem_st32_u(tmem + lanes + 32 * b, v);
+                }
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.q_ready);  // also frees ring stages 1 and 2
+        }
+        const float sl2 = p.sm_scale * kLog2e;
+        const float l = T > 0 ? __ldg(lse + (int64_t)t * kHeads + h) : 0.f;
+        // nothing selected for this head: it adds nothing
+        const float minus = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        float *wt = w + (int64_t)t * ld + (int64_t)j0 * kKeys;
+        const int e = static_cast<int>(__brev(static_cast<unsigned>(lane)) >> 27);
+        // After a failed wait the loop keeps going without waiting or touching
+        // TMEM, so that the warps still meet at the named barrier.
+        for (int n = 0; n < T; ++n) {
+            const int sb = n & 1;
+            if (ok) ok = warp_wait(&sm.s_full[sb], (n >> 1) & 1, abort_flag, status);
+            float v[kKeys];
+            if (ok) {
+                tc_fence_after();
+                float a[32], b[32];
+                tmem_ld32(tmem + lanes + kWColS + kTile * sb, a);
+                tmem_ld32(tmem + lanes + kWColS + kTile * sb + 32, b);
+                tmem_wait_ld_keep(a);
+                tmem_wait_ld_keep(b);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if constexpr (kKeys == 32) {
+                        v[i] = ex2(fmaf(a[i] + b[i], sl2, minus));
+                    } else {
+                        v[i] = ex2(fmaf(a[i], sl2, minus));
+                        v[32 + i] = ex2(fmaf(b[i], sl2, minus));
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < kKeys; ++i) v[i] = 0.f;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sm.s_empty[sb]);
+            lane_sums(v, lane);
+            float *part = sm.part[sb][j];
+#pragma unroll
+            for (int i = 0; i < kKeys / 32; ++i) part[kKeys / 32 * e + i] = v[i];
+            // one barrier a tile: the other parity's sums are read before it
+            named_barrier(1, 128);
+            const int k = 32 * j + lane;  // the first warps finish one key per lane
+            if (k < kKeys && (j0 + n) * kKeys + k < n_valid) {
+                const float(*ps)[kTile] = sm.part[sb];
+                wt[n * kKeys + k] = (ps[0][k] + ps[1][k]) + (ps[2][k] + ps[3][k]);
+            }
+        }
+    } else if (warp >= 1) {
+        const int32_t *tile_rows = rows + (int64_t)t * ld + (int64_t)j0 * kKeys;
+        if constexpr (kKv == SA_E4M3)
+            produce_e4m3_pairs(p, tile_rows, T, warp - 1, sm, abort_flag, status);
+        else
+            produce_rows<kKv>(p, tile_rows, T, warp - 1, sm.kv, sm.kv_full, sm.kv_empty,
+                              &sm.q_ready, 1, abort_flag, status);
+    } else if (lane == 0 && T > 0) {
+        constexpr uint32_t id_s = instr_desc(kHeads, kTile, 1 /*bf16*/, 0, 0);
+        bool ok = mbar_wait(&sm.q_ready, 0, abort_flag, status);
+        for (int n = 0; ok && n < T; ++n) {
+            const int st = n % kStages, sb = n & 1;
+            ok = mbar_wait(&sm.s_empty[sb], ((n >> 1) & 1) ^ 1, abort_flag, status) &&
+                 mbar_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
+            if (!ok) break;
+            fence_proxy_async_smem();
+            tc_fence_after();
+            const uint32_t d = tmem + kWColS + kTile * sb;
+            const uint32_t stage = smem_u32(sm.kv[st]);
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const uint64_t bd = desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    mma_bf16_ts(d, tmem + 32 * b + 8 * k, bd + 2 * k, id_s, (b | k) != 0);
+            }
+            mma_commit(&sm.s_full[sb]);
+            if (n + kStages < T) mma_commit(&sm.kv_empty[st]);
+        }
+        // every MMA issued above has completed before TMEM is released, after a
+        // timeout too
+        mma_commit(&sm.done);
+        int never = 0;
+        mbar_wait(&sm.done, 0, &never, status);
+    }
+    // with no tiles nobody waited for Q: its copy must land before the CTA ends
+    if (warp == 0 && lane == 0 && T == 0) mbar_wait(&sm.q_full, 0, abort_flag, status);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, kWTmemCols);
+    }
+}
+
+// The attention's tensor-core shape; other shapes take the CUDA-core kernel.
+bool weights_mma_supported(const PathParams &p) {
+    const bool kv_ok = p.kv_dtype == SA_BF16 ||
+                       ((p.kv_dtype == SA_E4M3 || is_fp4(p.kv_dtype)) && p.kv_rope != nullptr);
+    return kv_ok && p.q_dtype == SA_BF16 && p.heads == kHeads && p.d_latent == kDl &&
+           p.d_rope == kDr;
+}
+
+cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t top_k, int32_t ld,
+                               const int32_t *rows, const int32_t *n_valid, float *w,
+                               cudaStream_t s) {
+    CUtensorMap tq;
+    if (!encode_tmap_2d(&tq, 2, p.q, kD, (uint64_t)p.n_q * kHeads, kD * 2, 64, 64, true))
+        return cudaErrorInvalidValue;
+    const size_t smem = sizeof(WeightsSmem) + 1024;
+    const auto kernel = p.kv_dtype == SA_BF16    ? weights_mma_kernel<SA_BF16>
+                        : p.kv_dtype == SA_E4M3  ? weights_mma_kernel<SA_E4M3>
+                        : p.kv_dtype == SA_MXFP4 ? weights_mma_kernel<SA_MXFP4>
+                                                 : weights_mma_kernel<SA_NVFP4>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    // one CTA per SM: split a query's tiles while there are SMs without one
+    const int32_t tiles =
+        (int32_t)ceil_div(top_k, p.kv_dtype == SA_E4M3 ? kKeysOf<SA_E4M3> : kTile);
+    const int32_t splits = std::max(1, std::min(tiles, num_sms() / p.n_q));
+    count_launch();
+    return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(kMmaThreads), smem,
+                      s, tq, p, splits, lse, ld, rows, n_valid, w);
 }
 
 // -------------------------------------------------------------------- sum ---
@@ -182,16 +538,9 @@ cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, i
         e = launch_pdl(weights_rows_kernel, dim3((unsigned)p.n_q), dim3(kRowsThreads), 0, s, p, idx,
                        top_k, ld, rows, kept, n_valid, ascending);
         if (e != cudaSuccess) return e;
-        const int D = p.d_latent + p.d_rope;
-        const size_t smem = sizeof(float) * ((size_t)kSimtRows * (D + 1) + (size_t)kSimtHeads * D +
-                                             kSimtHeads * kSimtRows);
-        e = cudaFuncSetAttribute(weights_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)smem);
-        if (e != cudaSuccess) return e;
-        count_launch();
-        e = launch_pdl(weights_simt_kernel, dim3((unsigned)(ld / kSimtRows), (unsigned)p.n_q),
-                       dim3(kSimtThreads), smem, s, p, lse, ld, (const int32_t *)rows,
-                       (const int32_t *)n_valid, w);
+        e = weights_mma_supported(p)
+                ? launch_weights_mma(p, lse, top_k, ld, rows, n_valid, w, s)
+                : launch_weights_simt(p, lse, ld, rows, n_valid, w, s);
         if (e != cudaSuccess) return e;
     }
     const int64_t limit = std::min(ld_acc, (int64_t)p.max_pages * 64);

@@ -7,7 +7,10 @@ sum_d q_d k_d of D products is off by at most dz = 2 eps (D + 2) sm sum |q_d k_d
 + 4 eps |z|.  A weight exp(z - lse) is then off by a factor within exp(+-(dz +
 2^-21)) (2^-21: the exponential itself and its argument's rounding).  The
 attention output also rounds each weight to bf16 (2^-8, half a step) before the
-product with v and itself to the output type.
+product with v and itself to the output type.  For the accumulated weights a
+value of an e4m3 latent (code times fp32 scale) enters as two bf16: the second
+holds what the first left, at most 2^-8 of the value, to half a step, 2^-8, so
+at most 2^-16 sm sum |q_d k_d| is missing from a logit.
 """
 import dataclasses
 
@@ -87,7 +90,10 @@ def logits(wl, t, sel):
     q, sm = q_values(wl)[t], wl.spec.softmax_scale
     z = (q @ kv.T) * sm
     size = (np.abs(q) @ np.abs(kv).T) * sm
-    return z, 2 * EPS * (kv.shape[1] + 2) * size + 4 * EPS * np.abs(z), kv
+    dz = 2 * EPS * (kv.shape[1] + 2) * size + 4 * EPS * np.abs(z)
+    if wl.spec.kv_dtype == "e4m3":
+        dz = dz + 2.0 ** -16 * size
+    return z, dz, kv
 
 
 # ------------------------------------------------------- write and read back ---
