@@ -27,10 +27,17 @@ constexpr int kChunksPerRow = kD * 2 / 16;  // 72 sixteen-byte pieces of a row
 constexpr uint32_t kGroupBytes = kBlocks * 1024;             // 9216
 constexpr uint32_t kStageBytes = (kTile / 8) * kGroupBytes;  // 73728
 
+// A 4-bit latent takes one more producer warp: its rows are decoded, and eight
+// warps of key pairs share a tile evenly.
+constexpr int kFp4Warps = 8;
 // Arrivals that fill a stage: every producer lane once, and once more for the
 // asynchronous rope copies next to a 4-bit latent's stores.
 template <int kKv>
-constexpr uint32_t kFullArrivals = (is_fp4(kKv) ? 2 : 1) * 32 * kProducerWarps;
+constexpr uint32_t kFullArrivals = is_fp4(kKv) ? 2 * 32 * kFp4Warps : 32 * kProducerWarps;
+// Warps of a CTA: 0 (Q and MMA), 1-7 (rows), 8-11 (TMEM readers), 12 (rows, 4 bits).
+template <int kKv>
+constexpr int kCtaThreads = is_fp4(kKv) ? 416 : 384;
+__device__ __forceinline__ int producer_index(int warp) { return warp < 8 ? warp - 1 : 7; }
 
 // The latent dims of a 4-bit row lie in the stage with each group of eight
 // reordered: place 2i holds dim i, place 2i + 1 dim i + 4 (i < 4), the order in
@@ -99,7 +106,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return ok;
 }
 
-// Row producers (kProducerWarps warps, pw = 0 .. kProducerWarps - 1): tiles
+// Row producers (kProducerWarps or, for 4 bits, kFp4Warps warps): tiles
 // 0 .. T - 1 of tile_rows (physical rows, whole tiles) go through the ring.
 // Stage `q_stage` and those behind it hold Q until q_ready completes.
 //
@@ -125,82 +132,94 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
         return n != q_stage || warp_wait(q_ready, 0, abort_flag, status);
     };
     if constexpr (is_fp4(kKv)) {
-        constexpr int kGroup = fp4_group(kKv);
-        constexpr int kSlots = (kTile + kProducerWarps - 1) / kProducerWarps;
+        // Warp pw takes key pairs pw, pw + 8, pw + 16, pw + 24 of a tile, each half
+        // of the warp one key; lane c of a half decodes dims 32c .. 32c + 31.  The
+        // four 16-byte pieces of a lane's dims go out in an order that differs
+        // between neighbouring 64-dim blocks, so that the 32 lanes of a store meet
+        // all banks alike.
+        constexpr int kSlots = kTile / 2 / kFp4Warps;
+        constexpr int kScales = 32 / fp4_group(kKv);  // scale bytes of a lane's dims
         const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale);
-        uint2 code[kSlots];
+        const int half = lane >> 4, c = lane & 15;
+        const int flip = (c >> 1) & 1;
+        const int key = 2 * pw + half;  // of slot 0; slot i: key + 16 i
+        uint2 code[kSlots][2];
         uint32_t sb[kSlots];
-        // warp pw takes keys pw, pw + 7, ...; lane c dims 16c .. 16c + 15
-        auto load = [&](int32_t lo, int32_t hi, uint2 *c, uint32_t *s) {
+        auto load = [&](int32_t lo, int32_t hi, uint2 (*x)[2], uint32_t *s) {
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
-                const int k = pw + kProducerWarps * i;
-                if (k < kTile) {
-                    const int32_t r = __shfl_sync(0xffffffffu, k < 32 ? lo : hi, k & 31);
-                    c[i] = __ldg(reinterpret_cast<const uint2 *>(kv + (int64_t)r * (kDl / 2)) +
-                                 lane);
-                    s[i] = __ldg(scales + (int64_t)r * (kDl / kGroup) + lane * 16 / kGroup);
-                }
+                const int32_t r = __shfl_sync(0xffffffffu, i < 2 ? lo : hi, (key + 16 * i) & 31);
+                const uint2 *src =
+                    reinterpret_cast<const uint2 *>(kv + (int64_t)r * (kDl / 2) + 16 * c);
+                x[i][0] = __ldg(src + flip);
+                x[i][1] = __ldg(src + (flip ^ 1));
+                const uint8_t *sp = scales + (int64_t)r * (kDl / fp4_group(kKv)) + kScales * c;
+                s[i] = kScales == 1 ? __ldg(sp)
+                                    : __ldg(reinterpret_cast<const uint16_t *>(sp));
             }
         };
         auto row_pair = [&](int n, int32_t &lo, int32_t &hi) {
             lo = n < T ? __ldg(tile_rows + n * kTile + lane) : 0;
             hi = n < T ? __ldg(tile_rows + n * kTile + 32 + lane) : 0;
         };
-        const int pk = pw * 32 + lane;
+        // where this lane's pieces go in slot 0's row; slot i is 2 i groups on
+        const int sw = key & 7;
+        const uint32_t row_at = (key >> 3) * kGroupBytes + sw * 128;
+        uint32_t piece[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            piece[j] = row_at + (c >> 1) * 1024 + (((4 * (c & 1) + (j ^ (2 * flip))) ^ sw) << 4);
+        // rope: 16-byte piece lane % 8 of keys 4 pw + lane / 8 and 32 more
+        const int rk = 4 * pw + (lane >> 3);
+        const uint32_t rope_at = (rk >> 3) * kGroupBytes + (kBlocks - 1) * 1024 + (rk & 7) * 128 +
+                                 (((lane & 7) ^ (rk & 7)) << 4);
         int32_t lo, hi, lo1, hi1;
         row_pair(0, lo, hi);
         row_pair(1, lo1, hi1);
         if (T > 0) load(lo, hi, code, sb);
         for (int n = 0; n < T; ++n) {
             const int st = n % kStages;
-            uint2 next_code[kSlots];
+            uint2 next_code[kSlots][2];
             uint32_t next_sb[kSlots];
             int32_t lo2, hi2;
             row_pair(n + 2, lo2, hi2);
             if (n + 1 < T) {
                 load(lo1, hi1, next_code, next_sb);
-                if (pk < kTile) {
-                    const int32_t r = pw == 0 ? lo1 : hi1;
-                    prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
-                }
+                if (pw < 2) prefetch_l2(rope + (int64_t)(pw == 0 ? lo1 : hi1) * (kDr * 2), kDr * 2);
             }
             if (!stage_free(n)) break;
             uint8_t *stage = stages[st];
-            const uint32_t stage_u = smem_u32(stage);
-#pragma unroll
-            for (int i = 0; i < (kTile * 8 + 32 * kProducerWarps - 1) / (32 * kProducerWarps); ++i) {
-                const int c = pk + i * 32 * kProducerWarps;  // 16-byte piece of a rope row
-                const int k = c >> 3;
-                const int32_t rl = __shfl_sync(0xffffffffu, lo, k & 31);
-                const int32_t rh = __shfl_sync(0xffffffffu, hi, k & 31);
-                if (c < kTile * 8) {
-                    const int32_t r = k < 32 ? rl : rh;
-                    cp_async16(stage_u + (k >> 3) * kGroupBytes + (kBlocks - 1) * 1024 +
-                                   (k & 7) * 128 + (((c & 7) ^ (k & 7)) << 4),
-                               rope + (int64_t)r * (kDr * 2) + (c & 7) * 16);
-                }
-            }
+            const uint32_t rope_dst = smem_u32(stage) + rope_at;
+            const int32_t ra = __shfl_sync(0xffffffffu, lo, rk);
+            const int32_t rb = __shfl_sync(0xffffffffu, hi, rk);
+            cp_async16(rope_dst, rope + (int64_t)ra * (kDr * 2) + (lane & 7) * 16);
+            cp_async16(rope_dst + 4 * kGroupBytes,
+                       rope + (int64_t)rb * (kDr * 2) + (lane & 7) * 16);
             cp_async_arrive(&kv_full[st]);
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
-                const int k = pw + kProducerWarps * i;
-                if (k < kTile) {
-                    const __nv_bfloat162 s2 = __float2bfloat162_rn(fp4_scale_value(kKv, sb[i]));
-                    const uint32_t scale2 = *reinterpret_cast<const uint32_t *>(&s2);
-                    uint8_t *dk = stage + (k >> 3) * kGroupBytes + (k & 7) * 128;
-                    const int sw = k & 7, b = lane >> 2, c0 = 2 * (lane & 3);
-                    *reinterpret_cast<uint4 *>(dk + b * 1024 + ((c0 ^ sw) << 4)) =
-                        fp4_to_bf16(code[i].x, scale2);
-                    *reinterpret_cast<uint4 *>(dk + b * 1024 + (((c0 + 1) ^ sw) << 4)) =
-                        fp4_to_bf16(code[i].y, scale2);
+                uint8_t *dst = stage + i * (2 * kGroupBytes);
+                // scales of the pieces in the order they are decoded
+                uint32_t s0 = sb[i], s1 = sb[i];
+                if (kScales == 2) {
+                    s0 = flip ? sb[i] >> 8 : sb[i] & 255u;
+                    s1 = flip ? sb[i] & 255u : sb[i] >> 8;
                 }
+                const __nv_bfloat162 a = __float2bfloat162_rn(fp4_scale_value(kKv, s0));
+                const __nv_bfloat162 b = __float2bfloat162_rn(fp4_scale_value(kKv, s1));
+                const uint32_t a2 = *reinterpret_cast<const uint32_t *>(&a);
+                const uint32_t b2 = *reinterpret_cast<const uint32_t *>(&b);
+                *reinterpret_cast<uint4 *>(dst + piece[0]) = fp4_to_bf16(code[i][0].x, a2);
+                *reinterpret_cast<uint4 *>(dst + piece[1]) = fp4_to_bf16(code[i][0].y, a2);
+                *reinterpret_cast<uint4 *>(dst + piece[2]) = fp4_to_bf16(code[i][1].x, b2);
+                *reinterpret_cast<uint4 *>(dst + piece[3]) = fp4_to_bf16(code[i][1].y, b2);
             }
             fence_proxy_async_smem();
             mbar_arrive(&kv_full[st]);
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
-                code[i] = next_code[i];
+                code[i][0] = next_code[i][0];
+                code[i][1] = next_code[i][1];
                 sb[i] = next_sb[i];
             }
             lo = lo1;

@@ -26,7 +26,7 @@
 // over it: every stage carries its own P, and the softmax of the next tile
 // never waits for P V of this one to release a shared P buffer.
 //
-// Roles (384 threads, one CTA per SM):
+// Roles (384 threads, 416 for a 4-bit latent; one CTA per SM):
 //   warp 0     lane 0 loads Q by TMA (into the third ring stage; this copy
 //              starts before the wait on the top-K kernel), then issues
 //              the MMAs from a non-blocking loop -- S of a tile as soon as its
@@ -35,7 +35,8 @@
 //   warps 1-7  copy the selected rows (16-byte cp.async, the swizzle applied
 //              in the addresses) into a 3-stage ring freed by each tile's P V;
 //              random 1152-byte rows reach shared memory fastest this way (an
-//              e4m3 or 4-bit latent is loaded, decoded to bf16 and stored);
+//              e4m3 or 4-bit latent is loaded, decoded to bf16 and stored, the
+//              4-bit one with warp 12's help);
 //   warps 8-11 move Q into TMEM, then run the online softmax.  Warp 8 + j
 //              owns heads 16j .. 16j + 15 and reads their S rows with 16-lane
 //              loads: thread i holds heads 16j + i/4 and 16j + i/4 + 8, keys
@@ -59,7 +60,6 @@ using namespace sfa;
 
 constexpr int kHeadsCta = 64;
 constexpr int kSoftmaxWarp0 = 8;  // warps 8-11, one per TMEM subpartition
-constexpr int kThreads = 384;
 constexpr int kMaxK = 2048;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColQ = 0;    // lower half-lanes: Q, 288 columns
@@ -117,7 +117,7 @@ sfa_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, 
 }
 
 template <int kKv>  // sa_dtype of the latent cache
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
 sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     SfaSmem &sm = *reinterpret_cast<SfaSmem *>(align1024(smem_raw));
@@ -163,7 +163,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     split_range(n_valid, split, a.splits, j0, j1);
     const int T = j1 - j0;
 
-    if (warp >= kSoftmaxWarp0) {
+    if (warp >= kSoftmaxWarp0 && warp < kSoftmaxWarp0 + 4) {
         const int j = warp & 3;  // TMEM subpartition of this warp
         const int q4 = lane & 3;
         const int ha = 16 * j + (lane >> 2), hb = ha + 8;  // the two heads of this thread
@@ -391,32 +391,44 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     } else if (warp >= 1) {
         // ---------------------------------------------- row producers ---
         // ring stage 2 holds Q until the softmax warps have moved it to TMEM
-        produce_rows<kKv>(p, a.rows + (int64_t)t * a.ld_rows + (int64_t)j0 * kTile, T, warp - 1,
+        produce_rows<kKv>(p, a.rows + (int64_t)t * a.ld_rows + (int64_t)j0 * kTile, T,
+                          producer_index(warp),
                           sm.kv, sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
-    } else if (lane == 0 && T > 0) {
+    } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
+        // The whole warp polls (lane 0's view counts) and computes
+        // descriptors, one elected lane issues.
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        auto ready = [&](uint64_t *bar, uint32_t parity) -> bool {
+            const bool done = __shfl_sync(0xffffffffu, mbar_test(bar, parity) ? 1 : 0, 0) != 0;
+            __syncwarp();
+            return done;
+        };
         constexpr uint32_t id_s = instr_desc(64, kTile, 1 /*bf16*/, 0, 0);
         constexpr uint32_t id_pv = instr_desc(64, 256, 1 /*bf16*/, 0, 1);
-        bool ok = mbar_wait(&sm.q_ready, 0, abort_flag, status);
+        bool ok = warp_wait(&sm.q_ready, 0, abort_flag, status);
         int ns = 0, np = 0;  // next S and next P V to issue
         // P V(np) needs P of tile np
         auto try_pv = [&]() -> bool {
             const int st = np % kStages;
-            if (!(np < ns && mbar_test(&sm.p_full[st], (np / kStages) & 1))) return false;
+            if (!(np < ns && ready(&sm.p_full[st], (np / kStages) & 1))) return false;
             fence_proxy_async_smem();
             tc_fence_after();
             const uint64_t ad = desc_kmajor_sw128_sbo(smem_u32(sm.kv[st]) + kPOffset, kGroupBytes);
+            if (elect_one()) {
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const uint32_t vb = smem_u32(sm.kv[st]) + 4 * half * 1024;
+                for (int half = 0; half < 2; ++half) {
+                    const uint32_t vb = smem_u32(sm.kv[st]) + 4 * half * 1024;
 #pragma unroll
-                for (int k = 0; k < 4; ++k)  // 16 keys (two groups) per instruction
-                    mma_bf16(tmem + (kLaneO << 16) + 256 * half, ad + 2 * k,
-                             desc_mnmajor_sw128(vb + 2 * k * kGroupBytes, 1024, kGroupBytes),
-                             id_pv, (np > 0 || k > 0) ? 1u : 0u);
+                    for (int k = 0; k < 4; ++k)  // 16 keys (two groups) per instruction
+                        mma_bf16(tm + (kLaneO << 16) + 256 * half, ad + 2 * k,
+                                 desc_mnmajor_sw128(vb + 2 * k * kGroupBytes, 1024, kGroupBytes),
+                                 id_pv, (np > 0 || k > 0) ? 1u : 0u);
+                }
+                mma_commit(&sm.o_done);
+                if (np + kStages < T) mma_commit(&sm.kv_empty[st]);
             }
-            mma_commit(&sm.o_done);
-            if (np + kStages < T) mma_commit(&sm.kv_empty[st]);
+            __syncwarp();
             ++np;
             return true;
         };
@@ -428,20 +440,24 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             // ns - 2 is over once P V of it was issued
             if (ns < T && ns < np + 2) {
                 const int st = ns % kStages;
-                if (mbar_test(&sm.kv_full[st], (ns / kStages) & 1)) {
+                if (ready(&sm.kv_full[st], (ns / kStages) & 1)) {
                     fence_proxy_async_smem();
                     tc_fence_after();
-                    const uint32_t d = tmem + kColS + kTile * (ns & 1);
+                    const uint32_t d = tm + kColS + kTile * (ns & 1);
                     const uint32_t stage = smem_u32(sm.kv[st]);
+                    if (elect_one()) {
 #pragma unroll  // 36 MMAs straight-line: measured faster than a loop over the blocks
-                    for (int b = 0; b < kBlocks; ++b) {
-                        const uint64_t bd = desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
+                        for (int b = 0; b < kBlocks; ++b) {
+                            const uint64_t bd =
+                                desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)  // 16 dims (32 bytes) per instruction
-                            mma_bf16_ts(d, tmem + kColQ + 32 * b + 8 * k, bd + 2 * k, id_s,
-                                        (b | k) != 0);
+                            for (int k = 0; k < 4; ++k)  // 16 dims (32 bytes) per instruction
+                                mma_bf16_ts(d, tm + kColQ + 32 * b + 8 * k, bd + 2 * k, id_s,
+                                            (b | k) != 0);
+                        }
+                        mma_commit(&sm.s_full[ns & 1]);
                     }
-                    mma_commit(&sm.s_full[ns & 1]);
+                    __syncwarp();
                     ++ns;
                     progressed = true;
                 }
@@ -450,15 +466,17 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             if (progressed) {
                 t0 = clock64();
                 idle = 0;
-            } else if ((++idle & 63) == 0 && wait_expired(t0, abort_flag, status)) {
-                break;
+            } else if ((++idle & 63) == 0) {
+                const bool stop = lane == 0 && wait_expired(t0, abort_flag, status);
+                if (__shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0) break;
             }
         }
         // o_final: every MMA issued above (all P V of the tiles) has completed;
         // after a timeout too, so that TMEM is never released under an MMA
-        mma_commit(&sm.o_final);
+        if (elect_one()) mma_commit(&sm.o_final);
+        __syncwarp();
         int never = 0;
-        mbar_wait(&sm.o_final, 0, &never, status);
+        warp_wait(&sm.o_final, 0, &never, status);
     }
     // with no tiles nobody waited for Q: its copy must land before the CTA ends
     if (warp == 0 && lane == 0 && T == 0) mbar_wait(&sm.q_full, 0, abort_flag, status);
@@ -573,9 +591,10 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                                                  : sfa_mma_kernel<SA_NVFP4>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
+    const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
     const int64_t grid = 2 * (int64_t)p.n_q * splits;
     count_launch();
-    e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, tq, a);
+    e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, s, tq, a);
     if (e != cudaSuccess || splits == 1) return e;
     count_launch();
     return launch_pdl(sfa_combine_kernel, dim3(static_cast<unsigned>(p.n_q * 128)), dim3(128), 0,

@@ -342,6 +342,27 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
         : "memory");
 }
 
+// One lane of the warp, the same one every time; every lane calls it.
+//
+// MMAs and their commits are issued in an `if (elect_one())` branch of a warp
+// whose lanes all compute the operands: the compiler then keeps descriptors
+// and addresses in uniform registers.  One CTA per SM, M = 128, bf16 K = 16 from
+// tensor memory, back to back: 32 cycles an MMA at N = 64 and 17 at N = 32, the
+// tensor pipe's own rate; in an `if (lane == 0)` branch any N up to 64 takes 48.
+// (Predicating the instructions on the election instead of branching is not
+// safe: a warp that has not reconverged then issues them more than once.)
+__device__ __forceinline__ bool elect_one() {
+    uint32_t lead;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(lead)
+        :
+        : "memory");
+    return lead != 0;
+}
+
 // 16 lanes x 256 bits, 16 repetitions (128 columns): thread t holds lanes
 // t/4 and t/4 + 8 of the addressed 16-lane group, columns 8j + 2(t%4) and
 // 8j + 2(t%4) + 1 of repetition j, as v[4j + 0..1] (first lane) and

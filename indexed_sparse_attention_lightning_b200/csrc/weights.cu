@@ -116,7 +116,7 @@ cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t l
 // once per query, and a stage is free again as soon as its S is done.
 //   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2,
 //               before the wait on the rows kernel), then issues the MMAs;
-//   warps 1-7   gather the rows (sfa_gather.cuh);
+//   warps 1-7   gather the rows (sfa_gather.cuh; warp 12 too for a 4-bit latent);
 //   warps 8-11  move Q into TMEM (warp 8 + j: heads 32j .. 32j + 31, one per
 //               lane), then read S: thread = head, 64 keys, exp2 of the logits
 //               minus its head's lse, summed over the 32 heads of the warp by
@@ -133,7 +133,6 @@ template <int kKv>
 constexpr int kKeysOf = kKv == SA_E4M3 ? 32 : kTile;
 
 constexpr int kHeads = 128;
-constexpr int kMmaThreads = 384;
 constexpr int kEpiWarp0 = 8;
 constexpr uint32_t kWTmemCols = 512;
 constexpr uint32_t kWColS = 288;
@@ -249,7 +248,7 @@ __device__ __forceinline__ void produce_e4m3_pairs(const PathParams &p, const in
 }
 
 template <int kKv>  // sa_dtype of the latent cache
-__global__ void __launch_bounds__(kMmaThreads, 1)
+__global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
 weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p, int32_t splits,
                    const float *__restrict__ lse, int32_t ld, const int32_t *__restrict__ rows,
                    const int32_t *__restrict__ n_valid_of, float *__restrict__ w) {
@@ -295,7 +294,7 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
     split_range<kKeys>(n_valid, split, splits, j0, j1);
     const int T = j1 - j0;
 
-    if (warp >= kEpiWarp0) {
+    if (warp >= kEpiWarp0 && warp < kEpiWarp0 + 4) {
         const int j = warp & 3;  // TMEM subpartition of this warp
         const int h = 32 * j + lane;
         const uint32_t lanes = static_cast<uint32_t>(32 * j) << 16;
@@ -377,35 +376,41 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
         if constexpr (kKv == SA_E4M3)
             produce_e4m3_pairs(p, tile_rows, T, warp - 1, sm, abort_flag, status);
         else
-            produce_rows<kKv>(p, tile_rows, T, warp - 1, sm.kv, sm.kv_full, sm.kv_empty,
+            produce_rows<kKv>(p, tile_rows, T, producer_index(warp), sm.kv, sm.kv_full, sm.kv_empty,
                               &sm.q_ready, 1, abort_flag, status);
-    } else if (lane == 0 && T > 0) {
+    } else if (T > 0) {
+        // the whole warp waits and computes descriptors, one lane issues
         constexpr uint32_t id_s = instr_desc(kHeads, kTile, 1 /*bf16*/, 0, 0);
-        bool ok = mbar_wait(&sm.q_ready, 0, abort_flag, status);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        bool ok = warp_wait(&sm.q_ready, 0, abort_flag, status);
         for (int n = 0; ok && n < T; ++n) {
             const int st = n % kStages, sb = n & 1;
-            ok = mbar_wait(&sm.s_empty[sb], ((n >> 1) & 1) ^ 1, abort_flag, status) &&
-                 mbar_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
+            ok = warp_wait(&sm.s_empty[sb], ((n >> 1) & 1) ^ 1, abort_flag, status) &&
+                 warp_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
             if (!ok) break;
             fence_proxy_async_smem();
             tc_fence_after();
-            const uint32_t d = tmem + kWColS + kTile * sb;
+            const uint32_t d = tm + kWColS + kTile * sb;
             const uint32_t stage = smem_u32(sm.kv[st]);
+            if (elect_one()) {
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const uint64_t bd = desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
+                for (int b = 0; b < kBlocks; ++b) {
+                    const uint64_t bd = desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    mma_bf16_ts(d, tmem + 32 * b + 8 * k, bd + 2 * k, id_s, (b | k) != 0);
+                    for (int k = 0; k < 4; ++k)
+                        mma_bf16_ts(d, tm + 32 * b + 8 * k, bd + 2 * k, id_s, (b | k) != 0);
+                }
+                mma_commit(&sm.s_full[sb]);
+                if (n + kStages < T) mma_commit(&sm.kv_empty[st]);
             }
-            mma_commit(&sm.s_full[sb]);
-            if (n + kStages < T) mma_commit(&sm.kv_empty[st]);
+            __syncwarp();
         }
         // every MMA issued above has completed before TMEM is released, after a
         // timeout too
-        mma_commit(&sm.done);
+        if (elect_one()) mma_commit(&sm.done);
+        __syncwarp();
         int never = 0;
-        mbar_wait(&sm.done, 0, &never, status);
+        warp_wait(&sm.done, 0, &never, status);
     }
     // with no tiles nobody waited for Q: its copy must land before the CTA ends
     if (warp == 0 && lane == 0 && T == 0) mbar_wait(&sm.q_full, 0, abort_flag, status);
@@ -444,8 +449,9 @@ cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t to
     const int32_t tiles =
         (int32_t)ceil_div(top_k, p.kv_dtype == SA_E4M3 ? kKeysOf<SA_E4M3> : kTile);
     const int32_t splits = std::max(1, std::min(tiles, num_sms() / p.n_q));
+    const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
     count_launch();
-    return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(kMmaThreads), smem,
+    return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(threads), smem,
                       s, tq, p, splits, lse, ld, rows, n_valid, w);
 }
 
