@@ -15,9 +15,6 @@ constexpr int kDl = 512, kDr = 64, kD = kDl + kDr;
 constexpr int kBlocks = kD / 64;  // 64-dim (128-byte) column blocks of a row
 constexpr int kTile = 64;         // selected keys per tile
 constexpr int kStages = 3;
-// tiles of rows prefetched into L2 ahead of the copies (1 measured faster
-// than 2, 3, 4 or 6 on the 32K decode: 0.0945 against 0.0977 ms at 4)
-constexpr int kPrefetch = 1;
 constexpr int kProducerWarps = 7;
 constexpr int kChunksPerRow = kD * 2 / 16;  // 72 sixteen-byte pieces of a row
 // Stage layout: key k of a tile, 64-dim block b -> byte (k/8)*kGroupBytes +
@@ -30,10 +27,9 @@ constexpr uint32_t kStageBytes = (kTile / 8) * kGroupBytes;  // 73728
 // A 4-bit latent takes one more producer warp: its rows are decoded, and eight
 // warps of key pairs share a tile evenly.
 constexpr int kFp4Warps = 8;
-// Arrivals that fill a stage: every producer lane once, and once more for the
-// asynchronous rope copies next to a 4-bit latent's stores.
+// Arrivals that fill a stage: every producer lane once.
 template <int kKv>
-constexpr uint32_t kFullArrivals = is_fp4(kKv) ? 2 * 32 * kFp4Warps : 32 * kProducerWarps;
+constexpr uint32_t kFullArrivals = 32 * (is_fp4(kKv) ? kFp4Warps : kProducerWarps);
 // Warps of a CTA: 0 (Q and MMA), 1-7 (rows), 8-11 (TMEM readers), 12 (rows, 4 bits).
 template <int kKv>
 constexpr int kCtaThreads = is_fp4(kKv) ? 416 : 384;
@@ -97,13 +93,13 @@ __device__ __forceinline__ void split_range(int32_t n_valid, int32_t split, int3
     j1 = (int32_t)((int64_t)tiles * (split + 1) / splits);
 }
 
+// Every lane waits itself: with lane 0 waiting for a warp that sits in a
+// shuffle, the other 31 came back about 2000 cycles after it whenever the
+// hardware had suspended it (512-query attention over 4 bits 589 -> 503 us).
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volatile int *abort_flag,
                                           int32_t *status) {
-    bool ok = true;
-    if (lane_id() == 0) ok = mbar_wait(bar, parity, abort_flag, status);
-    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-    __syncwarp();
-    return ok;
+    const bool ok = mbar_wait(bar, parity, abort_flag, status);
+    return __all_sync(0xffffffffu, ok) != 0;
 }
 
 // Row producers (kProducerWarps or, for 4 bits, kFp4Warps warps): tiles
@@ -112,11 +108,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 //
 // The ring holds about one tile in flight per SM, too little to cover the
 // latency of random row reads from HBM; so the rows of the next tile are on
-// their way while a tile is written: pulled into L2 (bf16, e4m3: one bulk
-// prefetch per row), or already loaded into registers (4 bits: a lane's eight
-// bytes of codes and its scale byte).  Row indices are loaded one iteration
-// before they are used, so no global load latency sits between a freed stage
-// and its copies.
+// their way while a tile is written: pulled into L2 (bf16, e4m3: one line per
+// prefetch, spread over all lanes; as one bulk prefetch per row they held two
+// warps up for about 1800 cycles a tile, and the 64-query decode's attention
+// took 0.078 instead of 0.064 ms), or already loaded into registers (4 bits: a
+// lane's sixteen bytes of codes and its scales).  Row indices are loaded one
+// iteration before they are used, so no global load latency sits between a
+// freed stage and its copies.
 template <int kKv>
 __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t *tile_rows, int T,
                                              int pw, uint8_t (*stages)[kStageBytes],
@@ -185,17 +183,20 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             row_pair(n + 2, lo2, hi2);
             if (n + 1 < T) {
                 load(lo1, hi1, next_code, next_sb);
-                if (pw < 2) prefetch_l2(rope + (int64_t)(pw == 0 ? lo1 : hi1) * (kDr * 2), kDr * 2);
+                // a 32-byte sector of a rope row per thread
+                const int32_t r = __shfl_sync(0xffffffffu, pw < 4 ? lo1 : hi1,
+                                              (8 * pw + (lane >> 2)) & 31);
+                prefetch_line_l2(rope + (int64_t)r * (kDr * 2) + (lane & 3) * 32);
             }
-            if (!stage_free(n)) break;
-            uint8_t *stage = stages[st];
-            const uint32_t rope_dst = smem_u32(stage) + rope_at;
+            // this tile's rope pieces: in L2 since the last tile, used after the codes
             const int32_t ra = __shfl_sync(0xffffffffu, lo, rk);
             const int32_t rb = __shfl_sync(0xffffffffu, hi, rk);
-            cp_async16(rope_dst, rope + (int64_t)ra * (kDr * 2) + (lane & 7) * 16);
-            cp_async16(rope_dst + 4 * kGroupBytes,
-                       rope + (int64_t)rb * (kDr * 2) + (lane & 7) * 16);
-            cp_async_arrive(&kv_full[st]);
+            const uint4 rope_a = __ldg(
+                reinterpret_cast<const uint4 *>(rope + (int64_t)ra * (kDr * 2)) + (lane & 7));
+            const uint4 rope_b = __ldg(
+                reinterpret_cast<const uint4 *>(rope + (int64_t)rb * (kDr * 2)) + (lane & 7));
+            if (!stage_free(n)) break;
+            uint8_t *stage = stages[st];
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
                 uint8_t *dst = stage + i * (2 * kGroupBytes);
@@ -214,6 +215,8 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
                 *reinterpret_cast<uint4 *>(dst + piece[2]) = fp4_to_bf16(code[i][1].x, b2);
                 *reinterpret_cast<uint4 *>(dst + piece[3]) = fp4_to_bf16(code[i][1].y, b2);
             }
+            *reinterpret_cast<uint4 *>(stage + rope_at) = rope_a;
+            *reinterpret_cast<uint4 *>(stage + rope_at + 4 * kGroupBytes) = rope_b;
             fence_proxy_async_smem();
             mbar_arrive(&kv_full[st]);
 #pragma unroll
@@ -228,37 +231,40 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             hi1 = hi2;
         }
     } else {
-        const int pk = pw * 32 + lane;  // key prefetched by this thread
-        const bool prefetcher = pk < kTile;
-        auto prefetch_row = [&](int32_t r) {
-            if constexpr (kKv == SA_BF16) {
-                prefetch_l2(kv + (int64_t)r * (kD * 2), kD * 2);
-            } else {
-                prefetch_l2(kv + (int64_t)r * kDl, kDl);
-                prefetch_l2(rope + (int64_t)r * (kDr * 2), kDr * 2);
+        // 128-byte lines of a row: 9 of a bf16 row; 4 of e4m3 codes and the rope
+        constexpr int kLines = kKv == SA_BF16 ? kD * 2 / 128 : kDl / 128 + 1;
+        const int tid = pw * 32 + lane;
+        auto prefetch_tile = [&](int32_t lo, int32_t hi) {
+            constexpr int kSteps =
+                (kTile * kLines + 32 * kProducerWarps - 1) / (32 * kProducerWarps);
+#pragma unroll
+            for (int i = 0; i < kSteps; ++i) {
+                const int c = tid + i * 32 * kProducerWarps;
+                const int k = c / kLines, line = c - k * kLines;
+                const int32_t rl = __shfl_sync(0xffffffffu, lo, k & 31);
+                const int32_t rh = __shfl_sync(0xffffffffu, hi, k & 31);
+                if (k < kTile) {
+                    const int64_t r = k < 32 ? rl : rh;
+                    if constexpr (kKv == SA_BF16)
+                        prefetch_line_l2(kv + r * (kD * 2) + line * 128);
+                    else
+                        prefetch_line_l2(line < kLines - 1 ? kv + r * kDl + line * 128
+                                                           : rope + r * (kDr * 2));
+                }
             }
         };
-        if (prefetcher) {
-            int32_t r0[kPrefetch];
-#pragma unroll
-            for (int n = 0; n < kPrefetch; ++n) r0[n] = n < T ? __ldg(tile_rows + n * kTile + pk) : 0;
-#pragma unroll
-            for (int n = 0; n < kPrefetch; ++n)
-                if (n < T) prefetch_row(r0[n]);
-        }
-        int32_t pf_row =
-            (prefetcher && kPrefetch < T) ? __ldg(tile_rows + kPrefetch * kTile + pk) : 0;
-        int32_t r_lo = T > 0 ? __ldg(tile_rows + lane) : 0;
-        int32_t r_hi = T > 0 ? __ldg(tile_rows + 32 + lane) : 0;
+        auto row_pair = [&](int n, int32_t &lo, int32_t &hi) {
+            lo = n < T ? __ldg(tile_rows + n * kTile + lane) : 0;
+            hi = n < T ? __ldg(tile_rows + n * kTile + 32 + lane) : 0;
+        };
+        int32_t r_lo, r_hi, lo1, hi1;
+        row_pair(0, r_lo, r_hi);
+        row_pair(1, lo1, hi1);
         for (int n = 0; n < T; ++n) {
             const int st = n % kStages;
-            if (prefetcher && n + kPrefetch < T) prefetch_row(pf_row);
-            const bool more = n + 1 < T;
-            const int32_t pf_next = (prefetcher && n + 1 + kPrefetch < T)
-                                        ? __ldg(tile_rows + (n + 1 + kPrefetch) * kTile + pk)
-                                        : 0;
-            const int32_t lo_next = more ? __ldg(tile_rows + (n + 1) * kTile + lane) : 0;
-            const int32_t hi_next = more ? __ldg(tile_rows + (n + 1) * kTile + 32 + lane) : 0;
+            if (n + 1 < T) prefetch_tile(lo1, hi1);
+            int32_t lo2, hi2;
+            row_pair(n + 2, lo2, hi2);
             if (!stage_free(n)) break;
             // warp pw copies keys pw, pw + 7, ... of each tile
             if constexpr (kKv == SA_BF16) {
@@ -315,9 +321,10 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
                 fence_proxy_async_smem();
                 mbar_arrive(&kv_full[st]);
             }
-            pf_row = pf_next;
-            r_lo = lo_next;
-            r_hi = hi_next;
+            r_lo = lo1;
+            r_hi = hi1;
+            lo1 = lo2;
+            hi1 = hi2;
         }
     }
     cp_async_wait_all();

@@ -396,13 +396,12 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                           sm.kv, sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
     } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
-        // The whole warp polls (lane 0's view counts) and computes
-        // descriptors, one elected lane issues.
+        // Lane 0 polls, the whole warp computes descriptors, one elected lane
+        // issues.
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         auto ready = [&](uint64_t *bar, uint32_t parity) -> bool {
-            const bool done = __shfl_sync(0xffffffffu, mbar_test(bar, parity) ? 1 : 0, 0) != 0;
-            __syncwarp();
-            return done;
+            const bool done = lane == 0 && mbar_test(bar, parity);
+            return __shfl_sync(0xffffffffu, done ? 1 : 0, 0) != 0;
         };
         constexpr uint32_t id_s = instr_desc(64, kTile, 1 /*bf16*/, 0, 0);
         constexpr uint32_t id_pv = instr_desc(64, 256, 1 /*bf16*/, 0, 1);
@@ -412,8 +411,8 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         auto try_pv = [&]() -> bool {
             const int st = np % kStages;
             if (!(np < ns && ready(&sm.p_full[st], (np / kStages) & 1))) return false;
-            fence_proxy_async_smem();
-            tc_fence_after();
+            __syncwarp();
+            tc_fence_after();  // P's writers have fenced for the tensor core
             const uint64_t ad = desc_kmajor_sw128_sbo(smem_u32(sm.kv[st]) + kPOffset, kGroupBytes);
             if (elect_one()) {
 #pragma unroll
@@ -441,7 +440,8 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             if (ns < T && ns < np + 2) {
                 const int st = ns % kStages;
                 if (ready(&sm.kv_full[st], (ns / kStages) & 1)) {
-                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if constexpr (kKv == SA_BF16) fence_proxy_async_smem();  // cp.async rows
                     tc_fence_after();
                     const uint32_t d = tm + kColS + kTile * (ns & 1);
                     const uint32_t stage = smem_u32(sm.kv[st]);

@@ -155,10 +155,11 @@ __device__ __forceinline__ void cp_async_wait_all() {
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Asynchronous prefetch of `bytes` (a multiple of 16) of global memory into
-// L2; no completion to wait for.
-__device__ __forceinline__ void prefetch_l2(const void *gmem, uint32_t bytes) {
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(gmem), "r"(bytes) : "memory");
+// Prefetch of the cache line at `gmem` into L2 (an ordinary load-store
+// instruction: a warp's bulk prefetches go out one lane at a time, about 55
+// cycles each).
+__device__ __forceinline__ void prefetch_line_l2(const void *gmem) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(gmem) : "memory");
 }
 
 // Plain bulk copy global -> shared (both 16-byte aligned, size a multiple of 16).

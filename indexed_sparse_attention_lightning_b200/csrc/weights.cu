@@ -388,7 +388,7 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
             ok = warp_wait(&sm.s_empty[sb], ((n >> 1) & 1) ^ 1, abort_flag, status) &&
                  warp_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
             if (!ok) break;
-            fence_proxy_async_smem();
+            if constexpr (kKv == SA_BF16) fence_proxy_async_smem();  // cp.async rows
             tc_fence_after();
             const uint32_t d = tm + kWColS + kTile * sb;
             const uint32_t stage = smem_u32(sm.kv[st]);
