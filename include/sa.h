@@ -430,7 +430,7 @@ SA_API sa_status sa_read_tokens(const sa_cache *cache, int32_t n, const int32_t 
  * equal to acc_out; otherwise the two must not overlap.  decay must be finite.
  * ld_acc >= query->max_visible; a sequence longer than ld_acc, or than its
  * page-table row, is reported (SA_DETAIL_BAD_POSITION) and written up to there.
- * Sums are fp32, taken in the order of t, so results do not change from run
+ * Sums are fp32, taken in a fixed order, so results do not change from run
  * to run.  Only the latent cache and the attention query are read: the
  * query's index fields may be NULL.  Workspace: SA_WS_WEIGHTS. */
 SA_API sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *query,

@@ -146,16 +146,18 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                            cudaStream_t s);
 
 // Accumulated attention weights (weights.cu): the rows kernel compacts each
-// query's selection (rows, kept positions, n_valid; ascending[t] tells whether
-// the kept positions ascend), a weights kernel writes one weight per kept
-// entry (w, same layout), and the sum kernel adds them to the sequences' rows.
-// Leading dimension of rows, kept and w: weights_ld(K).
+// query's selection (rows, kept positions, n_valid) and notes in `starts` where
+// each range of positions begins in it, a weights kernel writes one weight per
+// kept entry (w, same layout), and the sum kernel adds them to the sequences'
+// rows.  Leading dimension of rows, kept and w: weights_ld(K); of starts:
+// weights_starts_ld(max_visible).
 int32_t weights_ld(int32_t top_k);
+int32_t weights_starts_ld(int32_t max_visible);
 cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, int32_t top_k,
                                       const float *lse, const float *acc_in, float decay,
                                       float *acc_out, int64_t ld_acc, int32_t *rows,
-                                      int32_t *kept, int32_t *n_valid, int32_t *ascending,
-                                      float *w, cudaStream_t s);
+                                      int32_t *kept, int32_t *n_valid, int32_t *starts, float *w,
+                                      cudaStream_t s);
 
 // Context-parallel decode steps (cp.cu).
 int32_t cp_merge_max_candidates();
@@ -223,46 +225,86 @@ __device__ __forceinline__ float kv_value(const PathParams &p, int64_t row, int 
 // reported; then padded with the first row up to a multiple of `tile`.
 // Writes rows[0, padded) and *n_valid, and with `kept` the positions behind
 // rows[0, *n_valid).  Called by every thread of a CTA (blockDim.x a multiple
-// of 32); `scratch` is shared memory of 33 ints.
+// of 32); `scratch` is shared memory of kCompactScratch ints.
+//
+// A thread takes four entries of a step (one of each quarter), whose loads are
+// all in flight at once; one scan over the warps' counts places them.
+constexpr int kCompactScratch = 4 * 32 + 2;
 __device__ __forceinline__ void compact_rows(const PathParams &p, int32_t t, const int32_t *sel,
                                              int32_t K, int32_t tile, int32_t *rows,
                                              int32_t *n_valid, int32_t *scratch,
                                              int32_t *kept = nullptr) {
     const int nwarps = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int32_t V = visible_len(p, t);
     const int32_t seq = __ldg(p.q_seq + t);
+    const bool seq_ok = seq >= 0 && seq < p.batch;
+    int32_t V = -1;  // known after the first loads are on their way
     int32_t base = 0;
-    for (int32_t r0 = 0; r0 < K; r0 += blockDim.x) {
-        const int32_t k = r0 + threadIdx.x;
-        const int32_t s = k < K ? sel[k] : -1;
-        int32_t v = -1;
-        if (s >= V) {
-            report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_INDEX);
-        } else if (s >= 0) {
-            const int64_t row = phys_row(p.page_table, p.max_pages, p.num_pages, seq, s);
-            if (row < 0) report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
-            else v = static_cast<int32_t>(row);
+    for (int64_t r0 = 0; r0 < K; r0 += 4 * blockDim.x) {
+        int32_t s[4], v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int64_t k = r0 + j * blockDim.x + threadIdx.x;
+            s[j] = k < K ? sel[k] : -1;
         }
-        const unsigned bal = __ballot_sync(0xffffffffu, v >= 0);
-        if (lane == 0) scratch[w] = __popc(bal);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[j] = -1;
+            if (s[j] >= 0 && seq_ok)
+                v[j] = static_cast<int32_t>(
+                    phys_row(p.page_table, p.max_pages, p.num_pages, seq, s[j]));
+        }
+        if (V < 0) V = visible_len(p, t);
+        unsigned bal[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (s[j] >= V) {
+                report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_INDEX);
+                v[j] = -1;
+            } else if (s[j] >= 0 && v[j] < 0) {
+                report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+            }
+            bal[j] = __ballot_sync(0xffffffffu, v[j] >= 0);
+            if (lane == 0) scratch[j * nwarps + w] = __popc(bal[j]);
+        }
         __syncthreads();
-        int32_t off = base, tot = 0;
-        for (int i = 0; i < nwarps; ++i) {
-            if (i < w) off += scratch[i];
-            tot += scratch[i];
-        }
-        const int32_t pos = off + __popc(bal & ((1u << lane) - 1u));
-        if (v >= 0) {
-            rows[pos] = v;
-            if (kept != nullptr) kept[pos] = s;
-            if (pos == 0) scratch[32] = v;
+        if (w == 0) {  // exclusive scan of 4 * nwarps counts, four per lane
+            int32_t c[4], sum = 0;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = 4 * lane + i < 4 * nwarps ? scratch[4 * lane + i] : 0;
+                sum += c[i];
+            }
+            int32_t inc = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            int32_t at = inc - sum;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (4 * lane + i < 4 * nwarps) scratch[4 * lane + i] = at;
+                at += c[i];
+            }
+            if (lane == 31) scratch[128] = inc;
         }
         __syncthreads();
-        base += tot;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (v[j] >= 0) {
+                const int32_t pos =
+                    base + scratch[j * nwarps + w] + __popc(bal[j] & ((1u << lane) - 1u));
+                rows[pos] = v[j];
+                if (kept != nullptr) kept[pos] = s[j];
+                if (pos == 0) scratch[129] = v[j];
+            }
+        }
+        base += scratch[128];
+        __syncthreads();
     }
     const int32_t padded = (base + tile - 1) / tile * tile;
     if (base > 0)
-        for (int32_t c = base + threadIdx.x; c < padded; c += blockDim.x) rows[c] = scratch[32];
+        for (int32_t c = base + threadIdx.x; c < padded; c += blockDim.x) rows[c] = scratch[129];
     if (threadIdx.x == 0) *n_valid = base;
 }
 }  // namespace sa

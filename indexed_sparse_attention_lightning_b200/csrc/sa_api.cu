@@ -161,8 +161,8 @@ struct Layout {
     size_t indexer_total, decode_total;
     size_t attn_rows, attn_n_valid, attn_o_part, attn_lse_part, attn_total;
     // accumulated weights: status | rows | kept | w [n_q, weights_ld] each |
-    // n_valid [n_q] | ascending [n_q]
-    size_t wt_rows, wt_kept, wt_w, wt_n_valid, wt_ascending, wt_total;
+    // n_valid [n_q] | starts [n_q, weights_starts_ld]
+    size_t wt_rows, wt_kept, wt_w, wt_n_valid, wt_starts, wt_total;
 };
 
 size_t part_bytes(size_t nq, int32_t splits, size_t per) {
@@ -203,8 +203,9 @@ Layout make_layout(const sa_query *q, int32_t top_k) {
     l.wt_kept = align_up(l.wt_rows + wt_bytes);
     l.wt_w = align_up(l.wt_kept + wt_bytes);
     l.wt_n_valid = align_up(l.wt_w + wt_bytes);
-    l.wt_ascending = align_up(l.wt_n_valid + sizeof(int32_t) * nq);
-    l.wt_total = align_up(l.wt_ascending + sizeof(int32_t) * nq);
+    l.wt_starts = align_up(l.wt_n_valid + sizeof(int32_t) * nq);
+    l.wt_total =
+        align_up(l.wt_starts + sizeof(int32_t) * nq * (size_t)weights_starts_ld(q->max_visible));
     return l;
 }
 
@@ -580,7 +581,7 @@ sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *query, co
         reinterpret_cast<int32_t *>(base + l.wt_rows),
         reinterpret_cast<int32_t *>(base + l.wt_kept),
         reinterpret_cast<int32_t *>(base + l.wt_n_valid),
-        reinterpret_cast<int32_t *>(base + l.wt_ascending),
+        reinterpret_cast<int32_t *>(base + l.wt_starts),
         reinterpret_cast<float *>(base + l.wt_w), s));
 }
 

@@ -110,7 +110,7 @@ sfa_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, 
                 int32_t *__restrict__ rows, int32_t *__restrict__ n_valid_out) {
     pdl_wait();
     pdl_trigger();
-    __shared__ int32_t scratch[33];
+    __shared__ int32_t scratch[kCompactScratch];
     const int t = blockIdx.x;
     compact_rows(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld_rows,
                  n_valid_out + t, scratch);

@@ -19,26 +19,42 @@ namespace sa {
 namespace {
 using namespace sfa;
 
+constexpr int kSumRange = 1024;  // positions per CTA of the sum kernel
+
 // ------------------------------------------------------------------- rows ---
+// starts[t, c] = first kept entry of query t at or past position c * kSumRange
+// (the last column: all of them); starts[t, 0] = -1 where the kept positions
+// do not ascend.
 constexpr int kRowsThreads = 512;
 __global__ void __launch_bounds__(kRowsThreads)
 weights_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, int32_t ld,
-                    int32_t *rows, int32_t *kept, int32_t *n_valid, int32_t *ascending) {
+                    int32_t ld_starts, int32_t *rows, int32_t *kept, int32_t *n_valid,
+                    int32_t *starts) {
     pdl_wait();
     pdl_trigger();
-    __shared__ int32_t scratch[33];
+    __shared__ int32_t scratch[kCompactScratch];
     __shared__ int32_t n_s;
     const int t = blockIdx.x;
     int32_t *pos = kept + (int64_t)t * ld;
     compact_rows(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld, &n_s, scratch, pos);
     __syncthreads();
     const int32_t n = n_s;
+    int32_t *st = starts + (int64_t)t * ld_starts;
     int32_t falls = 0;
-    for (int32_t i = threadIdx.x; i + 1 < n; i += kRowsThreads) falls |= pos[i] > pos[i + 1];
+    for (int32_t i = threadIdx.x; i <= n; i += kRowsThreads) {
+        const int32_t at = i < n ? pos[i] : -1, before = i > 0 ? pos[i - 1] : -1;
+        if (i > 0 && i < n && before > at) {
+            falls = 1;
+            continue;
+        }
+        const int32_t c0 = i > 0 ? before / kSumRange + 1 : 0;
+        const int32_t c1 = i < n ? at / kSumRange : ld_starts - 1;
+        for (int32_t c = c0; c <= c1; ++c) st[c] = i;
+    }
     falls = __syncthreads_or(falls);
     if (threadIdx.x == 0) {
         n_valid[t] = n;
-        ascending[t] = !falls;
+        if (falls) st[0] = -1;
     }
 }
 
@@ -456,75 +472,112 @@ cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t to
 }
 
 // -------------------------------------------------------------------- sum ---
+// One CTA per range of a sequence's positions.  Warp w walks query groups w,
+// w + 8, ... of 32: its lanes look the queries' entries in the range up, then
+// the entries are added to the warp's own sums in shared memory, one query
+// after another (four queries' loads in flight).  The warps' sums are added in
+// the order of w at the end.
 constexpr int kSumWarps = 8;
-constexpr int kSumRange = 512;  // positions per warp
+constexpr int kSumThreads = 32 * kSumWarps;
+constexpr int kSumQueries = 4;  // queries whose entries are loaded together
+constexpr int kSumEntries = 2;  // of each, 32 entries this many times; the rest follow one by one
 
-// First entry of pos[0, n) (ascending) that is >= v.
-__device__ __forceinline__ int32_t lower_bound(const int32_t *pos, int32_t n, int32_t v) {
-    int32_t lo = 0, hi = n;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi) >> 1;
-        if (pos[mid] < v) lo = mid + 1;
-        else hi = mid;
-    }
-    return lo;
-}
-
-__global__ void __launch_bounds__(32 * kSumWarps)
+__global__ void __launch_bounds__(kSumThreads)
 weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld,
-                   const int32_t *__restrict__ kept, const int32_t *__restrict__ n_valid,
-                   const int32_t *__restrict__ ascending, const float *__restrict__ w,
-                   const float *acc_in, float decay, float *acc_out, int64_t ld_acc) {
+                   int32_t ld_starts, const int32_t *__restrict__ kept,
+                   const int32_t *__restrict__ n_valid, const int32_t *__restrict__ starts,
+                   const float *__restrict__ w, const float *acc_in, float decay, float *acc_out,
+                   int64_t ld_acc) {
     pdl_wait();
     pdl_trigger();
     __shared__ float sums[kSumWarps][kSumRange];
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int32_t used[kSumWarps];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int32_t b = (int32_t)(blockIdx.x / chunks), c = (int32_t)(blockIdx.x % chunks);
     int32_t len = p.seq_len[b];
     if (len > limit) {
-        if (c == 0 && threadIdx.x == 0)
-            report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
+        if (c == 0 && tid == 0) report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
         len = limit;
     }
-    const int64_t p0 = ((int64_t)c * kSumWarps + warp) * kSumRange;
-    if (p0 >= len) return;
-    const int32_t lo = (int32_t)p0, hi = (int32_t)min((int64_t)len, p0 + kSumRange);
+    const int32_t lo = c * kSumRange;
+    if (lo >= len) return;
+    const int32_t hi = min(len, lo + kSumRange);
+    const int64_t base = (int64_t)b * ld_acc;
+    float old[kSumRange / kSumThreads];  // on its way while the entries are added
+#pragma unroll
+    for (int i = 0; i < kSumRange / kSumThreads; ++i) {
+        const int32_t at = lo + i * kSumThreads + tid;
+        old[i] = acc_in != nullptr && at < hi ? acc_in[base + at] : 0.0f;
+    }
     float *s = sums[warp];
-    for (int i = lane; i < kSumRange; i += 32) s[i] = 0.0f;
-    __syncwarp();
-    for (int32_t t0 = 0; t0 < p.n_q; t0 += 32) {
-        // lane l looks query t0 + l up: its entries [k0, k1) may fall in the range
+    bool cleared = false;
+    for (int32_t t0 = 32 * warp; t0 < p.n_q; t0 += 32 * kSumWarps) {
         const int32_t t = t0 + lane;
         int32_t k0 = 0, k1 = 0;
         if (t < p.n_q && p.q_seq[t] == b) {
-            k1 = n_valid[t];
-            if (ascending[t]) {
-                const int32_t *pos = kept + (int64_t)t * ld;
-                const int32_t n = k1;
-                k0 = lower_bound(pos, n, lo);
-                k1 = k0 + lower_bound(pos + k0, n - k0, hi);
+            // a query sees fewer positions than the sequence has when others follow
+            const int32_t *st = starts + (int64_t)t * ld_starts;
+            k0 = st[min(c, ld_starts - 1)];
+            k1 = st[min(c + 1, ld_starts - 1)];
+            if (st[0] < 0) {  // not ascending: look at all of them
+                k0 = 0;
+                k1 = n_valid[t];
             }
         }
         uint32_t todo = __ballot_sync(0xffffffffu, k1 > k0);
+        if (todo != 0 && !cleared) {
+            for (int i = lane; i < kSumRange; i += 32) s[i] = 0.0f;
+            __syncwarp();
+            cleared = true;
+        }
         while (todo != 0) {
-            const int u = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int32_t e0 = __shfl_sync(0xffffffffu, k0, u);
-            const int32_t e1 = __shfl_sync(0xffffffffu, k1, u);
-            const int64_t row = (int64_t)(t0 + u) * ld;
-            for (int32_t k = e0 + lane; k < e1; k += 32) {
-                const int32_t at = kept[row + k];
+            int32_t at[kSumQueries][kSumEntries], from[kSumQueries], to[kSumQueries];
+            float x[kSumQueries][kSumEntries];
+            int64_t row[kSumQueries];
+#pragma unroll
+            for (int j = 0; j < kSumQueries; ++j) {
+                const int u = todo != 0 ? __ffs(todo) - 1 : 0;
+                from[j] = __shfl_sync(0xffffffffu, k0, u);
+                to[j] = todo != 0 ? __shfl_sync(0xffffffffu, k1, u) : from[j];
+                row[j] = (int64_t)(t0 + u) * ld;
+                todo &= todo - 1;
+#pragma unroll
+                for (int e = 0; e < kSumEntries; ++e) {
+                    const int32_t k = from[j] + 32 * e + lane;
+                    at[j][e] = k < to[j] ? kept[row[j] + k] - lo : -1;
+                    x[j][e] = k < to[j] ? w[row[j] + k] : 0.0f;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kSumQueries; ++j) {
                 // an entry that occurs twice in a query adds the same weight
                 // twice: the order of the two does not matter
-                if (at >= lo && at < hi) atomicAdd(&s[at - lo], w[row + k]);
+#pragma unroll
+                for (int e = 0; e < kSumEntries; ++e)
+                    if (at[j][e] >= 0 && at[j][e] < kSumRange) atomicAdd(&s[at[j][e]], x[j][e]);
+                for (int32_t k = from[j] + 32 * kSumEntries + lane; k < to[j]; k += 32) {
+                    const int32_t a = kept[row[j] + k] - lo;
+                    if (a >= 0 && a < kSumRange) atomicAdd(&s[a], w[row[j] + k]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
     }
-    const int64_t base = (int64_t)b * ld_acc;
-    for (int32_t i = lo + lane; i < hi; i += 32) {
-        const float old = acc_in != nullptr ? decay * acc_in[base + i] : 0.0f;
-        acc_out[base + i] = old + s[i - lo];
+    if (lane == 0) used[warp] = cleared;
+    __syncthreads();
+    float total[kSumRange / kSumThreads] = {};
+#pragma unroll
+    for (int v = 0; v < kSumWarps; ++v) {
+        if (!used[v]) continue;
+#pragma unroll
+        for (int i = 0; i < kSumRange / kSumThreads; ++i)
+            total[i] += sums[v][i * kSumThreads + tid];
+    }
+#pragma unroll
+    for (int i = 0; i < kSumRange / kSumThreads; ++i) {
+        const int32_t at = lo + i * kSumThreads + tid;
+        if (at < hi)
+            acc_out[base + at] = (acc_in != nullptr ? decay * old[i] : 0.0f) + total[i];
     }
 }
 
@@ -532,17 +585,21 @@ weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld
 
 int32_t weights_ld(int32_t top_k) { return (int32_t)round_up(top_k > 0 ? top_k : 1, kTile); }
 
+int32_t weights_starts_ld(int32_t max_visible) {
+    return (int32_t)ceil_div(max_visible > 0 ? max_visible : 1, kSumRange) + 1;
+}
+
 cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, int32_t top_k,
                                       const float *lse, const float *acc_in, float decay,
                                       float *acc_out, int64_t ld_acc, int32_t *rows,
-                                      int32_t *kept, int32_t *n_valid, int32_t *ascending,
-                                      float *w, cudaStream_t s) {
-    const int32_t ld = weights_ld(top_k);
+                                      int32_t *kept, int32_t *n_valid, int32_t *starts, float *w,
+                                      cudaStream_t s) {
+    const int32_t ld = weights_ld(top_k), ld_starts = weights_starts_ld(p.max_visible);
     cudaError_t e;
     if (p.n_q > 0) {
         count_launch();
         e = launch_pdl(weights_rows_kernel, dim3((unsigned)p.n_q), dim3(kRowsThreads), 0, s, p, idx,
-                       top_k, ld, rows, kept, n_valid, ascending);
+                       top_k, ld, ld_starts, rows, kept, n_valid, starts);
         if (e != cudaSuccess) return e;
         e = weights_mma_supported(p)
                 ? launch_weights_mma(p, lse, top_k, ld, rows, n_valid, w, s)
@@ -550,12 +607,12 @@ cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, i
         if (e != cudaSuccess) return e;
     }
     const int64_t limit = std::min(ld_acc, (int64_t)p.max_pages * 64);
-    const int64_t chunks = ceil_div(limit, kSumWarps * kSumRange);
+    const int64_t chunks = ceil_div(limit, kSumRange);
     count_launch();
-    return launch_pdl(weights_sum_kernel, dim3((unsigned)(chunks * p.batch)), dim3(32 * kSumWarps),
-                      0, s, p, (int32_t)chunks, (int32_t)limit, ld, (const int32_t *)kept,
-                      (const int32_t *)n_valid, (const int32_t *)ascending, (const float *)w,
-                      acc_in, decay, acc_out, ld_acc);
+    return launch_pdl(weights_sum_kernel, dim3((unsigned)(chunks * p.batch)), dim3(kSumThreads), 0,
+                      s, p, (int32_t)chunks, (int32_t)limit, ld, ld_starts, (const int32_t *)kept,
+                      (const int32_t *)n_valid, (const int32_t *)starts, (const float *)w, acc_in,
+                      decay, acc_out, ld_acc);
 }
 
 }  // namespace sa
