@@ -150,9 +150,9 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
 // each range of positions begins in it, a weights kernel writes one weight per
 // kept entry (w, same layout), and the sum kernel adds them to the sequences'
 // rows.  Leading dimension of rows, kept and w: weights_ld(K); of starts:
-// weights_starts_ld(max_visible).
+// weights_starts_ld(n_q, batch, max_visible).
 int32_t weights_ld(int32_t top_k);
-int32_t weights_starts_ld(int32_t max_visible);
+int32_t weights_starts_ld(int32_t n_q, int32_t batch, int32_t max_visible);
 cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, int32_t top_k,
                                       const float *lse, const float *acc_in, float decay,
                                       float *acc_out, int64_t ld_acc, int32_t *rows,
@@ -223,17 +223,58 @@ __device__ __forceinline__ float kv_value(const PathParams &p, int64_t row, int 
 // Physical cache rows of query t's selected positions sel[0, K): list order,
 // -1 entries dropped, out-of-range positions and bad page ids skipped and
 // reported; then padded with the first row up to a multiple of `tile`.
-// Writes rows[0, padded) and *n_valid, and with `kept` the positions behind
-// rows[0, *n_valid).  Called by every thread of a CTA (blockDim.x a multiple
-// of 32); `scratch` is shared memory of kCompactScratch ints.
-//
-// A thread takes four entries of a step (one of each quarter), whose loads are
-// all in flight at once; one scan over the warps' counts places them.
-constexpr int kCompactScratch = 4 * 32 + 2;
+// Writes rows[0, padded) and *n_valid.  Called by every thread of a CTA
+// (blockDim.x a multiple of 32); `scratch` is shared memory of 33 ints.
 __device__ __forceinline__ void compact_rows(const PathParams &p, int32_t t, const int32_t *sel,
                                              int32_t K, int32_t tile, int32_t *rows,
-                                             int32_t *n_valid, int32_t *scratch,
-                                             int32_t *kept = nullptr) {
+                                             int32_t *n_valid, int32_t *scratch) {
+    const int nwarps = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int32_t V = visible_len(p, t);
+    const int32_t seq = __ldg(p.q_seq + t);
+    int32_t base = 0;
+    for (int32_t r0 = 0; r0 < K; r0 += blockDim.x) {
+        const int32_t k = r0 + threadIdx.x;
+        const int32_t s = k < K ? sel[k] : -1;
+        int32_t v = -1;
+        if (s >= V) {
+            report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_INDEX);
+        } else if (s >= 0) {
+            const int64_t row = phys_row(p.page_table, p.max_pages, p.num_pages, seq, s);
+            if (row < 0) report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+            else v = static_cast<int32_t>(row);
+        }
+        const unsigned bal = __ballot_sync(0xffffffffu, v >= 0);
+        if (lane == 0) scratch[w] = __popc(bal);
+        __syncthreads();
+        int32_t off = base, tot = 0;
+        for (int i = 0; i < nwarps; ++i) {
+            if (i < w) off += scratch[i];
+            tot += scratch[i];
+        }
+        const int32_t pos = off + __popc(bal & ((1u << lane) - 1u));
+        if (v >= 0) {
+            rows[pos] = v;
+            if (pos == 0) scratch[32] = v;
+        }
+        __syncthreads();
+        base += tot;
+    }
+    const int32_t padded = (base + tile - 1) / tile * tile;
+    if (base > 0)
+        for (int32_t c = base + threadIdx.x; c < padded; c += blockDim.x) rows[c] = scratch[32];
+    if (threadIdx.x == 0) *n_valid = base;
+}
+
+// compact_rows for the kernels that do nothing else: a thread takes four
+// entries of a step (one of each quarter), whose loads are all in flight at
+// once, and one scan over the warps' counts places them (2048 entries by 512
+// threads: 9 instead of 11 us with cold caches).  With `kept` it also writes
+// the positions behind rows[0, *n_valid).  `scratch`: kCompactScratch ints.
+constexpr int kCompactScratch = 4 * 32 + 2;
+__device__ __forceinline__ void compact_selection(const PathParams &p, int32_t t,
+                                                  const int32_t *sel, int32_t K, int32_t tile,
+                                                  int32_t *rows, int32_t *n_valid,
+                                                  int32_t *scratch, int32_t *kept = nullptr) {
     const int nwarps = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t seq = __ldg(p.q_seq + t);
     const bool seq_ok = seq >= 0 && seq < p.batch;

@@ -102,7 +102,7 @@ struct SfaArgs {
     float *lse_part;         // [n_q, splits, 128]      (splits > 1)
 };
 
-// Query t's selected positions -> physical cache rows (compact_rows): one
+// Query t's selected positions -> physical cache rows (compact_selection): one
 // CTA per query.  The fused decode path gets the rows from the top-K kernel.
 constexpr int kRowsThreads = 512;
 __global__ void __launch_bounds__(kRowsThreads)
@@ -112,8 +112,8 @@ sfa_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, 
     pdl_trigger();
     __shared__ int32_t scratch[kCompactScratch];
     const int t = blockIdx.x;
-    compact_rows(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld_rows,
-                 n_valid_out + t, scratch);
+    compact_selection(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld_rows,
+                      n_valid_out + t, scratch);
 }
 
 template <int kKv>  // sa_dtype of the latent cache

@@ -546,7 +546,7 @@ topk_finalize_kernel(const float *__restrict__ scores, int64_t ld, const int32_t
     pdl_trigger();
     extern __shared__ uint64_t fin_smem[];
     __shared__ unsigned dh[1024];
-    __shared__ int warp_sums[kCompactScratch];
+    __shared__ int warp_sums[33];
     __shared__ int slot_s[kMaxChunks], bbase_s[kMaxChunks], bcount_s[kMaxChunks];
     const int t = blockIdx.x, tid = threadIdx.x;
     const int32_t V = vis[t];
@@ -695,7 +695,7 @@ topk_single_kernel(const float *__restrict__ scores, int64_t ld, const int32_t *
     uint32_t *bits = reinterpret_cast<uint32_t *>(single_smem + kSingleCap);  // [V / 32]
     int32_t *pt = reinterpret_cast<int32_t *>(bits + kSingleMaxV / 32);       // [V / 64]
     __shared__ unsigned dh[1024];
-    __shared__ int warp_sums[kCompactScratch];
+    __shared__ int warp_sums[33];
     __shared__ int bstar_s, above_s;
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31;
     const int32_t V = vis[t];

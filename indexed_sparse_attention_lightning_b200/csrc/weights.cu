@@ -19,36 +19,49 @@ namespace sa {
 namespace {
 using namespace sfa;
 
-constexpr int kSumRange = 1024;  // positions per CTA of the sum kernel
+// The sum kernel's shape: positions per CTA, warps, and queries that a warp looks
+// up at a time.
+template <int R, int W, int G>
+struct SumShape {
+    static constexpr int kRange = R, kWarps = W, kGroup = G;
+};
+// Few queries a sequence (a decode step has one): many small CTAs, one wave of
+// them for 64 sequences of 32K.  Many (a prompt's last queries): more warps share
+// the queries of a smaller range.
+using SumFew = SumShape<1024, 2, 32>;
+using SumMany = SumShape<256, 32, 8>;
+static_assert(SumFew::kRange == 1 << 10 && SumMany::kRange == 1 << 8, "range_log2 below");
+bool sum_many(int32_t n_q, int32_t batch) { return n_q > 16 * (int64_t)batch; }
 
 // ------------------------------------------------------------------- rows ---
-// starts[t, c] = first kept entry of query t at or past position c * kSumRange
+// starts[t, c] = first kept entry of query t at or past position c * range
 // (the last column: all of them); starts[t, 0] = -1 where the kept positions
-// do not ascend.
+// do not ascend strictly.
 constexpr int kRowsThreads = 512;
 __global__ void __launch_bounds__(kRowsThreads)
 weights_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, int32_t ld,
-                    int32_t ld_starts, int32_t *rows, int32_t *kept, int32_t *n_valid,
-                    int32_t *starts) {
+                    int32_t ld_starts, int32_t range_log2, int32_t *rows, int32_t *kept,
+                    int32_t *n_valid, int32_t *starts) {
     pdl_wait();
     pdl_trigger();
     __shared__ int32_t scratch[kCompactScratch];
     __shared__ int32_t n_s;
     const int t = blockIdx.x;
     int32_t *pos = kept + (int64_t)t * ld;
-    compact_rows(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld, &n_s, scratch, pos);
+    compact_selection(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld, &n_s, scratch,
+                      pos);
     __syncthreads();
     const int32_t n = n_s;
     int32_t *st = starts + (int64_t)t * ld_starts;
     int32_t falls = 0;
     for (int32_t i = threadIdx.x; i <= n; i += kRowsThreads) {
         const int32_t at = i < n ? pos[i] : -1, before = i > 0 ? pos[i - 1] : -1;
-        if (i > 0 && i < n && before > at) {
+        if (i > 0 && i < n && before >= at) {
             falls = 1;
             continue;
         }
-        const int32_t c0 = i > 0 ? before / kSumRange + 1 : 0;
-        const int32_t c1 = i < n ? at / kSumRange : ld_starts - 1;
+        const int32_t c0 = i > 0 ? (before >> range_log2) + 1 : 0;
+        const int32_t c1 = i < n ? at >> range_log2 : ld_starts - 1;
         for (int32_t c = c0; c <= c1; ++c) st[c] = i;
     }
     falls = __syncthreads_or(falls);
@@ -134,10 +147,12 @@ cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t l
 //               before the wait on the rows kernel), then issues the MMAs;
 //   warps 1-7   gather the rows (sfa_gather.cuh; warp 12 too for a 4-bit latent);
 //   warps 8-11  move Q into TMEM (warp 8 + j: heads 32j .. 32j + 31, one per
-//               lane), then read S: thread = head, 64 keys, exp2 of the logits
-//               minus its head's lse, summed over the 32 heads of the warp by
-//               halving exchanges (62 shuffles leave each lane two keys) and
-//               over the four warps through shared memory, in a fixed order.
+//               lane), then read S with 16-lane loads, so that a thread holds
+//               four heads of sixteen keys: exp2 of the logits minus the heads'
+//               lse, summed over the thread's heads, over the eight lanes of the
+//               same keys by halving exchanges (14 shuffles; one head per lane
+//               would take 62) and over the four warps through shared memory,
+//               all in a fixed order.
 // All waits are bounded; a timeout is reported in the workspace status word.
 // An e4m3 latent value is code x fp32 scale, 24 significant bits: rounded to one
 // bf16 its logits, and with them the fp32 weights, would be off by 2^-9 of
@@ -163,12 +178,13 @@ struct WeightsSmem {
 };
 static_assert(sizeof(WeightsSmem) + 1024 <= 232448, "shared memory budget of one CTA");
 
-// Sums v[i] over the warp's lanes: afterwards v[0 .. N/32) hold the totals of
-// entries N/32 * (lane read with its bits reversed) and those behind it.
+// Sums v[i] over the eight lanes that differ in bits 2-4: each gives half of
+// its sums away and keeps the other, three times.  Afterwards v[0 .. N/8) hold
+// the totals of entries N/8 * sum_block(lane) and those behind.
 template <int N>
-__device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
+__device__ __forceinline__ void octet_sums(float (&v)[N], int lane) {
 #pragma unroll
-    for (int half = N / 2, bit = 1; bit < 32; half >>= 1, bit <<= 1) {
+    for (int half = N / 2, bit = 4; bit < 32; half >>= 1, bit <<= 1) {
         const bool up = (lane & bit) != 0;
 #pragma unroll
         for (int i = 0; i < half; ++i) {
@@ -177,6 +193,9 @@ __device__ __forceinline__ void lane_sums(float (&v)[N], int lane) {
             v[i] = keep + __shfl_xor_sync(0xffffffffu, send, bit);
         }
     }
+}
+__device__ __forceinline__ int sum_block(int lane) {
+    return (lane & 4) | ((lane >> 2) & 2) | ((lane >> 4) & 1);
 }
 
 // Row producers of an e4m3 latent: tiles of 32 keys as 64 rows (see kKeysOf).
@@ -341,44 +360,59 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
             if (lane == 0) mbar_arrive(&sm.q_ready);  // also frees ring stages 1 and 2
         }
         const float sl2 = p.sm_scale * kLog2e;
-        const float l = T > 0 ? __ldg(lse + (int64_t)t * kHeads + h) : 0.f;
-        // nothing selected for this head: it adds nothing
-        const float minus = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        // this thread's heads in S: 32j + lane / 4 + 8i; one with nothing selected
+        // (lse = -inf) adds nothing
+        float minus[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float l =
+                T > 0 ? __ldg(lse + (int64_t)t * kHeads + 32 * j + (lane >> 2) + 8 * i) : 0.f;
+            minus[i] = l == -INFINITY ? -INFINITY : -l * kLog2e;
+        }
         float *wt = w + (int64_t)t * ld + (int64_t)j0 * kKeys;
-        const int e = static_cast<int>(__brev(static_cast<unsigned>(lane)) >> 27);
+        const int block = sum_block(lane), q2 = 2 * (lane & 3);
         // After a failed wait the loop keeps going without waiting or touching
         // TMEM, so that the warps still meet at the named barrier.
         for (int n = 0; n < T; ++n) {
             const int sb = n & 1;
             if (ok) ok = warp_wait(&sm.s_full[sb], (n >> 1) & 1, abort_flag, status);
-            float v[kKeys];
+            // v[2r + e]: key 8r + 2 (lane % 4) + e, over this thread's four heads
+            constexpr int kSums = kKeys / 4;
+            float v[kSums];
             if (ok) {
                 tc_fence_after();
-                float a[32], b[32];
-                tmem_ld32(tmem + lanes + kWColS + kTile * sb, a);
-                tmem_ld32(tmem + lanes + kWColS + kTile * sb + 32, b);
+                uint32_t a[32], b[32];
+                tmem_ld_16x256b_x8(tmem + lanes + kWColS + kTile * sb, a);
+                tmem_ld_16x256b_x8(tmem + lanes + (16u << 16) + kWColS + kTile * sb, b);
                 tmem_wait_ld_keep(a);
                 tmem_wait_ld_keep(b);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if constexpr (kKeys == 32) {
-                        v[i] = ex2(fmaf(a[i] + b[i], sl2, minus));
-                    } else {
-                        v[i] = ex2(fmaf(a[i], sl2, minus));
-                        v[32 + i] = ex2(fmaf(b[i], sl2, minus));
+                for (int i = 0; i < kSums; ++i) {
+                    float z[4];  // column i of the four heads
+#pragma unroll
+                    for (int h4 = 0; h4 < 4; ++h4) {
+                        const uint32_t *s = h4 < 2 ? a : b;
+                        const int at = 4 * (i >> 1) + (i & 1) + 2 * (h4 & 1);
+                        z[h4] = __uint_as_float(s[at]);
+                        if constexpr (kKeys == 32) z[h4] += __uint_as_float(s[at + 16]);
                     }
+                    v[i] = (ex2(fmaf(z[0], sl2, minus[0])) + ex2(fmaf(z[1], sl2, minus[1]))) +
+                           (ex2(fmaf(z[2], sl2, minus[2])) + ex2(fmaf(z[3], sl2, minus[3])));
                 }
             } else {
 #pragma unroll
-                for (int i = 0; i < kKeys; ++i) v[i] = 0.f;
+                for (int i = 0; i < kSums; ++i) v[i] = 0.f;
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.s_empty[sb]);
-            lane_sums(v, lane);
+            octet_sums(v, lane);
             float *part = sm.part[sb][j];
-#pragma unroll
-            for (int i = 0; i < kKeys / 32; ++i) part[kKeys / 32 * e + i] = v[i];
+            if constexpr (kKeys == 32) {
+                part[8 * (block >> 1) + q2 + (block & 1)] = v[0];
+            } else {
+                *reinterpret_cast<float2 *>(part + 8 * block + q2) = make_float2(v[0], v[1]);
+            }
             // one barrier a tile: the other parity's sums are read before it
             named_barrier(1, 128);
             const int k = 32 * j + lane;  // the first warps finish one key per lane
@@ -473,16 +507,15 @@ cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t to
 
 // -------------------------------------------------------------------- sum ---
 // One CTA per range of a sequence's positions.  Warp w walks query groups w,
-// w + 8, ... of 32: its lanes look the queries' entries in the range up, then
+// w + kWarps, ...: its lanes look the queries' entries in the range up, then
 // the entries are added to the warp's own sums in shared memory, one query
 // after another (four queries' loads in flight).  The warps' sums are added in
 // the order of w at the end.
-constexpr int kSumWarps = 8;
-constexpr int kSumThreads = 32 * kSumWarps;
 constexpr int kSumQueries = 4;  // queries whose entries are loaded together
 constexpr int kSumEntries = 2;  // of each, 32 entries this many times; the rest follow one by one
 
-__global__ void __launch_bounds__(kSumThreads)
+template <typename Shape>
+__global__ void __launch_bounds__(32 * Shape::kWarps)
 weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld,
                    int32_t ld_starts, const int32_t *__restrict__ kept,
                    const int32_t *__restrict__ n_valid, const int32_t *__restrict__ starts,
@@ -490,6 +523,8 @@ weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld
                    int64_t ld_acc) {
     pdl_wait();
     pdl_trigger();
+    constexpr int kSumRange = Shape::kRange, kSumWarps = Shape::kWarps;
+    constexpr int kSumThreads = 32 * kSumWarps;
     __shared__ float sums[kSumWarps][kSumRange];
     __shared__ int32_t used[kSumWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -503,28 +538,32 @@ weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld
     if (lo >= len) return;
     const int32_t hi = min(len, lo + kSumRange);
     const int64_t base = (int64_t)b * ld_acc;
-    float old[kSumRange / kSumThreads];  // on its way while the entries are added
+    constexpr int kPer = (kSumRange + kSumThreads - 1) / kSumThreads;
+    float old[kPer];  // on its way while the entries are added
 #pragma unroll
-    for (int i = 0; i < kSumRange / kSumThreads; ++i) {
+    for (int i = 0; i < kPer; ++i) {
         const int32_t at = lo + i * kSumThreads + tid;
         old[i] = acc_in != nullptr && at < hi ? acc_in[base + at] : 0.0f;
     }
     float *s = sums[warp];
     bool cleared = false;
-    for (int32_t t0 = 32 * warp; t0 < p.n_q; t0 += 32 * kSumWarps) {
-        const int32_t t = t0 + lane;
+    for (int32_t t0 = Shape::kGroup * warp; t0 < p.n_q; t0 += Shape::kGroup * kSumWarps) {
+        const int32_t t = lane < Shape::kGroup ? t0 + lane : p.n_q;
         int32_t k0 = 0, k1 = 0;
+        bool plain = true;
         if (t < p.n_q && p.q_seq[t] == b) {
             // a query sees fewer positions than the sequence has when others follow
             const int32_t *st = starts + (int64_t)t * ld_starts;
             k0 = st[min(c, ld_starts - 1)];
             k1 = st[min(c + 1, ld_starts - 1)];
-            if (st[0] < 0) {  // not ascending: look at all of them
+            if (st[0] < 0) {  // in no order, or with repeats: look at all of them
+                plain = false;
                 k0 = 0;
                 k1 = n_valid[t];
             }
         }
         uint32_t todo = __ballot_sync(0xffffffffu, k1 > k0);
+        const uint32_t distinct = __ballot_sync(0xffffffffu, plain);
         if (todo != 0 && !cleared) {
             for (int i = lane; i < kSumRange; i += 32) s[i] = 0.0f;
             __syncwarp();
@@ -534,9 +573,11 @@ weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld
             int32_t at[kSumQueries][kSumEntries], from[kSumQueries], to[kSumQueries];
             float x[kSumQueries][kSumEntries];
             int64_t row[kSumQueries];
+            bool once[kSumQueries];  // the query's positions are distinct
 #pragma unroll
             for (int j = 0; j < kSumQueries; ++j) {
                 const int u = todo != 0 ? __ffs(todo) - 1 : 0;
+                once[j] = (distinct >> u) & 1u;
                 from[j] = __shfl_sync(0xffffffffu, k0, u);
                 to[j] = todo != 0 ? __shfl_sync(0xffffffffu, k1, u) : from[j];
                 row[j] = (int64_t)(t0 + u) * ld;
@@ -550,43 +591,61 @@ weights_sum_kernel(const PathParams p, int32_t chunks, int32_t limit, int32_t ld
             }
 #pragma unroll
             for (int j = 0; j < kSumQueries; ++j) {
-                // an entry that occurs twice in a query adds the same weight
-                // twice: the order of the two does not matter
+                // entries that repeat a position add the same weight each: their
+                // order does not matter
+                auto add = [&](int32_t a, float y) {
+                    if (a < 0 || a >= kSumRange) return;
+                    if (once[j]) s[a] += y;
+                    else atomicAdd(&s[a], y);
+                };
 #pragma unroll
-                for (int e = 0; e < kSumEntries; ++e)
-                    if (at[j][e] >= 0 && at[j][e] < kSumRange) atomicAdd(&s[at[j][e]], x[j][e]);
-                for (int32_t k = from[j] + 32 * kSumEntries + lane; k < to[j]; k += 32) {
-                    const int32_t a = kept[row[j] + k] - lo;
-                    if (a >= 0 && a < kSumRange) atomicAdd(&s[a], w[row[j] + k]);
-                }
+                for (int e = 0; e < kSumEntries; ++e) add(at[j][e], x[j][e]);
+                for (int32_t k = from[j] + 32 * kSumEntries + lane; k < to[j]; k += 32)
+                    add(kept[row[j] + k] - lo, w[row[j] + k]);
                 __syncwarp();
             }
         }
     }
     if (lane == 0) used[warp] = cleared;
     __syncthreads();
-    float total[kSumRange / kSumThreads] = {};
-#pragma unroll
+    float total[kPer] = {};
+#pragma unroll 8
     for (int v = 0; v < kSumWarps; ++v) {
         if (!used[v]) continue;
 #pragma unroll
-        for (int i = 0; i < kSumRange / kSumThreads; ++i)
-            total[i] += sums[v][i * kSumThreads + tid];
+        for (int i = 0; i < kPer; ++i) {
+            const int at = i * kSumThreads + tid;
+            if (at < kSumRange) total[i] += sums[v][at];
+        }
     }
 #pragma unroll
-    for (int i = 0; i < kSumRange / kSumThreads; ++i) {
+    for (int i = 0; i < kPer; ++i) {
         const int32_t at = lo + i * kSumThreads + tid;
         if (at < hi)
             acc_out[base + at] = (acc_in != nullptr ? decay * old[i] : 0.0f) + total[i];
     }
 }
 
+template <typename Shape>
+cudaError_t launch_weights_sum(const PathParams &p, int32_t ld, int32_t ld_starts,
+                               const int32_t *kept, const int32_t *n_valid,
+                               const int32_t *starts, const float *w, const float *acc_in,
+                               float decay, float *acc_out, int64_t ld_acc, cudaStream_t s) {
+    const int64_t limit = std::min(ld_acc, (int64_t)p.max_pages * 64);
+    const int64_t chunks = ceil_div(limit, Shape::kRange);
+    count_launch();
+    return launch_pdl(weights_sum_kernel<Shape>, dim3((unsigned)(chunks * p.batch)),
+                      dim3(32 * Shape::kWarps), 0, s, p, (int32_t)chunks, (int32_t)limit, ld,
+                      ld_starts, kept, n_valid, starts, w, acc_in, decay, acc_out, ld_acc);
+}
+
 }  // namespace
 
 int32_t weights_ld(int32_t top_k) { return (int32_t)round_up(top_k > 0 ? top_k : 1, kTile); }
 
-int32_t weights_starts_ld(int32_t max_visible) {
-    return (int32_t)ceil_div(max_visible > 0 ? max_visible : 1, kSumRange) + 1;
+int32_t weights_starts_ld(int32_t n_q, int32_t batch, int32_t max_visible) {
+    const int32_t range = sum_many(n_q, batch) ? SumMany::kRange : SumFew::kRange;
+    return (int32_t)ceil_div(max_visible > 0 ? max_visible : 1, range) + 1;
 }
 
 cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, int32_t top_k,
@@ -594,25 +653,24 @@ cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, i
                                       float *acc_out, int64_t ld_acc, int32_t *rows,
                                       int32_t *kept, int32_t *n_valid, int32_t *starts, float *w,
                                       cudaStream_t s) {
-    const int32_t ld = weights_ld(top_k), ld_starts = weights_starts_ld(p.max_visible);
+    const bool many = sum_many(p.n_q, p.batch);
+    const int32_t ld = weights_ld(top_k);
+    const int32_t ld_starts = weights_starts_ld(p.n_q, p.batch, p.max_visible);
     cudaError_t e;
     if (p.n_q > 0) {
         count_launch();
         e = launch_pdl(weights_rows_kernel, dim3((unsigned)p.n_q), dim3(kRowsThreads), 0, s, p, idx,
-                       top_k, ld, ld_starts, rows, kept, n_valid, starts);
+                       top_k, ld, ld_starts, many ? 8 : 10, rows, kept, n_valid, starts);
         if (e != cudaSuccess) return e;
         e = weights_mma_supported(p)
                 ? launch_weights_mma(p, lse, top_k, ld, rows, n_valid, w, s)
                 : launch_weights_simt(p, lse, ld, rows, n_valid, w, s);
         if (e != cudaSuccess) return e;
     }
-    const int64_t limit = std::min(ld_acc, (int64_t)p.max_pages * 64);
-    const int64_t chunks = ceil_div(limit, kSumRange);
-    count_launch();
-    return launch_pdl(weights_sum_kernel, dim3((unsigned)(chunks * p.batch)), dim3(kSumThreads), 0,
-                      s, p, (int32_t)chunks, (int32_t)limit, ld, ld_starts, (const int32_t *)kept,
-                      (const int32_t *)n_valid, (const int32_t *)starts, (const float *)w, acc_in,
-                      decay, acc_out, ld_acc);
+    return many ? launch_weights_sum<SumMany>(p, ld, ld_starts, kept, n_valid, starts, w, acc_in,
+                                              decay, acc_out, ld_acc, s)
+                : launch_weights_sum<SumFew>(p, ld, ld_starts, kept, n_valid, starts, w, acc_in,
+                                             decay, acc_out, ld_acc, s);
 }
 
 }  // namespace sa
