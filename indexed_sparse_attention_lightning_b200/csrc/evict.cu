@@ -4,13 +4,15 @@
 // Of a sequence of n > budget tokens the first F, the last R and, between
 // them, the budget - F - R positions with the largest acc stay (ties to the
 // lower position).  Two kernels:
-//   select  finds the threshold of the middle part exactly by a radix select on
-//           order-preserving keys and lists the kept positions in ascending
-//           order with their physical rows;
+//   select  one cluster of eight CTAs per sequence, each holding an eighth of
+//           its positions: the threshold of the middle part by an exact radix
+//           select on order-preserving keys (11 + 11 + 10 bits; the CTAs'
+//           histograms are added through distributed shared memory), then the
+//           kept positions in ascending order with their physical rows;
 //   move    copies each kept token's index key, latent row and scales byte for
 //           byte to its place in the destination pages.
-// Both are bound by memory: select reads acc, move reads and writes the kept
-// rows.
+// Both are bound by memory: select reads acc (five times, from L2 after the
+// first), move reads and writes the kept rows.
 #include "evict.h"
 
 #include <algorithm>
@@ -22,6 +24,9 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kSelectCtas = 8;   // of a cluster: one sequence
+constexpr int kSelectBins = 2048;
+constexpr int kSelectLoads = 8;  // of a lane in flight
 constexpr int kMoveThreads = 256;
 constexpr int kMaxFields = 5;
 
@@ -58,17 +63,62 @@ __device__ __forceinline__ uint32_t keep_key(float a) {
     return a != a ? 0xFFFFFFFFu : order_key(a);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+__device__ __forceinline__ int cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return static_cast<int>(r);
+}
+// A word of shared memory of the cluster's CTA `rank`, at this CTA's address `p`.
+__device__ __forceinline__ int32_t peer_word(const int32_t *p, int rank) {
+    uint32_t at;
+    int32_t v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                 : "=r"(at)
+                 : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(p))), "r"(rank));
+    asm volatile("ld.shared::cluster.b32 %0, [%1];" : "=r"(v) : "r"(at) : "memory");
+    return v;
+}
+
+// Visits positions [w0, w1) of a warp: f(i, key, in_range) with the warp's 32
+// lanes at consecutive positions, kSelectLoads loads in flight.
+template <typename F>
+__device__ __forceinline__ void for_keys(const float *acc, int32_t w0, int32_t w1, int lane, F f) {
+    for (int32_t i0 = w0; i0 < w1; i0 += 32 * kSelectLoads) {
+        float x[kSelectLoads];
+#pragma unroll
+        for (int u = 0; u < kSelectLoads; ++u) {
+            const int32_t i = i0 + 32 * u + lane;
+            x[u] = i < w1 ? acc[i] : 0.0f;
+        }
+#pragma unroll
+        for (int u = 0; u < kSelectLoads; ++u) {
+            const int32_t i = i0 + 32 * u + lane;
+            if (i0 + 32 * u < w1) f(i, keep_key(x[u]), i < w1, x[u]);
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a) {
-    __shared__ int32_t hist[256];
-    __shared__ int32_t scratch[2 * kSelectWarps];
+    pdl_trigger();
+    __shared__ int32_t hist[3][kSelectBins];
+    __shared__ int32_t scan[kSelectWarps];
+    __shared__ int32_t gt_s[kSelectWarps], eq_s[kSelectWarps];
+    __shared__ int32_t totals[2];  // this CTA's entries above the threshold, and on it
     __shared__ int32_t pick[2];
-    const int b = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int b = blockIdx.x / kSelectCtas, rank = cluster_rank();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t n = a.src_len[b];
     const float *acc = a.acc + (int64_t)b * a.ld_acc;
     const int32_t *st = a.src_table + (int64_t)b * a.src_max_pages;
     const int32_t *dt = a.dst_table + (int64_t)b * a.dst_max_pages;
     const int64_t out0 = (int64_t)b * a.budget;
+    for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
 
+    // every CTA checks the whole sequence, so that all take the same way
     const bool fits = n >= 0 && n <= (int64_t)a.src_max_pages * 64 && n <= a.ld_acc;
     int32_t bad = 0;
     if (fits) {
@@ -79,121 +129,249 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             bad |= dt[i] < 0 || dt[i] >= a.dst_pages;
     }
     bad = __syncthreads_or(bad);
-    if (tid == 0 && !fits) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
-    if (tid == 0 && bad) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+    if (tid == 0 && rank == 0) {
+        if (!fits) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
+        if (bad) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+    }
     const int32_t len = fits && !bad ? n : 0;
     const int32_t kept = min(len, a.budget);
 
     // the middle part [lo, hi) keeps its `want` largest keys: all above the
-    // threshold and the first `ties` equal to it
-    int32_t lo = 0, hi = 0, want = 0;
-    if (len > a.budget) {
-        lo = a.first;
-        hi = len - a.last;
-        want = a.budget - a.first - a.last;
-    }
+    // threshold and the first `ties` on it
+    const bool shrink = len > a.budget;
+    const int32_t lo = shrink ? a.first : 0, hi = shrink ? len - a.last : 0;
+    const int32_t want = shrink ? a.budget - a.first - a.last : 0;
+    // this warp's positions, whole 32s of the sequence
+    const int32_t warps = kSelectCtas * kSelectWarps;
+    const int32_t per = (int32_t)round_up(ceil_div(len, warps), 32);
+    const int64_t w0l = (int64_t)(rank * kSelectWarps + warp) * per;
+    const int32_t w0 = (int32_t)min(w0l, (int64_t)len), w1 = (int32_t)min(w0l + per, (int64_t)len);
+    const int32_t m0 = max(w0, lo), m1 = min(w1, hi);
+
     uint32_t threshold = 0xFFFFFFFFu;
     int32_t ties = 0;
     if (want > 0) {
+        const uint32_t zero_key = keep_key(0.0f);
         uint32_t prefix = 0, mask = 0;
         int32_t left = want;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            for (int i = tid; i < 256; i += kSelectThreads) hist[i] = 0;
-            __syncthreads();
-            for (int32_t i = lo + tid; i < hi; i += kSelectThreads) {
-                const uint32_t k = keep_key(acc[i]);
-                if ((k & mask) == prefix) atomicAdd(&hist[(k >> shift) & 255u], 1);
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            const uint32_t digits = pass < 2 ? 0x7FFu : 0x3FFu;
+            int32_t *h = hist[pass];
+            // positions that never received weight share one key: they are
+            // counted in registers, not by colliding atomics
+            int32_t zeros = 0;
+            for_keys(acc, m0, m1, lane, [&](int32_t, uint32_t k, bool in, float) {
+                if (!in || (k & mask) != prefix) return;
+                if (k == zero_key) ++zeros;
+                else atomicAdd(&h[(k >> shift) & digits], 1);
+            });
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) zeros += __shfl_xor_sync(0xffffffffu, zeros, o);
+            if (lane == 0 && zeros > 0) atomicAdd(&h[(zero_key >> shift) & digits], zeros);
+            cluster_sync();
+            // the sequence's histogram, two bins a thread from the top, and the
+            // bin in which the `left`-th largest key lies
+            int32_t c0 = 0, c1 = 0;
+            const int d0 = kSelectBins - 1 - 2 * tid, d1 = d0 - 1;
+#pragma unroll
+            for (int r = 0; r < kSelectCtas; ++r) {
+                c0 += peer_word(&h[d0], r);
+                c1 += peer_word(&h[d1], r);
             }
+            int32_t inc = c0 + c1;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+                if (lane >= o) inc += up;
+            }
+            if (lane == 31) scan[warp] = inc;
             __syncthreads();
-            if (tid == 0) {
-                int32_t above = 0, d = 255;
-                while (d > 0 && above + hist[d] < left) above += hist[d--];
-                pick[0] = d;
+            int32_t above = inc - (c0 + c1);
+            for (int w = 0; w < warp; ++w) above += scan[w];
+            if (above < left && left <= above + c0) {
+                pick[0] = d0;
                 pick[1] = above;
+            } else if (above + c0 < left && left <= above + c0 + c1) {
+                pick[0] = d1;
+                pick[1] = above + c0;
             }
             __syncthreads();
             prefix |= (uint32_t)pick[0] << shift;
-            mask |= 255u << shift;
+            mask |= digits << shift;
             left -= pick[1];
-            __syncthreads();
+            __syncthreads();  // scan and pick are written again
         }
         threshold = prefix;
         ties = left;
     }
 
-    int32_t at = 0, tied = 0;  // kept and tied entries before this step
-    for (int32_t i0 = 0; i0 < len; i0 += kSelectThreads) {
-        const int32_t i = i0 + tid;
-        bool keep = i < len, tie = false;
-        if (keep && i >= lo && i < hi) {
-            const uint32_t k = want > 0 ? keep_key(acc[i]) : 0u;
-            keep = want > 0 && k > threshold;
-            tie = want > 0 && k == threshold;
+    // entries of each warp that stay for certain, and those on the threshold
+    int32_t gt = 0, eq = 0;
+    if (want > 0) {
+        gt = (w1 - w0) - max(0, m1 - m0);  // first and last tokens
+        int32_t above = 0, on = 0;
+        for_keys(acc, m0, m1, lane, [&](int32_t, uint32_t k, bool in, float) {
+            above += in && k > threshold;
+            on += in && k == threshold;
+        });
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            above += __shfl_xor_sync(0xffffffffu, above, o);
+            on += __shfl_xor_sync(0xffffffffu, on, o);
         }
-        const uint32_t tie_bits = __ballot_sync(0xffffffffu, tie);
-        if (lane == 0) scratch[warp] = __popc(tie_bits);
-        __syncthreads();
-        int32_t before = tied, all_ties = 0;
-        for (int w = 0; w < kSelectWarps; ++w) {
-            if (w < warp) before += scratch[w];
-            all_ties += scratch[w];
-        }
-        if (tie) keep = before + __popc(tie_bits & ((1u << lane) - 1u)) < ties;
-        const uint32_t keep_bits = __ballot_sync(0xffffffffu, keep);
-        if (lane == 0) scratch[kSelectWarps + warp] = __popc(keep_bits);
-        __syncthreads();
-        int32_t slot = at, all_keep = 0;
-        for (int w = 0; w < kSelectWarps; ++w) {
-            if (w < warp) slot += scratch[kSelectWarps + w];
-            all_keep += scratch[kSelectWarps + w];
-        }
-        slot += __popc(keep_bits & ((1u << lane) - 1u));
-        if (keep) {
-            a.src_row[out0 + slot] = st[i >> 6] * 64 + (i & 63);
-            if (a.src_pos != nullptr) a.src_pos[out0 + slot] = i;
-            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + slot] = acc[i];
-        }
-        at += all_keep;
-        tied += all_ties;
-        __syncthreads();
+        gt += above;
+        eq = on;
+    } else {
+        gt = (w1 - w0) - max(0, m1 - m0);
     }
+    if (lane == 0) {
+        gt_s[warp] = gt;
+        eq_s[warp] = eq;
+    }
+    __syncthreads();
+    if (warp == 0) {  // exclusive sums over the CTA's warps
+        const int32_t g = gt_s[lane], e = eq_s[lane];
+        int32_t gi = g, ei = e;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t gu = __shfl_up_sync(0xffffffffu, gi, o);
+            const int32_t eu = __shfl_up_sync(0xffffffffu, ei, o);
+            if (lane >= o) {
+                gi += gu;
+                ei += eu;
+            }
+        }
+        gt_s[lane] = gi - g;
+        eq_s[lane] = ei - e;
+        if (lane == 31) {
+            totals[0] = gi;
+            totals[1] = ei;
+        }
+    }
+    cluster_sync();
+    int32_t gt_before = gt_s[warp], eq_before = eq_s[warp];
+    for (int r = 0; r < rank; ++r) {
+        gt_before += peer_word(&totals[0], r);
+        eq_before += peer_word(&totals[1], r);
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+
+    // ascending emission: a warp's entries start behind all earlier ones that stay
+    int32_t on = eq_before;                       // entries on the threshold so far
+    int32_t slot = gt_before + min(on, ties);     // kept entries so far
+    const uint32_t below = (1u << lane) - 1u;
+    for_keys(acc, w0, w1, lane, [&](int32_t i, uint32_t k, bool in, float x) {
+        const bool middle = in && i >= lo && i < hi;
+        const bool tie = middle && want > 0 && k == threshold;
+        const uint32_t tie_bits = __ballot_sync(0xffffffffu, tie);
+        bool keep = in && !middle;
+        if (middle) keep = want > 0 && (k > threshold || (tie && on + __popc(tie_bits & below) < ties));
+        const uint32_t bits = __ballot_sync(0xffffffffu, keep);
+        if (keep) {
+            const int32_t at = slot + __popc(bits & below);
+            a.src_row[out0 + at] = st[i >> 6] * 64 + (i & 63);
+            if (a.src_pos != nullptr) a.src_pos[out0 + at] = i;
+            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = x;
+        }
+        on += __popc(tie_bits);
+        slot += __popc(bits);
+    });
+    const int32_t first = rank * kSelectThreads + tid;
     if (a.src_pos != nullptr)
-        for (int32_t i = kept + tid; i < a.budget; i += kSelectThreads) a.src_pos[out0 + i] = -1;
+        for (int64_t i = (int64_t)kept + first; i < a.budget; i += kSelectCtas * kSelectThreads)
+            a.src_pos[out0 + i] = -1;
     if (a.acc_out != nullptr)
-        for (int64_t i = kept + tid; i < a.ld_out; i += kSelectThreads)
+        for (int64_t i = (int64_t)kept + first; i < a.ld_out; i += kSelectCtas * kSelectThreads)
             a.acc_out[(int64_t)b * a.ld_out + i] = 0.0f;
-    if (tid == 0) {
+    if (first == 0) {
         a.kept[b] = kept;
         a.dst_len[b] = kept;
     }
 }
 
-template <typename T>
-__device__ __forceinline__ void move_row(const EvictField &f, int64_t from, int64_t to, int lane) {
-    const T *src = reinterpret_cast<const T *>(f.src) + from * f.units;
-    T *dst = reinterpret_cast<T *>(f.dst) + to * f.units;
-    for (int i = lane; i < f.units; i += 32) dst[i] = src[i];
-}
-
-// One warp per kept token (grid-stride).
+// One warp moves kMoveRows consecutive kept tokens at a time.  The 16-byte pieces
+// of a token's rows in all pools are dealt to the lanes, kPieces each, and all
+// loads of the tokens are in flight before the first store.
+constexpr int kMoveRows = 4;
+template <int kPieces>
 __global__ void __launch_bounds__(kMoveThreads)
 evict_move_kernel(const EvictArgs a, const EvictFields fields) {
+    pdl_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t rows = (int64_t)a.batch * a.budget;
-    const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
-    for (int64_t r = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); r < rows;
-         r += warps) {
-        const int32_t b = (int32_t)(r / a.budget), i = (int32_t)(r % a.budget);
-        if (i >= a.kept[b]) continue;
-        const int64_t from = a.src_row[r];
-        const int64_t to =
-            (int64_t)a.dst_table[(int64_t)b * a.dst_max_pages + (i >> 6)] * 64 + (i & 63);
+    // this lane's pieces: where they start in row 0 of their pools
+    const uint8_t *src[kPieces];
+    uint8_t *dst[kPieces];
+    int32_t row_bytes[kPieces];
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+        int32_t piece = lane + 32 * j;
+        row_bytes[j] = 0;
         for (int k = 0; k < fields.n; ++k) {
             const EvictField &f = fields.f[k];
-            if (f.unit == 16) move_row<uint4>(f, from, to, lane);
-            else if (f.unit == 4) move_row<uint32_t>(f, from, to, lane);
-            else if (f.unit == 2) move_row<uint16_t>(f, from, to, lane);
-            else move_row<uint8_t>(f, from, to, lane);
+            if (f.unit != 16) continue;
+            if (piece >= 0 && piece < f.units) {
+                src[j] = f.src + piece * 16;
+                dst[j] = f.dst + piece * 16;
+                row_bytes[j] = f.units * 16;
+            }
+            piece -= f.units;
+        }
+    }
+    const int64_t groups = ceil_div(a.budget, kMoveRows);
+    const int64_t all = a.batch * groups;
+    const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
+    for (int64_t g = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); g < all;
+         g += warps) {
+        const int32_t b = (int32_t)(g / groups);
+        const int32_t i0 = (int32_t)(g % groups) * kMoveRows;
+        const int32_t rows = min(a.kept[b] - i0, kMoveRows);
+        if (rows <= 0) continue;
+        int64_t from[kMoveRows], to[kMoveRows];
+#pragma unroll
+        for (int r = 0; r < kMoveRows; ++r) {
+            const int32_t i = i0 + min(r, rows - 1);  // past the end: the last row again
+            from[r] = a.src_row[(int64_t)b * a.budget + i];
+            to[r] = (int64_t)a.dst_table[(int64_t)b * a.dst_max_pages + (i >> 6)] * 64 + (i & 63);
+        }
+        uint4 x[kMoveRows][kPieces];
+#pragma unroll
+        for (int r = 0; r < kMoveRows; ++r)
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j)
+                if (row_bytes[j] > 0)
+                    x[r][j] = __ldcs(
+                        reinterpret_cast<const uint4 *>(src[j] + from[r] * row_bytes[j]));
+#pragma unroll
+        for (int r = 0; r < kMoveRows; ++r)
+#pragma unroll
+            for (int j = 0; j < kPieces; ++j)
+                if (row_bytes[j] > 0 && r < rows)
+                    __stcs(reinterpret_cast<uint4 *>(dst[j] + to[r] * row_bytes[j]), x[r][j]);
+        // rows that are not whole 16-byte pieces: a few small units each
+        for (int k = 0; k < fields.n; ++k) {
+            const EvictField &f = fields.f[k];
+            if (f.unit == 16) continue;
+            for (int32_t u = lane; u < rows * f.units; u += 32) {
+                const int32_t r = u / f.units, c = u % f.units;
+                int64_t s = from[0], d = to[0];
+#pragma unroll
+                for (int q = 1; q < kMoveRows; ++q) {
+                    s = r == q ? from[q] : s;
+                    d = r == q ? to[q] : d;
+                }
+                s = s * f.units + c;
+                d = d * f.units + c;
+                if (f.unit == 4)
+                    reinterpret_cast<uint32_t *>(f.dst)[d] =
+                        reinterpret_cast<const uint32_t *>(f.src)[s];
+                else if (f.unit == 2)
+                    reinterpret_cast<uint16_t *>(f.dst)[d] =
+                        reinterpret_cast<const uint16_t *>(f.src)[s];
+                else
+                    f.dst[d] = f.src[s];
+            }
         }
     }
 }
@@ -257,15 +435,34 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     a.src_row = reinterpret_cast<int32_t *>(base + kStatusBytes);
     a.kept = reinterpret_cast<int32_t *>(base + evict_kept_offset(src->batch, budget));
     a.status = reinterpret_cast<int32_t *>(base);
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)src->batch * kSelectCtas);
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = kSelectCtas;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
     count_launch();
-    evict_select_kernel<<<src->batch, kSelectThreads, 0, s>>>(a);
-    cudaError_t e = cudaGetLastError();
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
     if (e != cudaSuccess) return e;
-    const int64_t rows = (int64_t)src->batch * budget;
-    const int64_t grid = std::min<int64_t>((rows + 7) / 8, (int64_t)num_sms() * 32);
+    const EvictFields fields = make_fields(src, dst);
+    int32_t pieces = 0;
+    for (int k = 0; k < fields.n; ++k)
+        if (fields.f[k].unit == 16) pieces += fields.f[k].units;
+    const int64_t groups = (int64_t)src->batch * ceil_div(budget, kMoveRows);
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(groups, kMoveThreads / 32),
+                                                (int64_t)num_sms() * 64));
+    const auto kernel = pieces <= 32    ? evict_move_kernel<1>
+                        : pieces <= 64  ? evict_move_kernel<2>
+                        : pieces <= 96  ? evict_move_kernel<3>
+                        : pieces <= 160 ? evict_move_kernel<5>
+                                        : evict_move_kernel<10>;
     count_launch();
-    evict_move_kernel<<<(unsigned)grid, kMoveThreads, 0, s>>>(a, make_fields(src, dst));
-    return cudaGetLastError();
+    return launch_pdl(kernel, grid, dim3(kMoveThreads), 0, s, a, fields);
 }
 
 }  // namespace sa

@@ -14,7 +14,8 @@
 // or e4m3(amax / 6); code = e2m1(x / scale), nearest even, saturated to +-6.
 //
 // The kernels are memory-bound: one warp per quantised row of the query
-// (d_index values), one CTA per appended or read token.
+// (d_index values), per token of a 4-bit cache and per row read back, one CTA
+// per other appended token.
 #include "common.cuh"
 #include "internal.h"
 #include "prep.h"
@@ -164,32 +165,30 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(int32_t dtype, float amax) {
     return static_cast<uint32_t>(__nv_cvt_float_to_fp8(s, __NV_SATFINITE, __NV_E4M3));
 }
 
-// Two values of a group -> one byte of two codes.
-__device__ __forceinline__ uint32_t to_e2m1x2(float a, float b, float scale) {
-    if (!(scale > 0.0f)) return 0u;  // an e4m3 scale that rounded to 0
-    return __nv_cvt_float2_to_fp4x2(make_float2(__fdiv_rn(a, scale), __fdiv_rn(b, scale)),
-                                    __NV_E2M1, cudaRoundNearest);
-}
-
-// n values starting at element s0 of src -> two codes a byte at dst[0..n/2)
-// and one scale byte per group of g values.  Every thread of the CTA calls it.
-__device__ void quantize_fp4(const void *src, int64_t s0, bool bf16, int32_t n, int32_t dtype,
-                             uint8_t *dst, uint8_t *scl, int32_t *gmax) {
-    const int32_t g = fp4_group(dtype), groups = n / g;
-    for (int32_t i = threadIdx.x; i < groups; i += blockDim.x) gmax[i] = 0;
-    __syncthreads();
-    for (int32_t i = threadIdx.x; i < n; i += blockDim.x)
-        atomicMax(&gmax[i / g], __float_as_int(fabsf(load_value(src, s0 + i, bf16))));
-    __syncthreads();
-    for (int32_t i = threadIdx.x; i < n / 2; i += blockDim.x) {
-        const uint32_t byte = fp4_scale_byte(dtype, __int_as_float(gmax[2 * i / g]));
-        dst[i] = static_cast<uint8_t>(to_e2m1x2(load_value(src, s0 + 2 * i, bf16),
-                                                load_value(src, s0 + 2 * i + 1, bf16),
-                                                fp4_scale_value(dtype, byte)));
+// Sixteen values -> eight bytes of codes of a 4-bit latent.  An E8M0 scale is a
+// power of two, and a product with its reciprocal the same as the quotient; an
+// e4m3 scale is divided by (IEEE), one that rounded to 0 gives zeros.
+template <int kKv>
+__device__ __forceinline__ uint2 to_fp4x16(const float (&x)[16], uint32_t scale_byte) {
+    float q[16];
+    if constexpr (kKv == SA_MXFP4) {
+        // 2^(127 - byte): byte <= 252, so neither end leaves the normal range
+        const float inv = __uint_as_float((254u - scale_byte) << 23);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = x[i] * inv;
+    } else {
+        const float scale = fp4_scale_value(SA_NVFP4, scale_byte);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) q[i] = scale > 0.0f ? __fdiv_rn(x[i], scale) : 0.0f;
     }
-    for (int32_t i = threadIdx.x; i < groups; i += blockDim.x)
-        scl[i] = static_cast<uint8_t>(fp4_scale_byte(dtype, __int_as_float(gmax[i])));
-    __syncthreads();  // gmax is reused by the next call
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t two = __nv_cvt_float2_to_fp4x2(make_float2(q[2 * i], q[2 * i + 1]),
+                                                      __NV_E2M1, cudaRoundNearest);
+        w[i >> 2] |= two << (8 * (i & 3));
+    }
+    return make_uint2(w[0], w[1]);
 }
 
 __device__ __forceinline__ uint16_t to_bf16_bits(const void *src, int64_t i, bool bf16) {
@@ -238,14 +237,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
                 uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
                 for (int32_t i = threadIdx.x; i < p.d_rope; i += blockDim.x)
                     rope[i] = to_bf16_bits(p.kv_new, s0 + p.d_latent + i, bf16);
-            } else if (is_fp4(p.kv_dtype)) {
-                const int32_t groups = p.d_latent / p.kv_scale_dims;
-                quantize_fp4(p.kv_new, s0, bf16, p.d_latent, p.kv_dtype,
-                             static_cast<uint8_t *>(p.kv) + row * (p.d_latent / 2),
-                             reinterpret_cast<uint8_t *>(p.kv_scale) + row * groups, gmax);
-                uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
-                for (int32_t i = threadIdx.x; i < p.d_rope; i += blockDim.x)
-                    rope[i] = to_bf16_bits(p.kv_new, s0 + p.d_latent + i, bf16);
             } else if (p.kv_dtype == SA_BF16) {
                 uint16_t *dst = static_cast<uint16_t *>(p.kv) + row * D;
                 for (int32_t i = threadIdx.x; i < D; i += blockDim.x)
@@ -259,29 +250,199 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
     }
 }
 
-// Rows back out of the latent pool: one CTA per token (grid-stride).
-__global__ void __launch_bounds__(kAppendThreads)
-read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
-            const int32_t *__restrict__ pos_of, void *out, int32_t out_dtype) {
-    const int32_t D = p.d_latent + p.d_rope;
-    for (int32_t t = blockIdx.x; t < n; t += gridDim.x) {
-        const int32_t seq = __ldg(seq_of + t), pos = __ldg(pos_of + t);
-        int64_t row = -1;
-        if (seq < 0 || seq >= p.batch || pos < 0 || (pos >> 6) >= p.max_pages) {
-            if (threadIdx.x == 0) report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
-        } else {
-            row = phys_row(p.page_table, p.max_pages, p.num_pages, seq, pos);
-            if (row < 0 && threadIdx.x == 0)
-                report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+// ---------------------------------------------------------------------------
+// Append to a 4-bit latent cache, and rows back out of any latent pool: one
+// warp per token, a lane takes 16 dims at a time (32 or 64 bytes of the row, 8
+// of the codes), so that every access is whole 16- or 8-byte pieces and a
+// warp's are contiguous.  40001 rows written and read back: 19.2 us of traffic.
+// ---------------------------------------------------------------------------
+constexpr int kWarpThreads = 256;
+constexpr int kWarpTokens = kWarpThreads / 32;
+
+// N consecutive values starting at element i of src (16-byte pieces).
+template <int N>
+__device__ __forceinline__ void load_values(const void *src, int64_t i, bool bf16, float (&x)[N]) {
+    if (bf16) {
+        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + i);
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+            const uint4 u = __ldg(s + j);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                x[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
+                x[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+            }
         }
-        for (int32_t i = threadIdx.x; i < D; i += blockDim.x) {
-            const float v = row >= 0 ? kv_value(p, row, i) : 0.0f;
-            if (out_dtype == SA_BF16)
-                static_cast<__nv_bfloat16 *>(out)[(int64_t)t * D + i] = __float2bfloat16_rn(v);
-            else
-                static_cast<float *>(out)[(int64_t)t * D + i] = v;
+    } else {
+        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + i);
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j) {
+            const float4 f = __ldg(s + j);
+            x[4 * j] = f.x, x[4 * j + 1] = f.y, x[4 * j + 2] = f.z, x[4 * j + 3] = f.w;
         }
     }
+}
+
+// N values to element i of dst, rounded to nearest even for bf16.
+template <int N>
+__device__ __forceinline__ void store_values(void *dst, int64_t i, bool bf16,
+                                             const float (&x)[N]) {
+    if (bf16) {
+        uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + i);
+#pragma unroll
+        for (int j = 0; j < N / 8; ++j) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162 b =
+                    __floats2bfloat162_rn(x[8 * j + 2 * k], x[8 * j + 2 * k + 1]);
+                w[k] = *reinterpret_cast<const uint32_t *>(&b);
+            }
+            d[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(dst) + i);
+#pragma unroll
+        for (int j = 0; j < N / 4; ++j)
+            d[j] = make_float4(x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+    }
+}
+
+// Physical row of a token, or -1 after reporting why it has none.
+__device__ __forceinline__ int64_t token_row(const int32_t *page_table, int32_t batch,
+                                             int32_t max_pages, int32_t num_pages, int32_t seq,
+                                             int32_t pos, int32_t *status, bool reporter) {
+    if (seq < 0 || seq >= batch || pos < 0 || (pos >> 6) >= max_pages) {
+        if (reporter) report(status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
+        return -1;
+    }
+    const int64_t row = phys_row(page_table, max_pages, num_pages, seq, pos);
+    if (row < 0 && reporter) report(status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+    return row;
+}
+
+template <int kKv, bool kBf16>
+__global__ void __launch_bounds__(kWarpThreads) append_fp4_kernel(const AppendParams p) {
+    const int lane = threadIdx.x & 31;
+    const int32_t D = p.d_latent + p.d_rope, chunks = p.d_latent / 16;
+    const int64_t warps = (int64_t)gridDim.x * kWarpTokens;
+    for (int64_t t = (int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5); t < p.n_new;
+         t += warps) {
+        const int32_t seq = __ldg(p.seq + t), pos = __ldg(p.pos + t);
+        const int64_t s0 = t * D;
+        // the first 512 dims and the rope are on their way before the row is known
+        float x[16] = {}, rp[8] = {};
+        if (lane < chunks) load_values(p.kv_new, s0 + 16 * lane, kBf16, x);
+        if (8 * lane < p.d_rope) load_values(p.kv_new, s0 + p.d_latent + 8 * lane, kBf16, rp);
+        const int64_t row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages, seq, pos,
+                                      p.status, lane == 0);
+        if (row < 0) continue;
+        uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.kv) +
+                                                 row * (p.d_latent / 2));
+        uint8_t *scales =
+            reinterpret_cast<uint8_t *>(p.kv_scale) + row * (p.d_latent / fp4_group(kKv));
+        if (lane < chunks) {  // an even number of lanes, at most 32: d_latent <= 512
+            float amax = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+            if (kKv == SA_MXFP4) {
+                const uint32_t lanes = 0xffffffffu >> (32 - chunks);
+                amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
+            }
+            const uint32_t byte = fp4_scale_byte(kKv, amax);
+            codes[lane] = to_fp4x16<kKv>(x, byte);
+            if (kKv == SA_NVFP4) scales[lane] = static_cast<uint8_t>(byte);
+            else if ((lane & 1) == 0) scales[lane >> 1] = static_cast<uint8_t>(byte);
+        }
+        uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
+        for (int32_t c = lane; 8 * c < p.d_rope; c += 32) {
+            if (c != lane) load_values(p.kv_new, s0 + p.d_latent + 8 * c, kBf16, rp);
+            store_values(rope, 8 * c, true, rp);
+        }
+    }
+}
+
+// kWide: rows are whole 16-dim pieces; otherwise a lane takes single values.
+template <int kKv, bool kWide>
+__global__ void __launch_bounds__(kWarpThreads)
+read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
+            const int32_t *__restrict__ pos_of, void *out, bool out_bf16) {
+    const int lane = threadIdx.x & 31;
+    const int32_t dl = p.d_latent, dr = p.d_rope, D = dl + dr;
+    const int64_t warps = (int64_t)gridDim.x * kWarpTokens;
+    for (int64_t t = (int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5); t < n; t += warps) {
+        const int64_t row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
+                                      __ldg(seq_of + t), __ldg(pos_of + t), p.status, lane == 0);
+        if constexpr (!kWide) {
+            for (int32_t i = lane; i < D; i += 32) {
+                const float v = row >= 0 ? kv_value(p, row, i) : 0.0f;
+                if (out_bf16)
+                    static_cast<__nv_bfloat16 *>(out)[t * D + i] = __float2bfloat16_rn(v);
+                else
+                    static_cast<float *>(out)[t * D + i] = v;
+            }
+        } else {
+            // rows of one piece (bf16, fp32) are copied whole, latent and rope alike
+            constexpr bool kOne = kKv == SA_BF16 || kKv == SA_F32;
+            const int32_t values = kOne ? D : dl;
+            for (int32_t c = lane; 16 * c < values; c += 32) {
+                float x[16] = {};
+                if (row < 0) {
+                } else if constexpr (kOne) {
+                    load_values(p.kv, row * D + 16 * c, kKv == SA_BF16, x);
+                } else if constexpr (kKv == SA_E4M3) {
+                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(
+                                              static_cast<const uint8_t *>(p.kv) + row * dl) +
+                                          c);
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+                    const float sc = kv_scale_at(p, row, 16 * c);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = e4m3x2_to_float2(
+                            static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
+                        x[2 * j] = f.x * sc;
+                        x[2 * j + 1] = f.y * sc;
+                    }
+                } else {
+                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(
+                                              static_cast<const uint8_t *>(p.kv) + row * (dl / 2)) +
+                                          c);
+                    const uint32_t w[2] = {u.x, u.y};
+                    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale) +
+                                            row * (dl / fp4_group(kKv));
+                    const float sc = fp4_scale_value(kKv, __ldg(scales + 16 * c / fp4_group(kKv)));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 f = e2m1x2_to_float2((w[j >> 2] >> (8 * (j & 3))) & 255u);
+                        x[2 * j] = f.x * sc;
+                        x[2 * j + 1] = f.y * sc;
+                    }
+                }
+                store_values(out, t * D + 16 * c, out_bf16, x);
+            }
+            if constexpr (!kOne) {
+                for (int32_t c = lane; 8 * c < dr; c += 32) {
+                    float x[8] = {};
+                    if (row >= 0) load_values(p.kv_rope, row * dr + 8 * c, true, x);
+                    store_values(out, t * D + dl + 8 * c, out_bf16, x);
+                }
+            }
+        }
+    }
+}
+
+template <int kKv>
+cudaError_t launch_read_kv(const PathParams &p, int32_t n, const int32_t *seq, const int32_t *pos,
+                           void *out, bool out_bf16, cudaStream_t s) {
+    const bool one = kKv == SA_BF16 || kKv == SA_F32;
+    const bool wide = one ? (p.d_latent + p.d_rope) % 16 == 0
+                          : p.d_latent % 16 == 0 && p.d_rope % 8 == 0;
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(n, kWarpTokens), num_sms() * 64));
+    count_launch();
+    if (wide) read_kernel<kKv, true><<<grid, kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16);
+    else read_kernel<kKv, false><<<grid, kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16);
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -289,10 +450,14 @@ read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
 cudaError_t launch_read(const PathParams &p, int32_t n, const int32_t *seq, const int32_t *pos,
                         void *out, int32_t out_dtype, cudaStream_t s) {
     if (n <= 0) return cudaSuccess;
-    const int grid = std::min(n, num_sms() * 16);
-    count_launch();
-    read_kernel<<<grid, kAppendThreads, 0, s>>>(p, n, seq, pos, out, out_dtype);
-    return cudaGetLastError();
+    const bool bf16 = out_dtype == SA_BF16;
+    switch (p.kv_dtype) {
+    case SA_BF16: return launch_read_kv<SA_BF16>(p, n, seq, pos, out, bf16, s);
+    case SA_F32: return launch_read_kv<SA_F32>(p, n, seq, pos, out, bf16, s);
+    case SA_E4M3: return launch_read_kv<SA_E4M3>(p, n, seq, pos, out, bf16, s);
+    case SA_MXFP4: return launch_read_kv<SA_MXFP4>(p, n, seq, pos, out, bf16, s);
+    default: return launch_read_kv<SA_NVFP4>(p, n, seq, pos, out, bf16, s);
+    }
 }
 
 cudaError_t launch_quantize_rows(const void *in, sa_dtype in_dtype, int64_t n_rows, int32_t d,
@@ -319,8 +484,24 @@ cudaError_t launch_quantize_rows(const void *in, sa_dtype in_dtype, int64_t n_ro
     return cudaGetLastError();
 }
 
-cudaError_t launch_append(const AppendParams &p, cudaStream_t s) {
-    if (p.n_new <= 0) return cudaSuccess;
+template <int kKv>
+static void launch_append_fp4(const AppendParams &p, cudaStream_t s) {
+    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(p.n_new, kWarpTokens), num_sms() * 64));
+    count_launch();
+    if (p.in_bf16) append_fp4_kernel<kKv, true><<<grid, kWarpThreads, 0, s>>>(p);
+    else append_fp4_kernel<kKv, false><<<grid, kWarpThreads, 0, s>>>(p);
+}
+
+cudaError_t launch_append(const AppendParams &params, cudaStream_t s) {
+    if (params.n_new <= 0) return cudaSuccess;
+    AppendParams p = params;
+    if (is_fp4(p.kv_dtype) && p.kv_new != nullptr) {
+        if (p.kv_dtype == SA_MXFP4) launch_append_fp4<SA_MXFP4>(p, s);
+        else launch_append_fp4<SA_NVFP4>(p, s);
+        p.kv_new = nullptr;
+        const cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess || p.k_new == nullptr) return e;
+    }
     const int grid = std::min(p.n_new, num_sms() * 16);
     count_launch();
     append_kernel<<<grid, kAppendThreads, 0, s>>>(p);
