@@ -4,15 +4,16 @@
 // Of a sequence of n > budget tokens the first F, the last R and, between
 // them, the budget - F - R positions with the largest acc stay (ties to the
 // lower position).  Two kernels:
-//   select  one cluster of eight CTAs per sequence, each holding an eighth of
-//           its positions: the threshold of the middle part by an exact radix
-//           select on order-preserving keys (11 + 11 + 10 bits; the CTAs'
-//           histograms are added through distributed shared memory), then the
-//           kept positions in ascending order with their physical rows;
+//   select  one CTA, or a cluster of up to eight, per sequence: its positions'
+//           acc in shared memory where they fit, the threshold of the middle
+//           part by an exact radix select on order-preserving keys (four 8-bit
+//           digits; the CTAs' histograms are added through distributed shared
+//           memory), then the kept positions in ascending order with their
+//           physical rows;
 //   move    copies each kept token's index key, latent row and scales byte for
 //           byte to its place in the destination pages.
-// Both are bound by memory: select reads acc (five times, from L2 after the
-// first), move reads and writes the kept rows.
+// Both are bound by memory: select reads acc, move reads and writes the kept
+// rows.
 #include "evict.h"
 
 #include <algorithm>
@@ -24,9 +25,11 @@ namespace {
 
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kSelectCtas = 8;   // of a cluster: one sequence
-constexpr int kSelectBins = 2048;
+constexpr int kSelectBins = 256;
 constexpr int kSelectLoads = 8;  // of a lane in flight
+// Positions of a CTA kept in shared memory: 48K of them; longer sequences are
+// read again in every pass.
+constexpr int64_t kSelectCached = 48 * 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMaxFields = 5;
 
@@ -67,11 +70,6 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
-__device__ __forceinline__ int cluster_rank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return static_cast<int>(r);
-}
 // A word of shared memory of the cluster's CTA `rank`, at this CTA's address `p`.
 __device__ __forceinline__ int32_t peer_word(const int32_t *p, int rank) {
     uint32_t at;
@@ -83,8 +81,8 @@ __device__ __forceinline__ int32_t peer_word(const int32_t *p, int rank) {
     return v;
 }
 
-// Visits positions [w0, w1) of a warp: f(i, key, in_range) with the warp's 32
-// lanes at consecutive positions, kSelectLoads loads in flight.
+// Visits positions [w0, w1) of a warp: f(i, key, in_range, acc[i]) with the
+// warp's 32 lanes at consecutive positions, kSelectLoads loads in flight.
 template <typename F>
 __device__ __forceinline__ void for_keys(const float *acc, int32_t w0, int32_t w1, int lane, F f) {
     for (int32_t i0 = w0; i0 < w1; i0 += 32 * kSelectLoads) {
@@ -102,21 +100,25 @@ __device__ __forceinline__ void for_keys(const float *acc, int32_t w0, int32_t w
     }
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictArgs a) {
+// ctas: CTAs of a sequence's cluster.  cache_per: positions of a warp that fit
+// its part of the shared memory behind this kernel's own (0: none).
+__global__ void __launch_bounds__(kSelectThreads)
+evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     pdl_trigger();
-    __shared__ int32_t hist[3][kSelectBins];
+    extern __shared__ float cache[];
+    __shared__ int32_t hist[4][kSelectBins];
     __shared__ int32_t scan[kSelectWarps];
     __shared__ int32_t gt_s[kSelectWarps], eq_s[kSelectWarps];
     __shared__ int32_t totals[2];  // this CTA's entries above the threshold, and on it
     __shared__ int32_t pick[2];
-    const int b = blockIdx.x / kSelectCtas, rank = cluster_rank();
+    const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t n = a.src_len[b];
-    const float *acc = a.acc + (int64_t)b * a.ld_acc;
+    const float *acc_row = a.acc + (int64_t)b * a.ld_acc;
     const int32_t *st = a.src_table + (int64_t)b * a.src_max_pages;
     const int32_t *dt = a.dst_table + (int64_t)b * a.dst_max_pages;
     const int64_t out0 = (int64_t)b * a.budget;
-    for (int i = tid; i < 3 * kSelectBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < 4 * kSelectBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
 
     // every CTA checks the whole sequence, so that all take the same way
     const bool fits = n >= 0 && n <= (int64_t)a.src_max_pages * 64 && n <= a.ld_acc;
@@ -142,11 +144,31 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     const int32_t lo = shrink ? a.first : 0, hi = shrink ? len - a.last : 0;
     const int32_t want = shrink ? a.budget - a.first - a.last : 0;
     // this warp's positions, whole 32s of the sequence
-    const int32_t warps = kSelectCtas * kSelectWarps;
+    const int32_t warps = ctas * kSelectWarps;
     const int32_t per = (int32_t)round_up(ceil_div(len, warps), 32);
     const int64_t w0l = (int64_t)(rank * kSelectWarps + warp) * per;
     const int32_t w0 = (int32_t)min(w0l, (int64_t)len), w1 = (int32_t)min(w0l + per, (int64_t)len);
     const int32_t m0 = max(w0, lo), m1 = min(w1, hi);
+    // acc[i] for the warp's positions: its copy in shared memory, or the row itself
+    const float *acc = acc_row;
+    if (per <= cache_per) {
+        float *mine = cache + warp * cache_per - w0;
+        for (int32_t i0 = w0; i0 < w1; i0 += 32 * kSelectLoads) {
+            float x[kSelectLoads];
+#pragma unroll
+            for (int u = 0; u < kSelectLoads; ++u) {
+                const int32_t i = i0 + 32 * u + lane;
+                x[u] = i < w1 ? acc_row[i] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < kSelectLoads; ++u) {
+                const int32_t i = i0 + 32 * u + lane;
+                if (i < w1) mine[i] = x[u];
+            }
+        }
+        __syncwarp();
+        acc = mine;
+    }
 
     uint32_t threshold = 0xFFFFFFFFu;
     int32_t ties = 0;
@@ -154,10 +176,9 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         const uint32_t zero_key = keep_key(0.0f);
         uint32_t prefix = 0, mask = 0;
         int32_t left = want;
-#pragma unroll
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t digits = pass < 2 ? 0x7FFu : 0x3FFu;
+        for (int pass = 0; pass < 4; ++pass) {
+            const int shift = 24 - 8 * pass;
+            const uint32_t digits = 0xFFu;
             int32_t *h = hist[pass];
             // positions that never received weight share one key: they are
             // counted in registers, not by colliding atomics
@@ -170,32 +191,32 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) zeros += __shfl_xor_sync(0xffffffffu, zeros, o);
             if (lane == 0 && zeros > 0) atomicAdd(&h[(zero_key >> shift) & digits], zeros);
-            cluster_sync();
-            // the sequence's histogram, two bins a thread from the top, and the
-            // bin in which the `left`-th largest key lies
-            int32_t c0 = 0, c1 = 0;
-            const int d0 = kSelectBins - 1 - 2 * tid, d1 = d0 - 1;
+            if (ctas > 1) cluster_sync();
+            else __syncthreads();
+            // the sequence's histogram, one bin a thread from the top, and the bin
+            // in which the `left`-th largest key lies
+            int32_t count = 0, inc = 0;
+            if (tid < kSelectBins) {
+                const int d = kSelectBins - 1 - tid;
+                if (ctas == 1) count = h[d];
+                else
+                    for (int r = 0; r < ctas; ++r) count += peer_word(&h[d], r);
+                inc = count;
 #pragma unroll
-            for (int r = 0; r < kSelectCtas; ++r) {
-                c0 += peer_word(&h[d0], r);
-                c1 += peer_word(&h[d1], r);
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int32_t up = __shfl_up_sync(0xffffffffu, inc, o);
+                    if (lane >= o) inc += up;
+                }
+                if (lane == 31) scan[warp] = inc;
             }
-            int32_t inc = c0 + c1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int32_t up = __shfl_up_sync(0xffffffffu, inc, o);
-                if (lane >= o) inc += up;
-            }
-            if (lane == 31) scan[warp] = inc;
             __syncthreads();
-            int32_t above = inc - (c0 + c1);
-            for (int w = 0; w < warp; ++w) above += scan[w];
-            if (above < left && left <= above + c0) {
-                pick[0] = d0;
-                pick[1] = above;
-            } else if (above + c0 < left && left <= above + c0 + c1) {
-                pick[0] = d1;
-                pick[1] = above + c0;
+            if (tid < kSelectBins) {
+                int32_t above = inc - count;
+                for (int w = 0; w < warp; ++w) above += scan[w];
+                if (above < left && left <= above + count) {
+                    pick[0] = kSelectBins - 1 - tid;
+                    pick[1] = above;
+                }
             }
             __syncthreads();
             prefix |= (uint32_t)pick[0] << shift;
@@ -250,13 +271,14 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             totals[1] = ei;
         }
     }
-    cluster_sync();
+    if (ctas > 1) cluster_sync();
+    else __syncthreads();
     int32_t gt_before = gt_s[warp], eq_before = eq_s[warp];
     for (int r = 0; r < rank; ++r) {
         gt_before += peer_word(&totals[0], r);
         eq_before += peer_word(&totals[1], r);
     }
-    cluster_sync();  // no CTA leaves while another reads its shared memory
+    if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
 
     // ascending emission: a warp's entries start behind all earlier ones that stay
     int32_t on = eq_before;                       // entries on the threshold so far
@@ -280,10 +302,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     });
     const int32_t first = rank * kSelectThreads + tid;
     if (a.src_pos != nullptr)
-        for (int64_t i = (int64_t)kept + first; i < a.budget; i += kSelectCtas * kSelectThreads)
+        for (int64_t i = (int64_t)kept + first; i < a.budget; i += ctas * kSelectThreads)
             a.src_pos[out0 + i] = -1;
     if (a.acc_out != nullptr)
-        for (int64_t i = (int64_t)kept + first; i < a.ld_out; i += kSelectCtas * kSelectThreads)
+        for (int64_t i = (int64_t)kept + first; i < a.ld_out; i += ctas * kSelectThreads)
             a.acc_out[(int64_t)b * a.ld_out + i] = 0.0f;
     if (first == 0) {
         a.kept[b] = kept;
@@ -291,78 +313,84 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
     }
 }
 
-// One warp moves kMoveRows consecutive kept tokens at a time.  The 16-byte pieces
-// of a token's rows in all pools are dealt to the lanes, kPieces each, and all
-// loads of the tokens are in flight before the first store.
-constexpr int kMoveRows = 4;
-template <int kPieces>
-__global__ void __launch_bounds__(kMoveThreads)
-evict_move_kernel(const EvictArgs a, const EvictFields fields) {
+// One warp moves `rows` consecutive kept tokens at a time.  The 16-byte pieces of
+// all their rows in all pools are dealt to the lanes, at most kMovePieces each,
+// and all loads are in flight before the first store; the next tokens' places
+// are looked up meanwhile.
+constexpr int kMovePieces = 10;
+__global__ void __launch_bounds__(kMoveThreads, 3)
+evict_move_kernel(const EvictArgs a, const EvictFields all_fields, int32_t pieces, int32_t rows) {
+    // in shared memory: the lanes of a warp index it differently
+    __shared__ EvictFields fields;
+    if (threadIdx.x == 0) fields = all_fields;
+    __syncthreads();
     pdl_wait();
     const int lane = threadIdx.x & 31;
-    // this lane's pieces: where they start in row 0 of their pools
-    const uint8_t *src[kPieces];
-    uint8_t *dst[kPieces];
-    int32_t row_bytes[kPieces];
+    // this lane's pieces, packed: token of the group (32 and up: none), field, piece
+    uint32_t mine[kMovePieces];
 #pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
-        int32_t piece = lane + 32 * j;
-        row_bytes[j] = 0;
+    for (int j = 0; j < kMovePieces; ++j) {
+        const int32_t q = lane + 32 * j, row = q / pieces;
+        int32_t piece = q % pieces;
+        mine[j] = 32u;
         for (int k = 0; k < fields.n; ++k) {
             const EvictField &f = fields.f[k];
             if (f.unit != 16) continue;
-            if (piece >= 0 && piece < f.units) {
-                src[j] = f.src + piece * 16;
-                dst[j] = f.dst + piece * 16;
-                row_bytes[j] = f.units * 16;
-            }
+            if (piece >= 0 && piece < f.units && row < rows)
+                mine[j] = (uint32_t)row | (uint32_t)k << 8 | (uint32_t)piece << 16;
             piece -= f.units;
         }
     }
-    const int64_t groups = ceil_div(a.budget, kMoveRows);
+    const int64_t groups = ceil_div(a.budget, rows);
     const int64_t all = a.batch * groups;
     const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
-    for (int64_t g = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5); g < all;
-         g += warps) {
+    // lane r of a group looks token r up
+    auto places = [&](int64_t g, int32_t &n, int32_t &from, int32_t &to) {
+        n = from = to = 0;
+        if (g >= all) return;
         const int32_t b = (int32_t)(g / groups);
-        const int32_t i0 = (int32_t)(g % groups) * kMoveRows;
-        const int32_t rows = min(a.kept[b] - i0, kMoveRows);
-        if (rows <= 0) continue;
-        int64_t from[kMoveRows], to[kMoveRows];
+        const int32_t i0 = (int32_t)(g % groups) * rows;
+        n = min(a.kept[b] - i0, rows);
+        if (lane >= n) return;
+        const int32_t i = i0 + lane;
+        from = a.src_row[(int64_t)b * a.budget + i];
+        to = a.dst_table[(int64_t)b * a.dst_max_pages + (i >> 6)] * 64 + (i & 63);
+    };
+    int64_t g = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
+    int32_t n, from, to;
+    places(g, n, from, to);
+    for (; g < all; g += warps) {
+        uint4 x[kMovePieces];
 #pragma unroll
-        for (int r = 0; r < kMoveRows; ++r) {
-            const int32_t i = i0 + min(r, rows - 1);  // past the end: the last row again
-            from[r] = a.src_row[(int64_t)b * a.budget + i];
-            to[r] = (int64_t)a.dst_table[(int64_t)b * a.dst_max_pages + (i >> 6)] * 64 + (i & 63);
+        for (int j = 0; j < kMovePieces; ++j) {
+            const int row = mine[j] & 255u;
+            const int64_t r = __shfl_sync(0xffffffffu, from, row & 31);
+            if (row < n) {
+                const EvictField &f = fields.f[(mine[j] >> 8) & 255u];
+                x[j] = __ldcs(reinterpret_cast<const uint4 *>(f.src) + r * f.units +
+                              (mine[j] >> 16));
+            }
         }
-        uint4 x[kMoveRows][kPieces];
+        int32_t n1, from1, to1;
+        places(g + warps, n1, from1, to1);
 #pragma unroll
-        for (int r = 0; r < kMoveRows; ++r)
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j)
-                if (row_bytes[j] > 0)
-                    x[r][j] = __ldcs(
-                        reinterpret_cast<const uint4 *>(src[j] + from[r] * row_bytes[j]));
-#pragma unroll
-        for (int r = 0; r < kMoveRows; ++r)
-#pragma unroll
-            for (int j = 0; j < kPieces; ++j)
-                if (row_bytes[j] > 0 && r < rows)
-                    __stcs(reinterpret_cast<uint4 *>(dst[j] + to[r] * row_bytes[j]), x[r][j]);
+        for (int j = 0; j < kMovePieces; ++j) {
+            const int row = mine[j] & 255u;
+            const int64_t r = __shfl_sync(0xffffffffu, to, row & 31);
+            if (row < n) {
+                const EvictField &f = fields.f[(mine[j] >> 8) & 255u];
+                __stcs(reinterpret_cast<uint4 *>(f.dst) + r * f.units + (mine[j] >> 16), x[j]);
+            }
+        }
         // rows that are not whole 16-byte pieces: a few small units each
         for (int k = 0; k < fields.n; ++k) {
             const EvictField &f = fields.f[k];
             if (f.unit == 16) continue;
-            for (int32_t u = lane; u < rows * f.units; u += 32) {
-                const int32_t r = u / f.units, c = u % f.units;
-                int64_t s = from[0], d = to[0];
-#pragma unroll
-                for (int q = 1; q < kMoveRows; ++q) {
-                    s = r == q ? from[q] : s;
-                    d = r == q ? to[q] : d;
-                }
-                s = s * f.units + c;
-                d = d * f.units + c;
+            for (int32_t u0 = 0; u0 < n * f.units; u0 += 32) {
+                const int32_t u = u0 + lane, r = u / f.units, c = u % f.units;
+                const int64_t s = (int64_t)__shfl_sync(0xffffffffu, from, r & 31) * f.units + c;
+                const int64_t d = (int64_t)__shfl_sync(0xffffffffu, to, r & 31) * f.units + c;
+                if (r >= n) continue;
                 if (f.unit == 4)
                     reinterpret_cast<uint32_t *>(f.dst)[d] =
                         reinterpret_cast<const uint32_t *>(f.src)[s];
@@ -373,6 +401,9 @@ evict_move_kernel(const EvictArgs a, const EvictFields fields) {
                     f.dst[d] = f.src[s];
             }
         }
+        n = n1;
+        from = from1;
+        to = to1;
     }
 }
 
@@ -435,34 +466,43 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     a.src_row = reinterpret_cast<int32_t *>(base + kStatusBytes);
     a.kept = reinterpret_cast<int32_t *>(base + evict_kept_offset(src->batch, budget));
     a.status = reinterpret_cast<int32_t *>(base);
+    // CTAs per sequence: while they fill no more than the GPU, and each has at
+    // least 4096 positions
+    const int64_t most = std::min(ld_acc, (int64_t)src->max_pages * 64);
+    int32_t ctas = 1;
+    while (ctas < 8 && 2 * ctas * src->batch <= num_sms() && 2 * ctas * 4096 <= most) ctas *= 2;
+    const int64_t per = round_up(ceil_div(most, ctas * kSelectWarps), 32);
+    const int32_t cache_per = per * kSelectWarps <= kSelectCached ? (int32_t)per : 0;
+    const size_t smem = sizeof(float) * kSelectWarps * (size_t)cache_per;
+    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)src->batch * kSelectCtas);
+    cfg.gridDim = dim3((unsigned)(src->batch * ctas));
     cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = kSelectCtas;
+    attr[0].val.clusterDim.x = (unsigned)ctas;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launch();
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a);
+    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctas, cache_per);
     if (e != cudaSuccess) return e;
     const EvictFields fields = make_fields(src, dst);
     int32_t pieces = 0;
     for (int k = 0; k < fields.n; ++k)
         if (fields.f[k].unit == 16) pieces += fields.f[k].units;
-    const int64_t groups = (int64_t)src->batch * ceil_div(budget, kMoveRows);
+    pieces = std::max(pieces, 1);
+    const int32_t rows = std::min(32, std::max(1, 32 * kMovePieces / pieces));
+    const int64_t groups = (int64_t)src->batch * ceil_div(budget, rows);
     const dim3 grid((unsigned)std::min<int64_t>(ceil_div(groups, kMoveThreads / 32),
-                                                (int64_t)num_sms() * 64));
-    const auto kernel = pieces <= 32    ? evict_move_kernel<1>
-                        : pieces <= 64  ? evict_move_kernel<2>
-                        : pieces <= 96  ? evict_move_kernel<3>
-                        : pieces <= 160 ? evict_move_kernel<5>
-                                        : evict_move_kernel<10>;
+                                                (int64_t)num_sms() * 3));
     count_launch();
-    return launch_pdl(kernel, grid, dim3(kMoveThreads), 0, s, a, fields);
+    return launch_pdl(evict_move_kernel, grid, dim3(kMoveThreads), 0, s, a, fields, pieces, rows);
 }
 
 }  // namespace sa

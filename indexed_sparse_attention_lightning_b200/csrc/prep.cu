@@ -166,9 +166,15 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(int32_t dtype, float amax) {
 }
 
 // Sixteen values -> eight bytes of codes of a 4-bit latent.  An E8M0 scale is a
-// power of two, and a product with its reciprocal the same as the quotient; an
-// e4m3 scale is divided by (IEEE), one that rounded to 0 gives zeros.
-template <int kKv>
+// power of two, and a product with its reciprocal the same as the quotient.  An
+// e4m3 scale s is divided by (IEEE) when the values are fp32.  A bf16 value x
+// has 8 significant bits and a border m s between two codes at most 7 (m: 3, s:
+// 4), so x / s either is m or differs from it by 2^-8 of it or more: the product
+// with fp32's 1 / s, within 2^-23 of x / s and rounded to 16 bits, is m in the
+// one case and on x / s's side of it in the other, and the code is the
+// quotient's (a division per value: 40001 rows appended in 35 us).  A scale
+// that rounded to 0 gives zeros.
+template <int kKv, bool kBf16>
 __device__ __forceinline__ uint2 to_fp4x16(const float (&x)[16], uint32_t scale_byte) {
     float q[16];
     if constexpr (kKv == SA_MXFP4) {
@@ -178,17 +184,18 @@ __device__ __forceinline__ uint2 to_fp4x16(const float (&x)[16], uint32_t scale_
         for (int i = 0; i < 16; ++i) q[i] = x[i] * inv;
     } else {
         const float scale = fp4_scale_value(SA_NVFP4, scale_byte);
+        if constexpr (kBf16) {
+            if (!(scale > 0.0f)) return make_uint2(0u, 0u);
+            const float inv = __fdiv_rn(1.0f, scale);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) q[i] = scale > 0.0f ? __fdiv_rn(x[i], scale) : 0.0f;
-    }
-    uint32_t w[2] = {0u, 0u};
+            for (int i = 0; i < 16; ++i)
+                q[i] = __uint_as_float((__float_as_uint(x[i] * inv) + 0x80u) & 0xFFFFFF00u);
+        } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t two = __nv_cvt_float2_to_fp4x2(make_float2(q[2 * i], q[2 * i + 1]),
-                                                      __NV_E2M1, cudaRoundNearest);
-        w[i >> 2] |= two << (8 * (i & 3));
+            for (int i = 0; i < 16; ++i) q[i] = scale > 0.0f ? __fdiv_rn(x[i], scale) : 0.0f;
+        }
     }
-    return make_uint2(w[0], w[1]);
+    return make_uint2(float_to_e2m1x8(q), float_to_e2m1x8(q + 8));
 }
 
 __device__ __forceinline__ uint16_t to_bf16_bits(const void *src, int64_t i, bool bf16) {
@@ -322,114 +329,194 @@ __device__ __forceinline__ int64_t token_row(const int32_t *page_table, int32_t 
     return row;
 }
 
-template <int kKv, bool kBf16>
+// kTokens consecutive tokens per warp and step: their loads are in flight
+// together, and lane u looks token u's row up.
+template <int kKv, bool kBf16, int kTokens>
 __global__ void __launch_bounds__(kWarpThreads) append_fp4_kernel(const AppendParams p) {
     const int lane = threadIdx.x & 31;
     const int32_t D = p.d_latent + p.d_rope, chunks = p.d_latent / 16;
-    const int64_t warps = (int64_t)gridDim.x * kWarpTokens;
-    for (int64_t t = (int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5); t < p.n_new;
-         t += warps) {
-        const int32_t seq = __ldg(p.seq + t), pos = __ldg(p.pos + t);
-        const int64_t s0 = t * D;
-        // the first 512 dims and the rope are on their way before the row is known
-        float x[16] = {}, rp[8] = {};
-        if (lane < chunks) load_values(p.kv_new, s0 + 16 * lane, kBf16, x);
-        if (8 * lane < p.d_rope) load_values(p.kv_new, s0 + p.d_latent + 8 * lane, kBf16, rp);
-        const int64_t row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages, seq, pos,
-                                      p.status, lane == 0);
-        if (row < 0) continue;
-        uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.kv) +
-                                                 row * (p.d_latent / 2));
-        uint8_t *scales =
-            reinterpret_cast<uint8_t *>(p.kv_scale) + row * (p.d_latent / fp4_group(kKv));
-        if (lane < chunks) {  // an even number of lanes, at most 32: d_latent <= 512
-            float amax = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * kWarpTokens * kTokens;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * kTokens;
+         t0 < p.n_new; t0 += step) {
+        float x[kTokens][16] = {}, rp[kTokens][8] = {};
 #pragma unroll
-            for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
-            if (kKv == SA_MXFP4) {
-                const uint32_t lanes = 0xffffffffu >> (32 - chunks);
-                amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
-            }
-            const uint32_t byte = fp4_scale_byte(kKv, amax);
-            codes[lane] = to_fp4x16<kKv>(x, byte);
-            if (kKv == SA_NVFP4) scales[lane] = static_cast<uint8_t>(byte);
-            else if ((lane & 1) == 0) scales[lane >> 1] = static_cast<uint8_t>(byte);
+        for (int u = 0; u < kTokens; ++u) {
+            const int64_t s0 = (t0 + u) * D;
+            if (t0 + u >= p.n_new) break;
+            if (lane < chunks) load_values(p.kv_new, s0 + 16 * lane, kBf16, x[u]);
+            if (8 * lane < p.d_rope)
+                load_values(p.kv_new, s0 + p.d_latent + 8 * lane, kBf16, rp[u]);
         }
-        uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
-        for (int32_t c = lane; 8 * c < p.d_rope; c += 32) {
-            if (c != lane) load_values(p.kv_new, s0 + p.d_latent + 8 * c, kBf16, rp);
-            store_values(rope, 8 * c, true, rp);
+        int64_t my_row = -1;
+        if (lane < kTokens && t0 + lane < p.n_new)
+            my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
+                               __ldg(p.seq + t0 + lane), __ldg(p.pos + t0 + lane), p.status, true);
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u) {
+            const int64_t row = __shfl_sync(0xffffffffu, my_row, u);
+            if (row < 0) continue;
+            if (lane < chunks) {  // an even number of lanes, at most 32: d_latent <= 512
+                uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.kv) +
+                                                         row * (p.d_latent / 2));
+                uint8_t *scales =
+                    reinterpret_cast<uint8_t *>(p.kv_scale) + row * (p.d_latent / fp4_group(kKv));
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
+                if (kKv == SA_MXFP4) {
+                    const uint32_t lanes = 0xffffffffu >> (32 - chunks);
+                    amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
+                }
+                const uint32_t byte = fp4_scale_byte(kKv, amax);
+                codes[lane] = to_fp4x16<kKv, kBf16>(x[u], byte);
+                if (kKv == SA_NVFP4) scales[lane] = static_cast<uint8_t>(byte);
+                else if ((lane & 1) == 0) scales[lane >> 1] = static_cast<uint8_t>(byte);
+            }
+            uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
+            for (int32_t c = lane; 8 * c < p.d_rope; c += 32) {
+                if (c != lane)
+                    load_values(p.kv_new, (t0 + u) * D + p.d_latent + 8 * c, kBf16, rp[u]);
+                store_values(rope, 8 * c, true, rp[u]);
+            }
         }
     }
 }
 
-// kWide: rows are whole 16-dim pieces; otherwise a lane takes single values.
-template <int kKv, bool kWide>
+// Sixteen dims (piece c) of a row's latent -- of the whole row where latent and
+// rope lie in one (bf16, fp32) -- as they are stored, and their values.
+template <int kKv>
+struct LatentPiece {
+    uint4 w[kKv == SA_F32 ? 4 : kKv == SA_BF16 ? 2 : 1];
+    float scale;
+
+    __device__ __forceinline__ void load(const PathParams &p, int64_t row, int c) {
+        const uint8_t *kv = static_cast<const uint8_t *>(p.kv);
+        const int32_t dl = p.d_latent, D = dl + p.d_rope;
+        if constexpr (kKv == SA_F32 || kKv == SA_BF16) {
+            constexpr int kBytes = kKv == SA_F32 ? 4 : 2;
+            const uint4 *s = reinterpret_cast<const uint4 *>(kv + (row * D + 16 * c) * kBytes);
+#pragma unroll
+            for (int j = 0; j < kBytes; ++j) w[j] = __ldg(s + j);
+        } else if constexpr (kKv == SA_E4M3) {
+            w[0] = __ldg(reinterpret_cast<const uint4 *>(kv + row * dl) + c);
+            scale = kv_scale_at(p, row, 16 * c);
+        } else {
+            const uint2 u = __ldg(reinterpret_cast<const uint2 *>(kv + row * (dl / 2)) + c);
+            w[0] = make_uint4(u.x, u.y, 0u, 0u);
+            scale = fp4_scale_value(
+                kKv, __ldg(reinterpret_cast<const uint8_t *>(p.kv_scale) +
+                           row * (dl / fp4_group(kKv)) + 16 * c / fp4_group(kKv)));
+        }
+    }
+
+    __device__ __forceinline__ void values(float (&x)[16]) const {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+        if constexpr (is_fp4(kKv)) {
+            float v[8];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                e2m1x8_to_float(u[j], v);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[8 * j + i] = v[i] * scale;
+            }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (kKv == SA_F32) {
+                x[2 * j] = __uint_as_float(u[2 * j]);
+                x[2 * j + 1] = __uint_as_float(u[2 * j + 1]);
+            } else if constexpr (kKv == SA_BF16) {
+                x[2 * j] = __uint_as_float(u[j] << 16);
+                x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+            } else {
+                const float2 f =
+                    e4m3x2_to_float2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1))));
+                x[2 * j] = f.x * scale;
+                x[2 * j + 1] = f.y * scale;
+            }
+        }
+    }
+};
+
+// kTokens as in append_fp4_kernel.  kWide: rows are whole 16-dim pieces;
+// otherwise a lane takes single values.
+template <int kKv, bool kWide, int kTokens>
 __global__ void __launch_bounds__(kWarpThreads)
 read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
             const int32_t *__restrict__ pos_of, void *out, bool out_bf16) {
     const int lane = threadIdx.x & 31;
     const int32_t dl = p.d_latent, dr = p.d_rope, D = dl + dr;
-    const int64_t warps = (int64_t)gridDim.x * kWarpTokens;
-    for (int64_t t = (int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5); t < n; t += warps) {
-        const int64_t row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
-                                      __ldg(seq_of + t), __ldg(pos_of + t), p.status, lane == 0);
+    const int64_t step = (int64_t)gridDim.x * kWarpTokens * kTokens;
+    for (int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * kTokens; t0 < n;
+         t0 += step) {
+        int64_t my_row = -1;
+        if (lane < kTokens && t0 + lane < n)
+            my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
+                               __ldg(seq_of + t0 + lane), __ldg(pos_of + t0 + lane), p.status,
+                               true);
+        int64_t row[kTokens];
+#pragma unroll
+        for (int u = 0; u < kTokens; ++u) row[u] = __shfl_sync(0xffffffffu, my_row, u);
         if constexpr (!kWide) {
-            for (int32_t i = lane; i < D; i += 32) {
-                const float v = row >= 0 ? kv_value(p, row, i) : 0.0f;
-                if (out_bf16)
-                    static_cast<__nv_bfloat16 *>(out)[t * D + i] = __float2bfloat16_rn(v);
-                else
-                    static_cast<float *>(out)[t * D + i] = v;
+#pragma unroll 1
+            for (int u = 0; u < kTokens; ++u) {
+                if (t0 + u >= n) break;
+                for (int32_t i = lane; i < D; i += 32) {
+                    const float v = row[u] >= 0 ? kv_value(p, row[u], i) : 0.0f;
+                    const int64_t o = (t0 + u) * D + i;
+                    if (out_bf16) static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(v);
+                    else static_cast<float *>(out)[o] = v;
+                }
             }
         } else {
-            // rows of one piece (bf16, fp32) are copied whole, latent and rope alike
             constexpr bool kOne = kKv == SA_BF16 || kKv == SA_F32;
-            const int32_t values = kOne ? D : dl;
-            for (int32_t c = lane; 16 * c < values; c += 32) {
-                float x[16] = {};
-                if (row < 0) {
-                } else if constexpr (kOne) {
-                    load_values(p.kv, row * D + 16 * c, kKv == SA_BF16, x);
-                } else if constexpr (kKv == SA_E4M3) {
-                    const uint4 u = __ldg(reinterpret_cast<const uint4 *>(
-                                              static_cast<const uint8_t *>(p.kv) + row * dl) +
-                                          c);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                    const float sc = kv_scale_at(p, row, 16 * c);
+            const int32_t pieces = (kOne ? D : dl) / 16, rope_pieces = kOne ? 0 : dr / 8;
+            for (int32_t c = lane; c < pieces || c < rope_pieces; c += 32) {
+                LatentPiece<kKv> piece[kTokens];
+                uint4 rope[kTokens];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = e4m3x2_to_float2(
-                            static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1))));
-                        x[2 * j] = f.x * sc;
-                        x[2 * j + 1] = f.y * sc;
-                    }
-                } else {
-                    const uint2 u = __ldg(reinterpret_cast<const uint2 *>(
-                                              static_cast<const uint8_t *>(p.kv) + row * (dl / 2)) +
-                                          c);
-                    const uint32_t w[2] = {u.x, u.y};
-                    const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale) +
-                                            row * (dl / fp4_group(kKv));
-                    const float sc = fp4_scale_value(kKv, __ldg(scales + 16 * c / fp4_group(kKv)));
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 f = e2m1x2_to_float2((w[j >> 2] >> (8 * (j & 3))) & 255u);
-                        x[2 * j] = f.x * sc;
-                        x[2 * j + 1] = f.y * sc;
-                    }
+                for (int u = 0; u < kTokens; ++u) {
+                    if (row[u] < 0) continue;
+                    if (c < pieces) piece[u].load(p, row[u], c);
+                    if (c < rope_pieces)
+                        rope[u] = __ldg(reinterpret_cast<const uint4 *>(
+                                            static_cast<const uint16_t *>(p.kv_rope) +
+                                            row[u] * dr) +
+                                        c);
                 }
-                store_values(out, t * D + 16 * c, out_bf16, x);
-            }
-            if constexpr (!kOne) {
-                for (int32_t c = lane; 8 * c < dr; c += 32) {
-                    float x[8] = {};
-                    if (row >= 0) load_values(p.kv_rope, row * dr + 8 * c, true, x);
-                    store_values(out, t * D + dl + 8 * c, out_bf16, x);
+#pragma unroll
+                for (int u = 0; u < kTokens; ++u) {
+                    if (t0 + u >= n) break;
+                    const int64_t o = (t0 + u) * D;
+                    if (c < pieces) {
+                        float x[16] = {};
+                        if (row[u] >= 0) piece[u].values(x);
+                        store_values(out, o + 16 * c, out_bf16, x);
+                    }
+                    if (c < rope_pieces) {
+                        const uint32_t w[4] = {rope[u].x, rope[u].y, rope[u].z, rope[u].w};
+                        float x[8] = {};
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            if (row[u] < 0) break;
+                            x[2 * j] = __uint_as_float(w[j] << 16);
+                            x[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+                        }
+                        store_values(out, o + dl + 8 * c, out_bf16, x);
+                    }
                 }
             }
         }
     }
+}
+
+// Tokens per warp: one while the tokens are fewer than the GPU's warps (a decode
+// step: the latency of one row), four beyond (a prompt: more loads in flight).
+bool many_tokens(int64_t n) { return n > (int64_t)num_sms() * 32; }
+dim3 token_grid(int64_t n, int tokens) {
+    return dim3((unsigned)std::min<int64_t>(ceil_div(n, (int64_t)kWarpTokens * tokens),
+                                            (int64_t)num_sms() * 64));
 }
 
 template <int kKv>
@@ -438,10 +525,11 @@ cudaError_t launch_read_kv(const PathParams &p, int32_t n, const int32_t *seq, c
     const bool one = kKv == SA_BF16 || kKv == SA_F32;
     const bool wide = one ? (p.d_latent + p.d_rope) % 16 == 0
                           : p.d_latent % 16 == 0 && p.d_rope % 8 == 0;
-    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(n, kWarpTokens), num_sms() * 64));
+    const int tokens = many_tokens(n) ? 4 : 1;
+    const auto kernel = tokens == 4 ? (wide ? read_kernel<kKv, true, 4> : read_kernel<kKv, false, 4>)
+                                    : (wide ? read_kernel<kKv, true, 1> : read_kernel<kKv, false, 1>);
     count_launch();
-    if (wide) read_kernel<kKv, true><<<grid, kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16);
-    else read_kernel<kKv, false><<<grid, kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16);
+    kernel<<<token_grid(n, tokens), kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16);
     return cudaGetLastError();
 }
 
@@ -486,10 +574,13 @@ cudaError_t launch_quantize_rows(const void *in, sa_dtype in_dtype, int64_t n_ro
 
 template <int kKv>
 static void launch_append_fp4(const AppendParams &p, cudaStream_t s) {
-    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(p.n_new, kWarpTokens), num_sms() * 64));
+    const int tokens = many_tokens(p.n_new) ? 4 : 1;
+    const auto kernel =
+        p.in_bf16 ? (tokens == 4 ? append_fp4_kernel<kKv, true, 4> : append_fp4_kernel<kKv, true, 1>)
+                  : (tokens == 4 ? append_fp4_kernel<kKv, false, 4>
+                                 : append_fp4_kernel<kKv, false, 1>);
     count_launch();
-    if (p.in_bf16) append_fp4_kernel<kKv, true><<<grid, kWarpThreads, 0, s>>>(p);
-    else append_fp4_kernel<kKv, false><<<grid, kWarpThreads, 0, s>>>(p);
+    kernel<<<token_grid(p.n_new, tokens), kWarpThreads, 0, s>>>(p);
 }
 
 cudaError_t launch_append(const AppendParams &params, cudaStream_t s) {
