@@ -26,9 +26,10 @@ namespace {
 constexpr int kSelectThreads = 1024;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kSelectBins = 256;
-constexpr int kSelectLoads = 8;  // of a lane in flight
-// Positions of a CTA kept in shared memory: 48K of them; longer sequences are
-// read again in every pass.
+constexpr int kSelectCopies = 8;  // of a histogram, so that equal digits collide less
+constexpr int kSelectStep = 128;  // positions of a warp at a time: four per lane
+// Keys of a CTA kept in shared memory: 48K of them; longer sequences are read
+// again in every pass.
 constexpr int64_t kSelectCached = 48 * 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMaxFields = 5;
@@ -81,31 +82,57 @@ __device__ __forceinline__ int32_t peer_word(const int32_t *p, int rank) {
     return v;
 }
 
-// Visits positions [w0, w1) of a warp: f(i, key, in_range, acc[i]) with the
-// warp's 32 lanes at consecutive positions, kSelectLoads loads in flight.
-template <typename F>
-__device__ __forceinline__ void for_keys(const float *acc, int32_t w0, int32_t w1, int lane, F f) {
-    for (int32_t i0 = w0; i0 < w1; i0 += 32 * kSelectLoads) {
-        float x[kSelectLoads];
+// A warp's positions [w0, w1) of a sequence, four consecutive ones per lane and
+// step.  keys() gives those of the middle part [lo, hi), and 0, which is no
+// value's key, for the others.
+template <bool kCached>
+struct WarpKeys {
+    const float *acc;
+    uint32_t *cache;  // the warp's keys
+    int32_t w0, w1, lo, hi, lane;
+
+    __device__ __forceinline__ uint4 fresh(int32_t i0) const {
+        uint32_t k[4];
 #pragma unroll
-        for (int u = 0; u < kSelectLoads; ++u) {
-            const int32_t i = i0 + 32 * u + lane;
-            x[u] = i < w1 ? acc[i] : 0.0f;
+        for (int e = 0; e < 4; ++e) {
+            const int32_t i = i0 + 4 * lane + e;
+            k[e] = i >= lo && i < min(hi, w1) ? keep_key(acc[i]) : 0u;
         }
-#pragma unroll
-        for (int u = 0; u < kSelectLoads; ++u) {
-            const int32_t i = i0 + 32 * u + lane;
-            if (i0 + 32 * u < w1) f(i, keep_key(x[u]), i < w1, x[u]);
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    }
+    __device__ __forceinline__ void fill() const {
+        if constexpr (kCached) {
+#pragma unroll 4
+            for (int32_t i0 = w0; i0 < w1; i0 += kSelectStep)
+                reinterpret_cast<uint4 *>(cache + (i0 - w0))[lane] = fresh(i0);
         }
     }
-}
+    __device__ __forceinline__ uint4 keys(int32_t i0) const {
+        if constexpr (kCached) return reinterpret_cast<const uint4 *>(cache + (i0 - w0))[lane];
+        else return fresh(i0);
+    }
+    // f(key) for every position of the middle part
+    template <typename F>
+    __device__ __forceinline__ void each(F f) const {
+#pragma unroll 4
+        for (int32_t i0 = w0; i0 < w1; i0 += kSelectStep) {
+            const uint4 k = keys(i0);
+            f(k.x);
+            f(k.y);
+            f(k.z);
+            f(k.w);
+        }
+    }
+};
 
-// ctas: CTAs of a sequence's cluster.  cache_per: positions of a warp that fit
-// its part of the shared memory behind this kernel's own (0: none).
-__global__ void __launch_bounds__(kSelectThreads)
+// ctas: CTAs of a sequence's cluster.  cache_per: keys of a warp in the dynamic
+// shared memory.
+template <bool kCached>
+__global__ void __launch_bounds__(kSelectThreads, 1)
 evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     pdl_trigger();
-    extern __shared__ float cache[];
+    extern __shared__ uint4 cache[];
+    __shared__ int32_t copies[kSelectCopies][kSelectBins];
     __shared__ int32_t hist[4][kSelectBins];
     __shared__ int32_t scan[kSelectWarps];
     __shared__ int32_t gt_s[kSelectWarps], eq_s[kSelectWarps];
@@ -114,11 +141,11 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     const int b = blockIdx.x / ctas, rank = blockIdx.x % ctas;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int32_t n = a.src_len[b];
-    const float *acc_row = a.acc + (int64_t)b * a.ld_acc;
+    const float *acc = a.acc + (int64_t)b * a.ld_acc;
     const int32_t *st = a.src_table + (int64_t)b * a.src_max_pages;
     const int32_t *dt = a.dst_table + (int64_t)b * a.dst_max_pages;
     const int64_t out0 = (int64_t)b * a.budget;
-    for (int i = tid; i < 4 * kSelectBins; i += kSelectThreads) (&hist[0][0])[i] = 0;
+    for (int i = tid; i < kSelectCopies * kSelectBins; i += kSelectThreads) (&copies[0][0])[i] = 0;
 
     // every CTA checks the whole sequence, so that all take the same way
     const bool fits = n >= 0 && n <= (int64_t)a.src_max_pages * 64 && n <= a.ld_acc;
@@ -130,77 +157,66 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
         for (int32_t i = tid; i < (kept + 63) / 64; i += kSelectThreads)
             bad |= dt[i] < 0 || dt[i] >= a.dst_pages;
     }
+    // the middle part [lo, hi) keeps its `want` largest keys: all above the
+    // threshold and the first `ties` on it
+    const bool shrink = fits && n > a.budget;
+    const int32_t lo = shrink ? a.first : 0, hi = shrink ? n - a.last : 0;
+    const int32_t want = shrink ? a.budget - a.first - a.last : 0;
+    // this warp's positions: whole steps of the sequence
+    const int32_t span = fits ? n : 0;
+    const int64_t per = round_up(ceil_div(span, ctas * kSelectWarps), kSelectStep);
+    const int64_t begin = (rank * kSelectWarps + warp) * per;
+    const WarpKeys<kCached> mine{
+        acc, reinterpret_cast<uint32_t *>(cache) + (int64_t)warp * cache_per,
+        (int32_t)min(begin, (int64_t)span), (int32_t)min(begin + per, (int64_t)span), lo, hi, lane};
+    if (want > 0) mine.fill();
     bad = __syncthreads_or(bad);
     if (tid == 0 && rank == 0) {
         if (!fits) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
         if (bad) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
     }
-    const int32_t len = fits && !bad ? n : 0;
-    const int32_t kept = min(len, a.budget);
-
-    // the middle part [lo, hi) keeps its `want` largest keys: all above the
-    // threshold and the first `ties` on it
-    const bool shrink = len > a.budget;
-    const int32_t lo = shrink ? a.first : 0, hi = shrink ? len - a.last : 0;
-    const int32_t want = shrink ? a.budget - a.first - a.last : 0;
-    // this warp's positions, whole 32s of the sequence
-    const int32_t warps = ctas * kSelectWarps;
-    const int32_t per = (int32_t)round_up(ceil_div(len, warps), 32);
-    const int64_t w0l = (int64_t)(rank * kSelectWarps + warp) * per;
-    const int32_t w0 = (int32_t)min(w0l, (int64_t)len), w1 = (int32_t)min(w0l + per, (int64_t)len);
-    const int32_t m0 = max(w0, lo), m1 = min(w1, hi);
-    // acc[i] for the warp's positions: its copy in shared memory, or the row itself
-    const float *acc = acc_row;
-    if (per <= cache_per) {
-        float *mine = cache + warp * cache_per - w0;
-        for (int32_t i0 = w0; i0 < w1; i0 += 32 * kSelectLoads) {
-            float x[kSelectLoads];
-#pragma unroll
-            for (int u = 0; u < kSelectLoads; ++u) {
-                const int32_t i = i0 + 32 * u + lane;
-                x[u] = i < w1 ? acc_row[i] : 0.0f;
-            }
-#pragma unroll
-            for (int u = 0; u < kSelectLoads; ++u) {
-                const int32_t i = i0 + 32 * u + lane;
-                if (i < w1) mine[i] = x[u];
-            }
-        }
-        __syncwarp();
-        acc = mine;
-    }
+    const int32_t kept = bad ? 0 : min(span, a.budget);
 
     uint32_t threshold = 0xFFFFFFFFu;
     int32_t ties = 0;
-    if (want > 0) {
+    if (want > 0 && !bad) {
         const uint32_t zero_key = keep_key(0.0f);
         uint32_t prefix = 0, mask = 0;
         int32_t left = want;
         for (int pass = 0; pass < 4; ++pass) {
             const int shift = 24 - 8 * pass;
-            const uint32_t digits = 0xFFu;
-            int32_t *h = hist[pass];
+            int32_t *h = copies[lane & (kSelectCopies - 1)];
             // positions that never received weight share one key: they are
             // counted in registers, not by colliding atomics
             int32_t zeros = 0;
-            for_keys(acc, m0, m1, lane, [&](int32_t, uint32_t k, bool in, float) {
-                if (!in || (k & mask) != prefix) return;
+            mine.each([&](uint32_t k) {
                 if (k == zero_key) ++zeros;
-                else atomicAdd(&h[(k >> shift) & digits], 1);
+                else if (k != 0u && (k & mask) == prefix) atomicAdd(&h[(k >> shift) & 255u], 1);
             });
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) zeros += __shfl_xor_sync(0xffffffffu, zeros, o);
-            if (lane == 0 && zeros > 0) atomicAdd(&h[(zero_key >> shift) & digits], zeros);
+            if (lane == 0 && (zero_key & mask) == prefix && zeros > 0)
+                atomicAdd(&h[(zero_key >> shift) & 255u], zeros);
+            __syncthreads();
+            if (tid < kSelectBins) {
+                int32_t sum = 0;
+#pragma unroll
+                for (int c = 0; c < kSelectCopies; ++c) {
+                    sum += copies[c][tid];
+                    copies[c][tid] = 0;
+                }
+                hist[pass][tid] = sum;
+            }
             if (ctas > 1) cluster_sync();
             else __syncthreads();
             // the sequence's histogram, one bin a thread from the top, and the bin
             // in which the `left`-th largest key lies
             int32_t count = 0, inc = 0;
             if (tid < kSelectBins) {
-                const int d = kSelectBins - 1 - tid;
-                if (ctas == 1) count = h[d];
+                const int32_t *d = &hist[pass][kSelectBins - 1 - tid];
+                if (ctas == 1) count = *d;
                 else
-                    for (int r = 0; r < ctas; ++r) count += peer_word(&h[d], r);
+                    for (int r = 0; r < ctas; ++r) count += peer_word(d, r);
                 inc = count;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -220,7 +236,7 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
             }
             __syncthreads();
             prefix |= (uint32_t)pick[0] << shift;
-            mask |= digits << shift;
+            mask |= 255u << shift;
             left -= pick[1];
             __syncthreads();  // scan and pick are written again
         }
@@ -229,26 +245,22 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     }
 
     // entries of each warp that stay for certain, and those on the threshold
+    const int32_t w0 = mine.w0, w1 = bad ? mine.w0 : mine.w1;
     int32_t gt = 0, eq = 0;
-    if (want > 0) {
-        gt = (w1 - w0) - max(0, m1 - m0);  // first and last tokens
-        int32_t above = 0, on = 0;
-        for_keys(acc, m0, m1, lane, [&](int32_t, uint32_t k, bool in, float) {
-            above += in && k > threshold;
-            on += in && k == threshold;
+    if (want > 0 && !bad) {
+        mine.each([&](uint32_t k) {
+            gt += k > threshold;
+            eq += k == threshold;
         });
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
-            above += __shfl_xor_sync(0xffffffffu, above, o);
-            on += __shfl_xor_sync(0xffffffffu, on, o);
+            gt += __shfl_xor_sync(0xffffffffu, gt, o);
+            eq += __shfl_xor_sync(0xffffffffu, eq, o);
         }
-        gt += above;
-        eq = on;
-    } else {
-        gt = (w1 - w0) - max(0, m1 - m0);
     }
     if (lane == 0) {
-        gt_s[warp] = gt;
+        // and the first and last tokens
+        gt_s[warp] = gt + (w1 - w0) - max(0, min(w1, hi) - max(w0, lo));
         eq_s[warp] = eq;
     }
     __syncthreads();
@@ -281,25 +293,42 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
 
     // ascending emission: a warp's entries start behind all earlier ones that stay
-    int32_t on = eq_before;                       // entries on the threshold so far
-    int32_t slot = gt_before + min(on, ties);     // kept entries so far
+    int32_t on = eq_before;                    // entries on the threshold so far
+    int32_t slot = gt_before + min(on, ties);  // kept entries so far
     const uint32_t below = (1u << lane) - 1u;
-    for_keys(acc, w0, w1, lane, [&](int32_t i, uint32_t k, bool in, float x) {
-        const bool middle = in && i >= lo && i < hi;
-        const bool tie = middle && want > 0 && k == threshold;
-        const uint32_t tie_bits = __ballot_sync(0xffffffffu, tie);
-        bool keep = in && !middle;
-        if (middle) keep = want > 0 && (k > threshold || (tie && on + __popc(tie_bits & below) < ties));
-        const uint32_t bits = __ballot_sync(0xffffffffu, keep);
-        if (keep) {
-            const int32_t at = slot + __popc(bits & below);
+    for (int32_t i0 = w0; i0 < w1; i0 += kSelectStep) {
+        const uint4 k4 = want > 0 ? mine.keys(i0) : make_uint4(0u, 0u, 0u, 0u);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+        int32_t rank_on = on;  // entries on the threshold before this lane's
+        bool tie[4], keep[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            tie[e] = k[e] != 0u && k[e] == threshold && want > 0;
+            const uint32_t bits = __ballot_sync(0xffffffffu, tie[e]);
+            rank_on += __popc(bits & below);
+            on += __popc(bits);
+        }
+        int32_t at = slot;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int32_t i = i0 + 4 * lane + e;
+            keep[e] = k[e] > threshold || (tie[e] && rank_on < ties) ||
+                      (i < w1 && (i < lo || i >= hi));
+            rank_on += tie[e];
+            const uint32_t bits = __ballot_sync(0xffffffffu, keep[e]);
+            at += __popc(bits & below);
+            slot += __popc(bits);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (!keep[e]) continue;
+            const int32_t i = i0 + 4 * lane + e;
             a.src_row[out0 + at] = st[i >> 6] * 64 + (i & 63);
             if (a.src_pos != nullptr) a.src_pos[out0 + at] = i;
-            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = x;
+            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = acc[i];
+            ++at;
         }
-        on += __popc(tie_bits);
-        slot += __popc(bits);
-    });
+    }
     const int32_t first = rank * kSelectThreads + tid;
     if (a.src_pos != nullptr)
         for (int64_t i = (int64_t)kept + first; i < a.budget; i += ctas * kSelectThreads)
@@ -471,11 +500,12 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     const int64_t most = std::min(ld_acc, (int64_t)src->max_pages * 64);
     int32_t ctas = 1;
     while (ctas < 8 && 2 * ctas * src->batch <= num_sms() && 2 * ctas * 4096 <= most) ctas *= 2;
-    const int64_t per = round_up(ceil_div(most, ctas * kSelectWarps), 32);
+    const int64_t per = round_up(ceil_div(most, ctas * kSelectWarps), kSelectStep);
     const int32_t cache_per = per * kSelectWarps <= kSelectCached ? (int32_t)per : 0;
-    const size_t smem = sizeof(float) * kSelectWarps * (size_t)cache_per;
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const size_t smem = sizeof(uint32_t) * kSelectWarps * (size_t)cache_per;
+    const auto select = cache_per > 0 ? evict_select_kernel<true> : evict_select_kernel<false>;
+    cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(src->batch * ctas));
@@ -490,7 +520,7 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     count_launch();
-    e = cudaLaunchKernelEx(&cfg, evict_select_kernel, a, ctas, cache_per);
+    e = cudaLaunchKernelEx(&cfg, select, a, ctas, cache_per);
     if (e != cudaSuccess) return e;
     const EvictFields fields = make_fields(src, dst);
     int32_t pieces = 0;

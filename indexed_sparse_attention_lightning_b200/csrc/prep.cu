@@ -329,54 +329,88 @@ __device__ __forceinline__ int64_t token_row(const int32_t *page_table, int32_t 
     return row;
 }
 
-// kTokens consecutive tokens per warp and step: their loads are in flight
-// together, and lane u looks token u's row up.
-template <int kKv, bool kBf16, int kTokens>
-__global__ void __launch_bounds__(kWarpThreads) append_fp4_kernel(const AppendParams p) {
+// A warp takes `block` consecutive tokens: its lanes look their rows up at once,
+// then kTokens of them at a time have their loads in flight together.
+constexpr int kMaxBlock = 32;
+
+// 16-byte pieces of N values, as they are stored.
+template <int N, bool kBf16>
+struct RawValues {
+    uint4 w[kBf16 ? N / 8 : N / 4];
+
+    __device__ __forceinline__ void load(const void *src, int64_t i) {
+        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(src) +
+                                                         i * (kBf16 ? 2 : 4));
+#pragma unroll
+        for (int j = 0; j < (kBf16 ? N / 8 : N / 4); ++j) w[j] = __ldcs(s + j);
+    }
+    __device__ __forceinline__ void values(float (&x)[N]) const {
+        const uint32_t *u = reinterpret_cast<const uint32_t *>(w);
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            x[2 * j] = __uint_as_float(kBf16 ? u[j] << 16 : u[2 * j]);
+            x[2 * j + 1] = __uint_as_float(kBf16 ? u[j] & 0xffff0000u : u[2 * j + 1]);
+        }
+    }
+};
+
+template <int kKv, bool kBf16>
+__global__ void __launch_bounds__(kWarpThreads)
+append_fp4_kernel(const AppendParams p, int32_t block) {
+    constexpr int kTokens = kBf16 ? 3 : 2;
     const int lane = threadIdx.x & 31;
     const int32_t D = p.d_latent + p.d_rope, chunks = p.d_latent / 16;
-    const int64_t step = (int64_t)gridDim.x * kWarpTokens * kTokens;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * kTokens;
-         t0 < p.n_new; t0 += step) {
-        float x[kTokens][16] = {}, rp[kTokens][8] = {};
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * block;
+    const int32_t count = (int32_t)min((int64_t)block, p.n_new - t0);
+    if (count <= 0) return;
+    int32_t my_seq = 0, my_pos = 0;
+    if (lane < count) {
+        my_seq = __ldg(p.seq + t0 + lane);
+        my_pos = __ldg(p.pos + t0 + lane);
+    }
+    int64_t my_row = -1;
+    for (int32_t u0 = 0; u0 < count; u0 += kTokens) {
+        RawValues<16, kBf16> raw[kTokens];
+        RawValues<8, kBf16> raw_rope[kTokens];
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
-            const int64_t s0 = (t0 + u) * D;
-            if (t0 + u >= p.n_new) break;
-            if (lane < chunks) load_values(p.kv_new, s0 + 16 * lane, kBf16, x[u]);
-            if (8 * lane < p.d_rope)
-                load_values(p.kv_new, s0 + p.d_latent + 8 * lane, kBf16, rp[u]);
+            const int64_t s0 = (t0 + u0 + u) * D;
+            if (u0 + u >= count) break;
+            if (lane < chunks) raw[u].load(p.kv_new, s0 + 16 * lane);
+            if (8 * lane < p.d_rope) raw_rope[u].load(p.kv_new, s0 + p.d_latent + 8 * lane);
         }
-        int64_t my_row = -1;
-        if (lane < kTokens && t0 + lane < p.n_new)
-            my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
-                               __ldg(p.seq + t0 + lane), __ldg(p.pos + t0 + lane), p.status, true);
+        if (u0 == 0 && lane < count)  // while the first rows are on their way
+            my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages, my_seq, my_pos,
+                               p.status, true);
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
-            const int64_t row = __shfl_sync(0xffffffffu, my_row, u);
-            if (row < 0) continue;
+            const int64_t row = __shfl_sync(0xffffffffu, my_row, (u0 + u) & 31);
+            if (u0 + u >= count || row < 0) continue;
             if (lane < chunks) {  // an even number of lanes, at most 32: d_latent <= 512
                 uint2 *codes = reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.kv) +
                                                          row * (p.d_latent / 2));
                 uint8_t *scales =
                     reinterpret_cast<uint8_t *>(p.kv_scale) + row * (p.d_latent / fp4_group(kKv));
-                float amax = 0.0f;
+                float x[16], amax = 0.0f;
+                raw[u].values(x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
+                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
                 if (kKv == SA_MXFP4) {
                     const uint32_t lanes = 0xffffffffu >> (32 - chunks);
                     amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
                 }
                 const uint32_t byte = fp4_scale_byte(kKv, amax);
-                codes[lane] = to_fp4x16<kKv, kBf16>(x[u], byte);
+                codes[lane] = to_fp4x16<kKv, kBf16>(x, byte);
                 if (kKv == SA_NVFP4) scales[lane] = static_cast<uint8_t>(byte);
                 else if ((lane & 1) == 0) scales[lane >> 1] = static_cast<uint8_t>(byte);
             }
             uint16_t *rope = static_cast<uint16_t *>(p.kv_rope) + row * p.d_rope;
             for (int32_t c = lane; 8 * c < p.d_rope; c += 32) {
+                float x[8];
                 if (c != lane)
-                    load_values(p.kv_new, (t0 + u) * D + p.d_latent + 8 * c, kBf16, rp[u]);
-                store_values(rope, 8 * c, true, rp[u]);
+                    raw_rope[u].load(p.kv_new, (t0 + u0 + u) * D + p.d_latent + 8 * c);
+                raw_rope[u].values(x);
+                store_values(rope, 8 * c, true, x);
             }
         }
     }
@@ -419,65 +453,66 @@ struct LatentPiece {
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[8 * j + i] = v[i] * scale;
             }
-            return;
-        }
+        } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if constexpr (kKv == SA_F32) {
-                x[2 * j] = __uint_as_float(u[2 * j]);
-                x[2 * j + 1] = __uint_as_float(u[2 * j + 1]);
-            } else if constexpr (kKv == SA_BF16) {
-                x[2 * j] = __uint_as_float(u[j] << 16);
-                x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
-            } else {
-                const float2 f =
-                    e4m3x2_to_float2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1))));
-                x[2 * j] = f.x * scale;
-                x[2 * j + 1] = f.y * scale;
+            for (int j = 0; j < 8; ++j) {
+                if constexpr (kKv == SA_F32) {
+                    x[2 * j] = __uint_as_float(u[2 * j]);
+                    x[2 * j + 1] = __uint_as_float(u[2 * j + 1]);
+                } else if constexpr (kKv == SA_BF16) {
+                    x[2 * j] = __uint_as_float(u[j] << 16);
+                    x[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+                } else {
+                    const float2 f =
+                        e4m3x2_to_float2(static_cast<uint16_t>(u[j >> 1] >> (16 * (j & 1))));
+                    x[2 * j] = f.x * scale;
+                    x[2 * j + 1] = f.y * scale;
+                }
             }
         }
     }
 };
 
-// kTokens as in append_fp4_kernel.  kWide: rows are whole 16-dim pieces;
-// otherwise a lane takes single values.
-template <int kKv, bool kWide, int kTokens>
+// Blocks of tokens as in append_fp4_kernel.  kWide: rows are whole 16-dim
+// pieces; otherwise a lane takes single values.
+template <int kKv, bool kWide>
 __global__ void __launch_bounds__(kWarpThreads)
 read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
-            const int32_t *__restrict__ pos_of, void *out, bool out_bf16) {
+            const int32_t *__restrict__ pos_of, void *out, bool out_bf16, int32_t block) {
+    constexpr int kTokens = kKv == SA_F32 ? 2 : 4;
     const int lane = threadIdx.x & 31;
     const int32_t dl = p.d_latent, dr = p.d_rope, D = dl + dr;
-    const int64_t step = (int64_t)gridDim.x * kWarpTokens * kTokens;
-    for (int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * kTokens; t0 < n;
-         t0 += step) {
-        int64_t my_row = -1;
-        if (lane < kTokens && t0 + lane < n)
-            my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
-                               __ldg(seq_of + t0 + lane), __ldg(pos_of + t0 + lane), p.status,
-                               true);
-        int64_t row[kTokens];
-#pragma unroll
-        for (int u = 0; u < kTokens; ++u) row[u] = __shfl_sync(0xffffffffu, my_row, u);
-        if constexpr (!kWide) {
-#pragma unroll 1
-            for (int u = 0; u < kTokens; ++u) {
-                if (t0 + u >= n) break;
-                for (int32_t i = lane; i < D; i += 32) {
-                    const float v = row[u] >= 0 ? kv_value(p, row[u], i) : 0.0f;
-                    const int64_t o = (t0 + u) * D + i;
-                    if (out_bf16) static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(v);
-                    else static_cast<float *>(out)[o] = v;
-                }
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * block;
+    const int32_t count = (int32_t)min((int64_t)block, n - t0);
+    if (count <= 0) return;
+    int64_t my_row = -1;
+    if (lane < count)
+        my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
+                           __ldg(seq_of + t0 + lane), __ldg(pos_of + t0 + lane), p.status, true);
+    if constexpr (!kWide) {
+        for (int32_t u = 0; u < count; ++u) {
+            const int64_t row = __shfl_sync(0xffffffffu, my_row, u);
+            for (int32_t i = lane; i < D; i += 32) {
+                const float v = row >= 0 ? kv_value(p, row, i) : 0.0f;
+                const int64_t o = (t0 + u) * D + i;
+                if (out_bf16) static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(v);
+                else static_cast<float *>(out)[o] = v;
             }
-        } else {
-            constexpr bool kOne = kKv == SA_BF16 || kKv == SA_F32;
-            const int32_t pieces = (kOne ? D : dl) / 16, rope_pieces = kOne ? 0 : dr / 8;
+        }
+    } else {
+        constexpr bool kOne = kKv == SA_BF16 || kKv == SA_F32;
+        const int32_t pieces = (kOne ? D : dl) / 16, rope_pieces = kOne ? 0 : dr / 8;
+        for (int32_t u0 = 0; u0 < count; u0 += kTokens) {
+            int64_t row[kTokens];
+#pragma unroll
+            for (int u = 0; u < kTokens; ++u)
+                row[u] = __shfl_sync(0xffffffffu, my_row, (u0 + u) & 31);
             for (int32_t c = lane; c < pieces || c < rope_pieces; c += 32) {
                 LatentPiece<kKv> piece[kTokens];
                 uint4 rope[kTokens];
 #pragma unroll
                 for (int u = 0; u < kTokens; ++u) {
-                    if (row[u] < 0) continue;
+                    if (u0 + u >= count || row[u] < 0) continue;
                     if (c < pieces) piece[u].load(p, row[u], c);
                     if (c < rope_pieces)
                         rope[u] = __ldg(reinterpret_cast<const uint4 *>(
@@ -487,8 +522,8 @@ read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
                 }
 #pragma unroll
                 for (int u = 0; u < kTokens; ++u) {
-                    if (t0 + u >= n) break;
-                    const int64_t o = (t0 + u) * D;
+                    if (u0 + u >= count) break;
+                    const int64_t o = (t0 + u0 + u) * D;
                     if (c < pieces) {
                         float x[16] = {};
                         if (row[u] >= 0) piece[u].values(x);
@@ -511,12 +546,13 @@ read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
     }
 }
 
-// Tokens per warp: one while the tokens are fewer than the GPU's warps (a decode
-// step: the latency of one row), four beyond (a prompt: more loads in flight).
-bool many_tokens(int64_t n) { return n > (int64_t)num_sms() * 32; }
-dim3 token_grid(int64_t n, int tokens) {
-    return dim3((unsigned)std::min<int64_t>(ceil_div(n, (int64_t)kWarpTokens * tokens),
-                                            (int64_t)num_sms() * 64));
+// Tokens per warp: one while the GPU has a warp for each (24 warps an SM; a decode
+// step: the latency of one row), then as many as keep one wave, up to 32.
+int32_t token_block(int64_t n) {
+    return (int32_t)std::min<int64_t>(kMaxBlock, ceil_div(n, (int64_t)num_sms() * 24));
+}
+dim3 token_grid(int64_t n, int32_t block) {
+    return dim3((unsigned)ceil_div(n, (int64_t)kWarpTokens * block));
 }
 
 template <int kKv>
@@ -525,11 +561,10 @@ cudaError_t launch_read_kv(const PathParams &p, int32_t n, const int32_t *seq, c
     const bool one = kKv == SA_BF16 || kKv == SA_F32;
     const bool wide = one ? (p.d_latent + p.d_rope) % 16 == 0
                           : p.d_latent % 16 == 0 && p.d_rope % 8 == 0;
-    const int tokens = many_tokens(n) ? 4 : 1;
-    const auto kernel = tokens == 4 ? (wide ? read_kernel<kKv, true, 4> : read_kernel<kKv, false, 4>)
-                                    : (wide ? read_kernel<kKv, true, 1> : read_kernel<kKv, false, 1>);
+    const int32_t block = token_block(n);
+    const auto kernel = wide ? read_kernel<kKv, true> : read_kernel<kKv, false>;
     count_launch();
-    kernel<<<token_grid(n, tokens), kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16);
+    kernel<<<token_grid(n, block), kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16, block);
     return cudaGetLastError();
 }
 
@@ -574,13 +609,10 @@ cudaError_t launch_quantize_rows(const void *in, sa_dtype in_dtype, int64_t n_ro
 
 template <int kKv>
 static void launch_append_fp4(const AppendParams &p, cudaStream_t s) {
-    const int tokens = many_tokens(p.n_new) ? 4 : 1;
-    const auto kernel =
-        p.in_bf16 ? (tokens == 4 ? append_fp4_kernel<kKv, true, 4> : append_fp4_kernel<kKv, true, 1>)
-                  : (tokens == 4 ? append_fp4_kernel<kKv, false, 4>
-                                 : append_fp4_kernel<kKv, false, 1>);
+    const int32_t block = token_block(p.n_new);
+    const auto kernel = p.in_bf16 ? append_fp4_kernel<kKv, true> : append_fp4_kernel<kKv, false>;
     count_launch();
-    kernel<<<token_grid(p.n_new, tokens), kWarpThreads, 0, s>>>(p);
+    kernel<<<token_grid(p.n_new, block), kWarpThreads, 0, s>>>(p, block);
 }
 
 cudaError_t launch_append(const AppendParams &params, cudaStream_t s) {
