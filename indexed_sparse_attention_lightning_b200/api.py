@@ -42,6 +42,8 @@ def _need(t, name: str, dtype=None, shape=None, optional: bool = False) -> None:
         if optional:
             return
         raise SaError(_abi.SA_ERR_INVALID_ARG, f"{name} is required")
+    if dtype is None and type(t) is torch.Tensor and t.is_cuda and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SaError(_abi.SA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
     if not t.is_contiguous():
@@ -84,8 +86,8 @@ def _need_here(where: str, *tensors) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle: a Stream object costs 3 us
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream
 
 
@@ -114,15 +116,14 @@ class DeviceCache:
         _need(self.seq_len, "seq_len", torch.int32)
         for name in ("k_index", "k_index_scale", "kv", "kv_rope", "kv_scale"):
             _need(getattr(self, name), name, optional=True)
+        # in the order of the struct's fields: by keyword the construction takes twice as long
         return SaCache(
-            page_table=_ptr(self.page_table), seq_len=_ptr(self.seq_len),
-            batch=self.page_table.shape[0], max_pages=self.page_table.shape[1],
-            num_pages=self.num_pages, page_size=self.page_size,
-            index_dtype=_abi.DTYPES[self.index_dtype], k_index=_ptr(self.k_index),
-            k_index_scale=_ptr(self.k_index_scale), d_index=self.d_index,
-            kv_dtype=_abi.DTYPES[self.kv_dtype], kv=_ptr(self.kv), kv_rope=_ptr(self.kv_rope),
-            kv_scale=_ptr(self.kv_scale), d_latent=self.d_latent, d_rope=self.d_rope,
-            kv_scale_tokens=int(self.kv_scale_tile[0]), kv_scale_dims=int(self.kv_scale_tile[1]))
+            _ptr(self.page_table), _ptr(self.seq_len), self.page_table.shape[0],
+            self.page_table.shape[1], self.num_pages, self.page_size,
+            _abi.DTYPES[self.index_dtype], _ptr(self.k_index), _ptr(self.k_index_scale),
+            self.d_index, _abi.DTYPES[self.kv_dtype], _ptr(self.kv), _ptr(self.kv_rope),
+            _ptr(self.kv_scale), self.d_latent, self.d_rope, int(self.kv_scale_tile[0]),
+            int(self.kv_scale_tile[1]))
 
 
 @dataclass
@@ -153,11 +154,9 @@ class DeviceQueries:
         for name in ("q_index", "q_index_scale", "w", "q"):
             _need(getattr(self, name), name, optional=True)
         return SaQuery(
-            n_q=self.n_q, q_seq=_ptr(self.q_seq), q_pos=_ptr(self.q_pos),
-            max_visible=self.max_visible, q_index=_ptr(self.q_index),
-            q_index_scale=_ptr(self.q_index_scale), w=_ptr(self.w), h_index=self.h_index,
-            q_dtype=_abi.DTYPES[self.q_dtype], q=_ptr(self.q), heads=self.heads,
-            sm_scale=self.sm_scale, q_group=self.q_group)
+            self.n_q, _ptr(self.q_seq), _ptr(self.q_pos), self.max_visible, _ptr(self.q_index),
+            _ptr(self.q_index_scale), _ptr(self.w), self.h_index, _abi.DTYPES[self.q_dtype],
+            _ptr(self.q), self.heads, self.sm_scale, self.q_group)
 
     def tensors(self) -> dict:
         return {"q_seq": self.q_seq, "q_pos": self.q_pos, "q_index": self.q_index,

@@ -82,6 +82,20 @@ __device__ __forceinline__ int32_t peer_word(const int32_t *p, int rank) {
     return v;
 }
 
+// The sum of such a word over CTAs [0, n) of the cluster of `ctas`, eight loads
+// in flight.
+__device__ __forceinline__ int32_t peer_sum(const int32_t *p, int n, int ctas) {
+    int32_t sum = 0;
+    for (int r0 = 0; r0 < n; r0 += 8) {
+        int32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = peer_word(p, min(r0 + i, ctas - 1));
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += r0 + i < n ? v[i] : 0;
+    }
+    return sum;
+}
+
 // A warp's positions [w0, w1) of a sequence, four consecutive ones per lane and
 // step.  keys() gives those of the middle part [lo, hi), and 0, which is no
 // value's key, for the others.
@@ -214,9 +228,7 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
             int32_t count = 0, inc = 0;
             if (tid < kSelectBins) {
                 const int32_t *d = &hist[pass][kSelectBins - 1 - tid];
-                if (ctas == 1) count = *d;
-                else
-                    for (int r = 0; r < ctas; ++r) count += peer_word(d, r);
+                count = ctas == 1 ? *d : peer_sum(d, ctas, ctas);
                 inc = count;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -286,10 +298,8 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     if (ctas > 1) cluster_sync();
     else __syncthreads();
     int32_t gt_before = gt_s[warp], eq_before = eq_s[warp];
-    for (int r = 0; r < rank; ++r) {
-        gt_before += peer_word(&totals[0], r);
-        eq_before += peer_word(&totals[1], r);
-    }
+    gt_before += peer_sum(&totals[0], rank, ctas);
+    eq_before += peer_sum(&totals[1], rank, ctas);
     if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
 
     // ascending emission: a warp's entries start behind all earlier ones that stay
@@ -323,9 +333,9 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
         for (int e = 0; e < 4; ++e) {
             if (!keep[e]) continue;
             const int32_t i = i0 + 4 * lane + e;
-            a.src_row[out0 + at] = st[i >> 6] * 64 + (i & 63);
+            a.src_row[out0 + at] = __ldg(st + (i >> 6)) * 64 + (i & 63);
             if (a.src_pos != nullptr) a.src_pos[out0 + at] = i;
-            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = acc[i];
+            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = __ldg(acc + i);
             ++at;
         }
     }
@@ -342,79 +352,81 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     }
 }
 
-// One warp moves `rows` consecutive kept tokens at a time.  The 16-byte pieces of
-// all their rows in all pools are dealt to the lanes, at most kMovePieces each,
-// and all loads are in flight before the first store; the next tokens' places
-// are looked up meanwhile.
-constexpr int kMovePieces = 10;
-__global__ void __launch_bounds__(kMoveThreads, 3)
-evict_move_kernel(const EvictArgs a, const EvictFields all_fields, int32_t pieces, int32_t rows) {
-    // in shared memory: the lanes of a warp index it differently
-    __shared__ EvictFields fields;
-    if (threadIdx.x == 0) fields = all_fields;
-    __syncthreads();
-    pdl_wait();
+// blockIdx.y: the sequence.  One warp moves `rows` consecutive kept tokens at a
+// time.  The 16-byte pieces of all their rows in all pools are dealt to the
+// lanes, at most kMovePieces each, and all loads are in flight before the first
+// store; the next tokens' places are looked up meanwhile.
+//
+// Many warps with few pieces each, in one wave: 64 sequences to 4096 bf16 tokens
+// (682 MB read and written) take 128 us with 3 pieces and 4 CTAs per SM, 5.3
+// TB/s; 145 with 8 and 2, 146 with 5 and 4, 150 with 3 and 6, and 142 with 3 and
+// as many waves as it takes.  Longer rows (over 96 pieces: fp32) take 10 pieces.
+template <int kMovePieces, int kMoveCtas>
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas)
+evict_move_kernel(const EvictArgs a, const EvictFields fields, int32_t pieces, int32_t rows) {
     const int lane = threadIdx.x & 31;
-    // this lane's pieces, packed: token of the group (32 and up: none), field, piece
-    uint32_t mine[kMovePieces];
+    // this lane's pieces: token of the group (none: 32), and where the piece lies
+    // in a pool's first row
+    int32_t token[kMovePieces], row_bytes[kMovePieces];
+    const uint8_t *src[kMovePieces];
+    uint8_t *dst[kMovePieces];
 #pragma unroll
     for (int j = 0; j < kMovePieces; ++j) {
-        const int32_t q = lane + 32 * j, row = q / pieces;
+        const int32_t q = lane + 32 * j;
         int32_t piece = q % pieces;
-        mine[j] = 32u;
-        for (int k = 0; k < fields.n; ++k) {
-            const EvictField &f = fields.f[k];
-            if (f.unit != 16) continue;
-            if (piece >= 0 && piece < f.units && row < rows)
-                mine[j] = (uint32_t)row | (uint32_t)k << 8 | (uint32_t)piece << 16;
-            piece -= f.units;
+        token[j] = 32;
+        row_bytes[j] = 0;
+        src[j] = nullptr;
+        dst[j] = nullptr;
+#pragma unroll
+        for (int k = 0; k < kMaxFields; ++k) {
+            if (k >= fields.n || fields.f[k].unit != 16) continue;
+            if (piece >= 0 && piece < fields.f[k].units && q / pieces < rows) {
+                token[j] = q / pieces;
+                row_bytes[j] = 16 * fields.f[k].units;
+                src[j] = fields.f[k].src + 16 * piece;
+                dst[j] = fields.f[k].dst + 16 * piece;
+            }
+            piece -= fields.f[k].units;
         }
     }
-    const int64_t groups = ceil_div(a.budget, rows);
-    const int64_t all = a.batch * groups;
-    const int64_t warps = (int64_t)gridDim.x * (kMoveThreads / 32);
-    // lane r of a group looks token r up
-    auto places = [&](int64_t g, int32_t &n, int32_t &from, int32_t &to) {
-        n = from = to = 0;
-        if (g >= all) return;
-        const int32_t b = (int32_t)(g / groups);
-        const int32_t i0 = (int32_t)(g % groups) * rows;
-        n = min(a.kept[b] - i0, rows);
-        if (lane >= n) return;
+    pdl_wait();
+    const int32_t b = blockIdx.y, kept = a.kept[b];
+    const int32_t *row_of = a.src_row + (int64_t)b * a.budget;
+    const int32_t *table = a.dst_table + (int64_t)b * a.dst_max_pages;
+    const int32_t step = gridDim.x * (kMoveThreads / 32) * rows;
+    // lane r looks token r of a group up
+    auto places = [&](int32_t i0, int32_t &from, int32_t &to) {
         const int32_t i = i0 + lane;
-        from = a.src_row[(int64_t)b * a.budget + i];
-        to = a.dst_table[(int64_t)b * a.dst_max_pages + (i >> 6)] * 64 + (i & 63);
+        from = to = 0;
+        if (lane >= rows || i >= kept) return;
+        from = row_of[i];
+        to = table[i >> 6] * 64 + (i & 63);
     };
-    int64_t g = (int64_t)blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5);
-    int32_t n, from, to;
-    places(g, n, from, to);
-    for (; g < all; g += warps) {
+    int32_t from, to;
+    int32_t i0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * rows;
+    places(i0, from, to);
+    for (; i0 < kept; i0 += step) {
+        const int32_t n = min(rows, kept - i0);
         uint4 x[kMovePieces];
 #pragma unroll
         for (int j = 0; j < kMovePieces; ++j) {
-            const int row = mine[j] & 255u;
-            const int64_t r = __shfl_sync(0xffffffffu, from, row & 31);
-            if (row < n) {
-                const EvictField &f = fields.f[(mine[j] >> 8) & 255u];
-                x[j] = __ldcs(reinterpret_cast<const uint4 *>(f.src) + r * f.units +
-                              (mine[j] >> 16));
-            }
+            const int64_t r = __shfl_sync(0xffffffffu, from, token[j] & 31);
+            if (token[j] < n)
+                x[j] = __ldcs(reinterpret_cast<const uint4 *>(src[j] + r * row_bytes[j]));
         }
-        int32_t n1, from1, to1;
-        places(g + warps, n1, from1, to1);
+        int32_t from1, to1;
+        places(i0 + step, from1, to1);
 #pragma unroll
         for (int j = 0; j < kMovePieces; ++j) {
-            const int row = mine[j] & 255u;
-            const int64_t r = __shfl_sync(0xffffffffu, to, row & 31);
-            if (row < n) {
-                const EvictField &f = fields.f[(mine[j] >> 8) & 255u];
-                __stcs(reinterpret_cast<uint4 *>(f.dst) + r * f.units + (mine[j] >> 16), x[j]);
-            }
+            const int64_t r = __shfl_sync(0xffffffffu, to, token[j] & 31);
+            if (token[j] < n) __stcs(reinterpret_cast<uint4 *>(dst[j] + r * row_bytes[j]), x[j]);
         }
         // rows that are not whole 16-byte pieces: a few small units each
-        for (int k = 0; k < fields.n; ++k) {
+#pragma unroll
+        for (int k = 0; k < kMaxFields; ++k) {
+            if (k >= fields.n || fields.f[k].unit == 16) continue;
             const EvictField &f = fields.f[k];
-            if (f.unit == 16) continue;
             for (int32_t u0 = 0; u0 < n * f.units; u0 += 32) {
                 const int32_t u = u0 + lane, r = u / f.units, c = u % f.units;
                 const int64_t s = (int64_t)__shfl_sync(0xffffffffu, from, r & 31) * f.units + c;
@@ -430,7 +442,6 @@ evict_move_kernel(const EvictArgs a, const EvictFields all_fields, int32_t piece
                     f.dst[d] = f.src[s];
             }
         }
-        n = n1;
         from = from1;
         to = to1;
     }
@@ -466,6 +477,18 @@ EvictFields make_fields(const sa_cache *s, const sa_cache *d) {
     return fs;
 }
 
+template <int kMovePieces, int kMoveCtas>
+cudaError_t launch_move(const EvictArgs &a, const EvictFields &fields, int32_t pieces,
+                        cudaStream_t s) {
+    const int32_t rows = std::min(32, std::max(1, 32 * kMovePieces / pieces));
+    const int64_t groups = ceil_div(ceil_div(a.budget, rows), kMoveThreads / 32);
+    const int64_t share = std::max(1, num_sms() * kMoveCtas / a.batch);
+    const dim3 grid((unsigned)std::min(groups, share), (unsigned)a.batch);
+    count_launch();
+    return launch_pdl(evict_move_kernel<kMovePieces, kMoveCtas>, grid, dim3(kMoveThreads), 0, s, a,
+                      fields, pieces, rows);
+}
+
 }  // namespace
 
 cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, int32_t budget,
@@ -496,16 +519,19 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     a.kept = reinterpret_cast<int32_t *>(base + evict_kept_offset(src->batch, budget));
     a.status = reinterpret_cast<int32_t *>(base);
     // CTAs per sequence: while they fill no more than the GPU, and each has at
-    // least 4096 positions
+    // least 4096 positions (64 sequences of 32K: 159 us with two, 171 with one; 2 of
+    // 256K: 54 us with sixteen, 64 with eight)
     const int64_t most = std::min(ld_acc, (int64_t)src->max_pages * 64);
     int32_t ctas = 1;
-    while (ctas < 8 && 2 * ctas * src->batch <= num_sms() && 2 * ctas * 4096 <= most) ctas *= 2;
+    while (ctas < 16 && 2 * ctas * src->batch <= num_sms() && 2 * ctas * 4096 <= most) ctas *= 2;
     const int64_t per = round_up(ceil_div(most, ctas * kSelectWarps), kSelectStep);
     const int32_t cache_per = per * kSelectWarps <= kSelectCached ? (int32_t)per : 0;
     const size_t smem = sizeof(uint32_t) * kSelectWarps * (size_t)cache_per;
     const auto select = cache_per > 0 ? evict_select_kernel<true> : evict_select_kernel<false>;
     cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          (int)smem);
+    if (e == cudaSuccess && ctas > 8)
+        e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(src->batch * ctas));
@@ -527,12 +553,8 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     for (int k = 0; k < fields.n; ++k)
         if (fields.f[k].unit == 16) pieces += fields.f[k].units;
     pieces = std::max(pieces, 1);
-    const int32_t rows = std::min(32, std::max(1, 32 * kMovePieces / pieces));
-    const int64_t groups = (int64_t)src->batch * ceil_div(budget, rows);
-    const dim3 grid((unsigned)std::min<int64_t>(ceil_div(groups, kMoveThreads / 32),
-                                                (int64_t)num_sms() * 3));
-    count_launch();
-    return launch_pdl(evict_move_kernel, grid, dim3(kMoveThreads), 0, s, a, fields, pieces, rows);
+    return pieces <= 96 ? launch_move<3, 4>(a, fields, pieces, s)
+                        : launch_move<10, 2>(a, fields, pieces, s);
 }
 
 }  // namespace sa

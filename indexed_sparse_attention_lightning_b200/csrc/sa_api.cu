@@ -599,7 +599,8 @@ sa_status sa_evict_tokens(const sa_cache *src, const float *acc, int64_t ld_acc,
         (int64_t)dst->max_pages * dst->page_size < budget || src->seq_len == dst->seq_len)
         return SA_ERR_INVALID_ARG;
     if (acc_out && (acc_out == acc || ld_out < budget)) return SA_ERR_INVALID_ARG;
-    if (!rows_fit_32(src) || !rows_fit_32(dst)) return SA_ERR_UNSUPPORTED;
+    if (!rows_fit_32(src) || !rows_fit_32(dst) || src->batch > kMaxQueries)
+        return SA_ERR_UNSUPPORTED;
     if ((st = check_workspace(workspace, workspace_bytes, evict_workspace(src, budget))) != SA_OK)
         return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -132,14 +132,14 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
     if constexpr (is_fp4(kKv)) {
         // Warp pw takes key pairs pw, pw + 8, pw + 16, pw + 24 of a tile, each half
         // of the warp one key; lane c of a half decodes dims 32c .. 32c + 31.  The
-        // four 16-byte pieces of a lane's dims go out in an order that differs
-        // between neighbouring 64-dim blocks, so that the 32 lanes of a store meet
-        // all banks alike.
+        // four 16-byte pieces of a lane's dims go out in an order that turns with
+        // the 64-dim block, so that each eight lanes of a store, which go together,
+        // meet all banks once.
         constexpr int kSlots = kTile / 2 / kFp4Warps;
         constexpr int kScales = 32 / fp4_group(kKv);  // scale bytes of a lane's dims
         const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale);
         const int half = lane >> 4, c = lane & 15;
-        const int flip = (c >> 1) & 1;
+        const int turn = (c >> 1) & 3, flip = turn >> 1;
         const int key = 2 * pw + half;  // of slot 0; slot i: key + 16 i
         uint2 code[kSlots][2];
         uint32_t sb[kSlots];
@@ -166,7 +166,7 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
         uint32_t piece[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            piece[j] = row_at + (c >> 1) * 1024 + (((4 * (c & 1) + (j ^ (2 * flip))) ^ sw) << 4);
+            piece[j] = row_at + (c >> 1) * 1024 + (((4 * (c & 1) + (j ^ turn)) ^ sw) << 4);
         // rope: 16-byte piece lane % 8 of keys 4 pw + lane / 8 and 32 more
         const int rk = 4 * pw + (lane >> 3);
         const uint32_t rope_at = (rk >> 3) * kGroupBytes + (kBlocks - 1) * 1024 + (rk & 7) * 128 +
@@ -210,10 +210,15 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
                 const __nv_bfloat162 b = __float2bfloat162_rn(fp4_scale_value(kKv, s1));
                 const uint32_t a2 = *reinterpret_cast<const uint32_t *>(&a);
                 const uint32_t b2 = *reinterpret_cast<const uint32_t *>(&b);
-                *reinterpret_cast<uint4 *>(dst + piece[0]) = fp4_to_bf16(code[i][0].x, a2);
-                *reinterpret_cast<uint4 *>(dst + piece[1]) = fp4_to_bf16(code[i][0].y, a2);
-                *reinterpret_cast<uint4 *>(dst + piece[2]) = fp4_to_bf16(code[i][1].x, b2);
-                *reinterpret_cast<uint4 *>(dst + piece[3]) = fp4_to_bf16(code[i][1].y, b2);
+                const bool swap = turn & 1;
+                const uint32_t w0 = swap ? code[i][0].y : code[i][0].x;
+                const uint32_t w1 = swap ? code[i][0].x : code[i][0].y;
+                const uint32_t w2 = swap ? code[i][1].y : code[i][1].x;
+                const uint32_t w3 = swap ? code[i][1].x : code[i][1].y;
+                *reinterpret_cast<uint4 *>(dst + piece[0]) = fp4_to_bf16(w0, a2);
+                *reinterpret_cast<uint4 *>(dst + piece[1]) = fp4_to_bf16(w1, a2);
+                *reinterpret_cast<uint4 *>(dst + piece[2]) = fp4_to_bf16(w2, b2);
+                *reinterpret_cast<uint4 *>(dst + piece[3]) = fp4_to_bf16(w3, b2);
             }
             *reinterpret_cast<uint4 *>(stage + rope_at) = rope_a;
             *reinterpret_cast<uint4 *>(stage + rope_at + 4 * kGroupBytes) = rope_b;

@@ -26,7 +26,7 @@
 // over it: every stage carries its own P, and the softmax of the next tile
 // never waits for P V of this one to release a shared P buffer.
 //
-// Roles (384 threads, 416 for a 4-bit latent; one CTA per SM):
+// Roles (384 threads, 672 for a 4-bit latent; one CTA per SM):
 //   warp 0     lane 0 loads Q by TMA (into the third ring stage; this copy
 //              starts before the wait on the top-K kernel), then issues
 //              the MMAs from a non-blocking loop -- S of a tile as soon as its
@@ -36,7 +36,7 @@
 //              in the addresses) into a 3-stage ring freed by each tile's P V;
 //              random 1152-byte rows reach shared memory fastest this way (an
 //              e4m3 or 4-bit latent is loaded, decoded to bf16 and stored, the
-//              4-bit one with warp 12's help);
+//              4-bit one with the help of warps 12-20);
 //   warps 8-11 move Q into TMEM, then run the online softmax.  Warp 8 + j
 //              owns heads 16j .. 16j + 15 and reads their S rows with 16-lane
 //              loads: thread i holds heads 16j + i/4 and 16j + i/4 + 8, keys
@@ -77,17 +77,44 @@ struct SfaSmem {
     // rows, each 8 x 128 bytes with the 128-byte swizzle (see kGroupBytes)
     uint8_t kv[kStages][kStageBytes];
     uint64_t kv_full[kStages], kv_empty[kStages];
-    // o_done: one phase per P V (a rescale waits for the previous tile's);
-    // o_final: once, after the last P V, for the final read of O (P V of the
-    // last two tiles may both be in flight then, which o_done's parity cannot
-    // tell apart)
-    uint64_t s_full[2], p_full[kStages], o_done, o_final, q_full, q_ready;
+    // kv_empty: one phase per P V of its stage, which frees the stage (and lets a
+    // rescale of the next tile at O); o_final: once, after the last P V, for the
+    // final read of O
+    uint64_t s_full[2], p_full[kStages], o_final, q_full, q_ready;
     uint32_t tmem_base;
     int abort;
 };
 
 static_assert(sizeof(SfaSmem) + 1024 <= 232448, "shared memory budget of one CTA");
 static_assert(kColS + 2 * kTile <= kTmemCols && kBlocks * 32 == (int)kColS, "TMEM columns");
+
+// Maximum over the four lanes of a row.
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 x, x, y;\n\t"
+        "mov.b64 {%0, %1}, x;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
 
 struct SfaArgs {
     PathParams p;
@@ -134,7 +161,6 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         }
         for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[b], 1);
         for (int s = 0; s < kStages; ++s) mbar_init(&sm.p_full[s], 4);  // the four softmax warps
-        mbar_init(&sm.o_done, 1);
         mbar_init(&sm.o_final, 1);
         mbar_init(&sm.q_full, 1);
         mbar_init(&sm.q_ready, 4);
@@ -204,6 +230,9 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         // The loop never leaves early: after a failed wait (a timeout raised
         // the abort flag) it keeps going without waiting or touching TMEM.
         const float sl2 = p.sm_scale * kLog2e;
+        // this lane's row of the P matrices it addresses
+        const uint32_t p_row = lane & 7, p_key = lane >> 3;
+        const uint32_t p_at = 2 * j * kGroupBytes + p_row * 128;
         float m_a = -INFINITY, m_b = -INFINITY, l_a = 0.f, l_b = 0.f;
         for (int n = 0; n < T; ++n) {
             const int sb = n & 1;
@@ -216,35 +245,73 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             }
             const int kvalid = ok ? n_valid - (j0 + n) * kTile : 0;
             float xa[16], xb[16];
+            float ta, tb;
+            if constexpr (is_fp4(kKv)) {
+                // The row maximum is taken of the raw sums (their minimum under a
+                // negative scale); scale and maximum are applied together below.
+                const float none = sl2 < 0.f ? INFINITY : -INFINITY;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    xa[2 * r + e] = __uint_as_float(v[4 * r + e]) * sl2;
-                    xb[2 * r + e] = __uint_as_float(v[4 * r + 2 + e]) * sl2;
+                for (int i = 0; i < 16; ++i) {
+                    xa[i] = __uint_as_float(v[4 * (i >> 1) + (i & 1)]);
+                    xb[i] = __uint_as_float(v[4 * (i >> 1) + 2 + (i & 1)]);
                 }
-            }
-            if (kvalid < kTile) {  // the last tile: mask the padding
+                if (kvalid < kTile) {  // the last tile: mask the padding
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const bool valid = 8 * (i >> 1) + 2 * q4 + (i & 1) < kvalid;
+                        xa[i] = valid ? xa[i] : none;
+                        xb[i] = valid ? xb[i] : none;
+                    }
+                }
+                ta = xa[0];
+                tb = xb[0];
+                if (sl2 < 0.f) {
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) {
+                        ta = fminf(ta, xa[i]);
+                        tb = fminf(tb, xb[i]);
+                    }
+                    ta = -quad_max(-ta) * sl2;
+                    tb = -quad_max(-tb) * sl2;
+                } else {
+#pragma unroll
+                    for (int i = 1; i < 16; ++i) {
+                        ta = fmaxf(ta, xa[i]);
+                        tb = fmaxf(tb, xb[i]);
+                    }
+                    ta = quad_max(ta) * sl2;
+                    tb = quad_max(tb) * sl2;
+                }
+            } else {
 #pragma unroll
                 for (int r = 0; r < 8; ++r) {
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const bool valid = 8 * r + 2 * q4 + e < kvalid;
-                        xa[2 * r + e] = valid ? xa[2 * r + e] : -INFINITY;
-                        xb[2 * r + e] = valid ? xb[2 * r + e] : -INFINITY;
+                        xa[2 * r + e] = __uint_as_float(v[4 * r + e]) * sl2;
+                        xb[2 * r + e] = __uint_as_float(v[4 * r + 2 + e]) * sl2;
                     }
                 }
-            }
-            float ta = xa[0], tb = xb[0];
+                if (kvalid < kTile) {  // the last tile: mask the padding
 #pragma unroll
-            for (int i = 1; i < 16; ++i) {
-                ta = fmaxf(ta, xa[i]);
-                tb = fmaxf(tb, xb[i]);
+                    for (int r = 0; r < 8; ++r) {
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const bool valid = 8 * r + 2 * q4 + e < kvalid;
+                            xa[2 * r + e] = valid ? xa[2 * r + e] : -INFINITY;
+                            xb[2 * r + e] = valid ? xb[2 * r + e] : -INFINITY;
+                        }
+                    }
+                }
+                ta = xa[0];
+                tb = xb[0];
+#pragma unroll
+                for (int i = 1; i < 16; ++i) {
+                    ta = fmaxf(ta, xa[i]);
+                    tb = fmaxf(tb, xb[i]);
+                }
+                ta = quad_max(ta);
+                tb = quad_max(tb);
             }
-            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 1));
-            ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, 2));
-            tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, 1));
-            tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, 2));
             // lazy rescaling: a running maximum moves only on a large jump
             const bool grow_a = ta > m_a + kRescaleLog2, grow_b = tb > m_b + kRescaleLog2;
             const float mn_a = grow_a ? ta : m_a, mn_b = grow_b ? tb : m_b;
@@ -252,36 +319,64 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             const float f_b = (grow_b && n > 0) ? exp2f(m_b - mn_b) : 1.f;
             uint32_t pa[8], pb[8];
             float la = 0.f, lb = 0.f;
+            if constexpr (is_fp4(kKv)) {
+                float2 sum_a = make_float2(0.f, 0.f), sum_b = sum_a;
+                const float2 scale = make_float2(sl2, sl2);
+                const float2 off_a = make_float2(-mn_a, -mn_a), off_b = make_float2(-mn_b, -mn_b);
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const float a0 = ex2(xa[2 * r] - mn_a), a1 = ex2(xa[2 * r + 1] - mn_a);
-                const float b0 = ex2(xb[2 * r] - mn_b), b1 = ex2(xb[2 * r + 1] - mn_b);
-                la += a0 + a1;
-                lb += b0 + b1;
-                __nv_bfloat162 x = __floats2bfloat162_rn(a0, a1);
-                __nv_bfloat162 y = __floats2bfloat162_rn(b0, b1);
-                pa[r] = *reinterpret_cast<uint32_t *>(&x);
-                pb[r] = *reinterpret_cast<uint32_t *>(&y);
+                for (int r = 0; r < 8; ++r) {
+                    float2 ya = fma2(make_float2(xa[2 * r], xa[2 * r + 1]), scale, off_a);
+                    float2 yb = fma2(make_float2(xb[2 * r], xb[2 * r + 1]), scale, off_b);
+                    if (kvalid < kTile) {  // a scale of 0 would leave the padding at 0
+                        const int k = 8 * r + 2 * q4;
+                        if (k >= kvalid) ya.x = yb.x = -INFINITY;
+                        if (k + 1 >= kvalid) ya.y = yb.y = -INFINITY;
+                    }
+                    ya = make_float2(ex2(ya.x), ex2(ya.y));
+                    yb = make_float2(ex2(yb.x), ex2(yb.y));
+                    sum_a = add2(sum_a, ya);
+                    sum_b = add2(sum_b, yb);
+                    const __nv_bfloat162 x = __floats2bfloat162_rn(ya.x, ya.y);
+                    const __nv_bfloat162 y = __floats2bfloat162_rn(yb.x, yb.y);
+                    pa[r] = *reinterpret_cast<const uint32_t *>(&x);
+                    pb[r] = *reinterpret_cast<const uint32_t *>(&y);
+                }
+                la = sum_a.x + sum_a.y;
+                lb = sum_b.x + sum_b.y;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 8; ++r) {
+                    const float a0 = ex2(xa[2 * r] - mn_a), a1 = ex2(xa[2 * r + 1] - mn_a);
+                    const float b0 = ex2(xb[2 * r] - mn_b), b1 = ex2(xb[2 * r + 1] - mn_b);
+                    la += a0 + a1;
+                    lb += b0 + b1;
+                    __nv_bfloat162 x = __floats2bfloat162_rn(a0, a1);
+                    __nv_bfloat162 y = __floats2bfloat162_rn(b0, b1);
+                    pa[r] = *reinterpret_cast<uint32_t *>(&x);
+                    pb[r] = *reinterpret_cast<uint32_t *>(&y);
+                }
             }
             // O belongs to P V of the previous tile until it is done: only a
             // rescale has to wait for it (P goes to this tile's own stage)
             const bool rescale = __any_sync(0xffffffffu, (grow_a || grow_b) && n > 0);
-            if (rescale && ok) ok = warp_wait(&sm.o_done, (n - 1) & 1, abort_flag, status);
+            if (rescale && ok)
+                ok = warp_wait(&sm.kv_empty[(n - 1) % kStages], ((n - 1) / kStages) & 1,
+                               abort_flag, status);
             if (ok && rescale) {
                 tc_fence_after();
 #pragma unroll 1
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t w[64];
-                    tmem_ld_16x256b_x16(tmem + lane_hi + 128 * c, w);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t w[32];
+                    tmem_ld_16x256b_x8(tmem + lane_hi + 64 * c, w);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) {
+                    for (int r = 0; r < 8; ++r) {
                         w[4 * r] = __float_as_uint(__uint_as_float(w[4 * r]) * f_a);
                         w[4 * r + 1] = __float_as_uint(__uint_as_float(w[4 * r + 1]) * f_a);
                         w[4 * r + 2] = __float_as_uint(__uint_as_float(w[4 * r + 2]) * f_b);
                         w[4 * r + 3] = __float_as_uint(__uint_as_float(w[4 * r + 3]) * f_b);
                     }
-                    tmem_st_16x256b_x16(tmem + lane_hi + 128 * c, w);
+                    tmem_st_16x256b_x8(tmem + lane_hi + 64 * c, w);
                 }
                 tmem_wait_st();
             }
@@ -289,15 +384,17 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             l_b = l_b * f_b + lb;
             m_a = mn_a;
             m_b = mn_b;
-            // P rows ha, hb: keys 8r + 2 q4 (+1) -> bytes 16r + 4 q4 of the row,
-            // in the rope block of this tile's stage (S has read it: s_full)
-            uint8_t *pbase = sm.kv[n % kStages] + kPOffset;
-            uint8_t *row_a = pbase + (ha >> 3) * kGroupBytes + (ha & 7) * 128 + 4 * q4;
-            uint8_t *row_b = pbase + (hb >> 3) * kGroupBytes + (hb & 7) * 128 + 4 * q4;
+            // P's heads 16j + 8h .. + 7, keys 8r .. 8r + 7 are an 8 x 8 matrix as
+            // the lanes hold it: four matrices per store, in the rope block of
+            // this tile's stage (S has read it: s_full)
+            const uint32_t pbase = smem_u32(sm.kv[n % kStages]) + kPOffset + p_at;
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                *reinterpret_cast<uint32_t *>(row_a + ((r ^ (ha & 7)) << 4)) = pa[r];
-                *reinterpret_cast<uint32_t *>(row_b + ((r ^ (hb & 7)) << 4)) = pb[r];
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t(&ph)[8] = h == 0 ? pa : pb;
+#pragma unroll
+                for (int r = 0; r < 8; r += 4)
+                    store_matrix_x4(pbase + h * kGroupBytes + (((r + p_key) ^ p_row) << 4), ph[r],
+                                    ph[r + 1], ph[r + 2], ph[r + 3]);
             }
             fence_proxy_async_smem();
             tc_fence_before();
@@ -333,13 +430,8 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                 for (int i = 0; i < 32; ++i) v[i] = 0.f;
             }
             if (!o_lane) continue;
-            if constexpr (is_fp4(kKv)) {  // back into the order of dims
-                float u[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) u[i] = v[fp4_place(i)];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = u[i];
-            }
+            // column c of a 4-bit latent's output holds the dim whose place is c
+            auto o_at = [&](int i) { return v[is_fp4(kKv) ? fp4_place(i) : i] * inv_o; };
             const int dv = 32 * c;
             if (a.splits == 1) {
                 if (a.out_dtype == SA_BF16) {
@@ -347,7 +439,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
 #pragma unroll
                     for (int i = 0; i < 32; i += 2) {
                         __nv_bfloat162 b2 =
-                            __floats2bfloat162_rn(v[i] * inv_o, v[i + 1] * inv_o);
+                            __floats2bfloat162_rn(o_at(i), o_at(i + 1));
                         w[i / 2] = *reinterpret_cast<uint32_t *>(&b2);
                     }
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
@@ -360,16 +452,16 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                         reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kDl + dv);
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(v[4 * i] * inv_o, v[4 * i + 1] * inv_o,
-                                             v[4 * i + 2] * inv_o, v[4 * i + 3] * inv_o);
+                        dst[i] = make_float4(o_at(4 * i), o_at(4 * i + 1), o_at(4 * i + 2),
+                                             o_at(4 * i + 3));
                 }
             } else {
                 const int64_t prow_i = ((int64_t)t * a.splits + split) * 128 + head;
                 float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow_i * kDl + dv);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
-                    dst[i] = make_float4(v[4 * i] * inv_o, v[4 * i + 1] * inv_o,
-                                         v[4 * i + 2] * inv_o, v[4 * i + 3] * inv_o);
+                    dst[i] = make_float4(o_at(4 * i), o_at(4 * i + 1), o_at(4 * i + 2),
+                                         o_at(4 * i + 3));
             }
         }
         if (q4 == 0) {
@@ -396,79 +488,56 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                           sm.kv, sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
     } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
-        // Lane 0 polls, the whole warp computes descriptors, one elected lane
-        // issues.
+        // The whole warp waits and computes descriptors, one elected lane issues.
+        // S of the next tile goes out before P V of this one, so that the tensor
+        // pipe works while the softmax does; the two then alternate.
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
-        auto ready = [&](uint64_t *bar, uint32_t parity) -> bool {
-            const bool done = lane == 0 && mbar_test(bar, parity);
-            return __shfl_sync(0xffffffffu, done ? 1 : 0, 0) != 0;
-        };
         constexpr uint32_t id_s = instr_desc(64, kTile, 1 /*bf16*/, 0, 0);
         constexpr uint32_t id_pv = instr_desc(64, 256, 1 /*bf16*/, 0, 1);
         bool ok = warp_wait(&sm.q_ready, 0, abort_flag, status);
-        int ns = 0, np = 0;  // next S and next P V to issue
-        // P V(np) needs P of tile np
-        auto try_pv = [&]() -> bool {
-            const int st = np % kStages;
-            if (!(np < ns && ready(&sm.p_full[st], (np / kStages) & 1))) return false;
-            __syncwarp();
-            tc_fence_after();  // P's writers have fenced for the tensor core
-            const uint64_t ad = desc_kmajor_sw128_sbo(smem_u32(sm.kv[st]) + kPOffset, kGroupBytes);
-            if (elect_one()) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    const uint32_t vb = smem_u32(sm.kv[st]) + 4 * half * 1024;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)  // 16 keys (two groups) per instruction
-                        mma_bf16(tm + (kLaneO << 16) + 256 * half, ad + 2 * k,
-                                 desc_mnmajor_sw128(vb + 2 * k * kGroupBytes, 1024, kGroupBytes),
-                                 id_pv, (np > 0 || k > 0) ? 1u : 0u);
-                }
-                mma_commit(&sm.o_done);
-                if (np + kStages < T) mma_commit(&sm.kv_empty[st]);
-            }
-            __syncwarp();
-            ++np;
-            return true;
-        };
-        long long t0 = clock64();
-        uint32_t idle = 0;
-        while (ok && np < T) {
-            bool progressed = false;
-            // S(ns) needs its rows and a free S buffer: the softmax of tile
-            // ns - 2 is over once P V of it was issued
-            if (ns < T && ns < np + 2) {
-                const int st = ns % kStages;
-                if (ready(&sm.kv_full[st], (ns / kStages) & 1)) {
-                    __syncwarp();
-                    if constexpr (kKv == SA_BF16) fence_proxy_async_smem();  // cp.async rows
-                    tc_fence_after();
-                    const uint32_t d = tm + kColS + kTile * (ns & 1);
-                    const uint32_t stage = smem_u32(sm.kv[st]);
-                    if (elect_one()) {
+        for (int n = 0; ok && n <= T; ++n) {
+            if (n < T) {  // S(n): its S buffer is free since P V (n - 2) was issued
+                const int st = n % kStages;
+                ok = warp_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
+                if (!ok) break;
+                if constexpr (kKv == SA_BF16) fence_proxy_async_smem();  // cp.async rows
+                tc_fence_after();
+                const uint32_t d = tm + kColS + kTile * (n & 1);
+                const uint32_t stage = smem_u32(sm.kv[st]);
+                if (elect_one()) {
 #pragma unroll  // 36 MMAs straight-line: measured faster than a loop over the blocks
-                        for (int b = 0; b < kBlocks; ++b) {
-                            const uint64_t bd =
-                                desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
+                    for (int b = 0; b < kBlocks; ++b) {
+                        const uint64_t bd = desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)  // 16 dims (32 bytes) per instruction
-                                mma_bf16_ts(d, tm + kColQ + 32 * b + 8 * k, bd + 2 * k, id_s,
-                                            (b | k) != 0);
-                        }
-                        mma_commit(&sm.s_full[ns & 1]);
+                        for (int k = 0; k < 4; ++k)  // 16 dims (32 bytes) per instruction
+                            mma_bf16_ts(d, tm + kColQ + 32 * b + 8 * k, bd + 2 * k, id_s,
+                                        (b | k) != 0);
                     }
-                    __syncwarp();
-                    ++ns;
-                    progressed = true;
+                    mma_commit(&sm.s_full[n & 1]);
                 }
+                __syncwarp();
             }
-            if (try_pv()) progressed = true;
-            if (progressed) {
-                t0 = clock64();
-                idle = 0;
-            } else if ((++idle & 63) == 0) {
-                const bool stop = lane == 0 && wait_expired(t0, abort_flag, status);
-                if (__shfl_sync(0xffffffffu, stop ? 1 : 0, 0) != 0) break;
+            if (n > 0) {  // P V (n - 1)
+                const int np = n - 1, st = np % kStages;
+                const uint32_t stage = smem_u32(sm.kv[st]);
+                const uint64_t ad = desc_kmajor_sw128_sbo(stage + kPOffset, kGroupBytes);
+                ok = warp_wait(&sm.p_full[st], (np / kStages) & 1, abort_flag, status);
+                if (!ok) break;
+                tc_fence_after();  // P's writers have fenced for the tensor core
+                if (elect_one()) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)  // 16 keys (two groups) per instruction
+                            mma_bf16(tm + (kLaneO << 16) + 256 * half, ad + 2 * k,
+                                     desc_mnmajor_sw128(stage + 4 * half * 1024 +
+                                                            2 * k * kGroupBytes,
+                                                        1024, kGroupBytes),
+                                     id_pv, (np > 0 || k > 0) ? 1u : 0u);
+                    }
+                    mma_commit(&sm.kv_empty[st]);
+                }
+                __syncwarp();
             }
         }
         // o_final: every MMA issued above (all P V of the tiles) has completed;

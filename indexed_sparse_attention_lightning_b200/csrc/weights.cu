@@ -145,7 +145,7 @@ cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t l
 // once per query, and a stage is free again as soon as its S is done.
 //   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2,
 //               before the wait on the rows kernel), then issues the MMAs;
-//   warps 1-7   gather the rows (sfa_gather.cuh; warp 12 too for a 4-bit latent);
+//   warps 1-7   gather the rows (sfa_gather.cuh; with warps 12-20 for a 4-bit latent);
 //   warps 8-11  move Q into TMEM (warp 8 + j: heads 32j .. 32j + 31, one per
 //               lane), then read S with 16-lane loads, so that a thread holds
 //               four heads of sixteen keys: exp2 of the logits minus the heads'
