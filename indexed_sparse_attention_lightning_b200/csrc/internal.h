@@ -130,18 +130,17 @@ cudaError_t launch_topk_hist(const float *scores, int64_t ld, const int32_t *vis
 cudaError_t launch_attn_simt(const PathParams &p, const int32_t *idx, int32_t top_k, void *out,
                              int32_t out_dtype, float *lse, cudaStream_t s);
 
-// Tensor-core sparse attention (bf16 cache and query, 128 heads, 512 + 64
-// dims, K <= 2048): a compaction kernel turns the selected positions into
-// physical rows (rows [n_q, sfa_rows_ld(K)], n_valid [n_q]; skipped when
-// `rows_ready`, i.e. the top-K kernel already wrote them), then one CTA per
-// 64 heads of a query and key split; with `splits` > 1 the partial outputs go
-// to o_part [n_q, splits, 128, 512] / lse_part [n_q, splits, 128] and a third
-// kernel merges them.
+// Tensor-core sparse attention (bf16 query, 128 heads, 512 + 64 dims, K <= 2048):
+// one CTA per 64 heads of a query and key split, over the physical rows of its
+// selection: `rows` [n_q, sfa_rows_ld(K)] and n_valid [n_q] from the top-K
+// kernel, or, where rows is null, compacted from idx [n_q, K] by each CTA
+// itself.  With `splits` > 1 the partial outputs go to o_part [n_q, splits, 128,
+// 512] / lse_part [n_q, splits, 128] and a second kernel merges them.
 bool sfa_mma_supported(const PathParams &p, int32_t top_k);
 int32_t sfa_splits(int32_t n_q, int32_t top_k);
 int32_t sfa_rows_ld(int32_t top_k);
 cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_k, int32_t splits,
-                           int32_t *rows, int32_t *n_valid, bool rows_ready, void *out,
+                           const int32_t *rows, const int32_t *n_valid, void *out,
                            int32_t out_dtype, float *lse, float *o_part, float *lse_part,
                            cudaStream_t s);
 
@@ -265,12 +264,13 @@ __device__ __forceinline__ void compact_rows(const PathParams &p, int32_t t, con
     if (threadIdx.x == 0) *n_valid = base;
 }
 
-// compact_rows for the kernels that do nothing else: a thread takes four
-// entries of a step (one of each quarter), whose loads are all in flight at
-// once, and one scan over the warps' counts places them (2048 entries by 512
-// threads: 9 instead of 11 us with cold caches).  With `kept` it also writes
-// the positions behind rows[0, *n_valid).  `scratch`: kCompactScratch ints.
-constexpr int kCompactScratch = 4 * 32 + 2;
+// compact_rows with more loads in flight: a thread takes kEntries entries of a
+// step, blockDim.x apart, and one scan over the warps' counts places them (2048
+// entries by 512 threads, four each: 9 instead of 11 us with cold caches).  With
+// `kept` it also writes the positions behind rows[0, *n_valid).  `scratch`:
+// kCompactScratch ints; kEntries times the warps of the CTA are at most 128.
+constexpr int kCompactScratch = 128 + 2;
+template <int kEntries>
 __device__ __forceinline__ void compact_selection(const PathParams &p, int32_t t,
                                                   const int32_t *sel, int32_t K, int32_t tile,
                                                   int32_t *rows, int32_t *n_valid,
@@ -280,24 +280,24 @@ __device__ __forceinline__ void compact_selection(const PathParams &p, int32_t t
     const bool seq_ok = seq >= 0 && seq < p.batch;
     int32_t V = -1;  // known after the first loads are on their way
     int32_t base = 0;
-    for (int64_t r0 = 0; r0 < K; r0 += 4 * blockDim.x) {
-        int32_t s[4], v[4];
+    for (int64_t r0 = 0; r0 < K; r0 += kEntries * blockDim.x) {
+        int32_t s[kEntries], v[kEntries];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kEntries; ++j) {
             const int64_t k = r0 + j * blockDim.x + threadIdx.x;
             s[j] = k < K ? sel[k] : -1;
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kEntries; ++j) {
             v[j] = -1;
             if (s[j] >= 0 && seq_ok)
                 v[j] = static_cast<int32_t>(
                     phys_row(p.page_table, p.max_pages, p.num_pages, seq, s[j]));
         }
         if (V < 0) V = visible_len(p, t);
-        unsigned bal[4];
+        unsigned bal[kEntries];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kEntries; ++j) {
             if (s[j] >= V) {
                 report(p.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_INDEX);
                 v[j] = -1;
@@ -308,11 +308,12 @@ __device__ __forceinline__ void compact_selection(const PathParams &p, int32_t t
             if (lane == 0) scratch[j * nwarps + w] = __popc(bal[j]);
         }
         __syncthreads();
-        if (w == 0) {  // exclusive scan of 4 * nwarps counts, four per lane
+        if (w == 0) {  // exclusive scan of the counts, four per lane
+            const int counts = kEntries * nwarps;
             int32_t c[4], sum = 0;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                c[i] = 4 * lane + i < 4 * nwarps ? scratch[4 * lane + i] : 0;
+                c[i] = 4 * lane + i < counts ? scratch[4 * lane + i] : 0;
                 sum += c[i];
             }
             int32_t inc = sum;
@@ -324,14 +325,14 @@ __device__ __forceinline__ void compact_selection(const PathParams &p, int32_t t
             int32_t at = inc - sum;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if (4 * lane + i < 4 * nwarps) scratch[4 * lane + i] = at;
+                if (4 * lane + i < counts) scratch[4 * lane + i] = at;
                 at += c[i];
             }
             if (lane == 31) scratch[128] = inc;
         }
         __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < kEntries; ++j) {
             if (v[j] >= 0) {
                 const int32_t pos =
                     base + scratch[j * nwarps + w] + __popc(bal[j] & ((1u << lane) - 1u));

@@ -151,15 +151,15 @@ PathParams make_params(const sa_cache *c, const sa_query *q, void *ws) {
 // | hist [n_q, 4096] | counts [n_q, 2] | sel [n_q, K] | cand [n_q, cap]
 // | chunk_info [n_q, C] | rows [n_q, R] | n_valid [n_q] | o_part [n_q, S, 128, 512]
 // | lse_part [n_q, S, 128]; the indexer needs the first three, the fused path
-// all of them; the attention alone needs the status, the compacted rows and
-// the split-KV partials (placed right after the status).
+// all of them; the attention alone needs the status and the split-KV partials
+// (placed right after the status).
 struct Layout {
     int64_t ld;
     int32_t splits;
     size_t vis, tile_end, scores, idx, hist, counts, sel, cand, chunk_info, rows, n_valid, o_part,
         lse_part;
     size_t indexer_total, decode_total;
-    size_t attn_rows, attn_n_valid, attn_o_part, attn_lse_part, attn_total;
+    size_t attn_o_part, attn_lse_part, attn_total;
     // accumulated weights: status | rows | kept | w [n_q, weights_ld] each |
     // n_valid [n_q] | starts [n_q, weights_starts_ld]
     size_t wt_rows, wt_kept, wt_w, wt_n_valid, wt_starts, wt_total;
@@ -193,9 +193,7 @@ Layout make_layout(const sa_query *q, int32_t top_k, int32_t batch) {
     l.o_part = align_up(l.n_valid + sizeof(int32_t) * nq);
     l.lse_part = align_up(l.o_part + o_bytes);
     l.decode_total = align_up(l.lse_part + lse_bytes);
-    l.attn_rows = align_up(kStatusBytes);
-    l.attn_n_valid = align_up(l.attn_rows + rows_bytes);
-    l.attn_o_part = align_up(l.attn_n_valid + sizeof(int32_t) * nq);
+    l.attn_o_part = align_up(kStatusBytes);
     l.attn_lse_part = align_up(l.attn_o_part + o_bytes);
     l.attn_total = align_up(l.attn_lse_part + lse_bytes);
     const size_t wt_bytes = 4 * nq * (size_t)weights_ld(top_k);
@@ -237,9 +235,9 @@ sa_status run_attention(const PathParams &p, const Layout &l, bool fused, bool r
         char *base = static_cast<char *>(ws);
         return cuda_status(launch_sfa_mma(
             p, idx, top_k, l.splits,
-            reinterpret_cast<int32_t *>(base + (fused ? l.rows : l.attn_rows)),
-            reinterpret_cast<int32_t *>(base + (fused ? l.n_valid : l.attn_n_valid)), rows_ready,
-            out, out_dtype, lse, reinterpret_cast<float *>(base + (fused ? l.o_part : l.attn_o_part)),
+            rows_ready ? reinterpret_cast<const int32_t *>(base + l.rows) : nullptr,
+            rows_ready ? reinterpret_cast<const int32_t *>(base + l.n_valid) : nullptr, out,
+            out_dtype, lse, reinterpret_cast<float *>(base + (fused ? l.o_part : l.attn_o_part)),
             reinterpret_cast<float *>(base + (fused ? l.lse_part : l.attn_lse_part)), s));
     }
     return cuda_status(launch_attn_simt(p, idx, top_k, out, out_dtype, lse, s));

@@ -103,7 +103,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 }
 
 // Row producers (kProducerWarps or, for 4 bits, kFp4Warps warps): tiles
-// 0 .. T - 1 of tile_rows (physical rows, whole tiles) go through the ring.
+// 0 .. T - 1 of tile_rows (physical rows, whole tiles, in global or shared
+// memory) go through the ring.
 // Stage `q_stage` and those behind it hold Q until q_ready completes.
 //
 // The ring holds about one tile in flight per SM, too little to cover the
@@ -157,8 +158,8 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             }
         };
         auto row_pair = [&](int n, int32_t &lo, int32_t &hi) {
-            lo = n < T ? __ldg(tile_rows + n * kTile + lane) : 0;
-            hi = n < T ? __ldg(tile_rows + n * kTile + 32 + lane) : 0;
+            lo = n < T ? tile_rows[n * kTile + lane] : 0;
+            hi = n < T ? tile_rows[n * kTile + 32 + lane] : 0;
         };
         // where this lane's pieces go in slot 0's row; slot i is 2 i groups on
         const int sw = key & 7;
@@ -259,8 +260,8 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             }
         };
         auto row_pair = [&](int n, int32_t &lo, int32_t &hi) {
-            lo = n < T ? __ldg(tile_rows + n * kTile + lane) : 0;
-            hi = n < T ? __ldg(tile_rows + n * kTile + 32 + lane) : 0;
+            lo = n < T ? tile_rows[n * kTile + lane] : 0;
+            hi = n < T ? tile_rows[n * kTile + 32 + lane] : 0;
         };
         int32_t r_lo, r_hi, lo1, hi1;
         row_pair(0, r_lo, r_hi);

@@ -28,10 +28,9 @@
 //
 // Roles (384 threads, 672 for a 4-bit latent; one CTA per SM):
 //   warp 0     lane 0 loads Q by TMA (into the third ring stage; this copy
-//              starts before the wait on the top-K kernel), then issues
-//              the MMAs from a non-blocking loop -- S of a tile as soon as its
-//              rows are in and an S buffer is free, P V as soon as P is
-//              written -- and commits them to mbarriers;
+//              starts before the wait on the top-K kernel); then the warp
+//              issues the MMAs, S of tile n + 1 before P V of tile n, and
+//              commits them to mbarriers;
 //   warps 1-7  copy the selected rows (16-byte cp.async, the swizzle applied
 //              in the addresses) into a 3-stage ring freed by each tile's P V;
 //              random 1152-byte rows reach shared memory fastest this way (an
@@ -46,9 +45,10 @@
 //              same thread-to-head mapping, leaving Q and S alone) only when a
 //              head's running maximum grows by more than 2^8; finally lanes
 //              16-31 read O with 32-lane loads and write O / l.
-// Selected positions are turned into physical cache rows by a small kernel
-// first (sfa_rows_kernel).  All waits are bounded; a timeout is reported in
-// the workspace status word.
+// The fused decode gets the selection's physical rows from the top-K kernel;
+// otherwise every CTA turns its query's positions into rows itself, in shared
+// memory, while Q is on its way (a kernel in front of this one took 9 us).  All
+// waits are bounded; a timeout is reported in the workspace status word.
 #include "common.cuh"
 #include "internal.h"
 #include "sfa_gather.cuh"
@@ -83,6 +83,8 @@ struct SfaSmem {
     uint64_t s_full[2], p_full[kStages], o_final, q_full, q_ready;
     uint32_t tmem_base;
     int abort;
+    int32_t n_valid, scratch[kCompactScratch];
+    int32_t rows[kMaxK];  // the selection's physical rows, whole tiles
 };
 
 static_assert(sizeof(SfaSmem) + 1024 <= 232448, "shared memory budget of one CTA");
@@ -118,9 +120,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 
 struct SfaArgs {
     PathParams p;
-    const int32_t *rows;     // [n_q, ld_rows] physical rows, padded to whole tiles
-    const int32_t *n_valid;  // [n_q]
+    const int32_t *rows;     // [n_q, ld_rows] physical rows, padded to whole tiles, or null
+    const int32_t *n_valid;  // [n_q] with rows
     int32_t ld_rows;
+    const int32_t *idx;      // [n_q, top_k] selected positions, without rows
+    int32_t top_k;
     int32_t splits;
     void *out;               // [n_q, 128, 512] (splits == 1)
     int32_t out_dtype;
@@ -128,20 +132,6 @@ struct SfaArgs {
     float *o_part;           // [n_q, splits, 128, 512] (splits > 1)
     float *lse_part;         // [n_q, splits, 128]      (splits > 1)
 };
-
-// Query t's selected positions -> physical cache rows (compact_selection): one
-// CTA per query.  The fused decode path gets the rows from the top-K kernel.
-constexpr int kRowsThreads = 512;
-__global__ void __launch_bounds__(kRowsThreads)
-sfa_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, int32_t ld_rows,
-                int32_t *__restrict__ rows, int32_t *__restrict__ n_valid_out) {
-    pdl_wait();
-    pdl_trigger();
-    __shared__ int32_t scratch[kCompactScratch];
-    const int t = blockIdx.x;
-    compact_selection(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld_rows,
-                      n_valid_out + t, scratch);
-}
 
 template <int kKv>  // sa_dtype of the latent cache
 __global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
@@ -180,11 +170,20 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             tma_load_2d(sm.kv[2] + b * (kHeadsCta * 128), &tm_q, 64 * b, t * 128 + kHeadsCta * hh,
                         &sm.q_full);
     }
-    pdl_wait();  // the selected rows come from the top-K kernel
+    pdl_wait();  // the selection comes from the kernel before
+    const int32_t *rows = sm.rows;
+    if (a.rows != nullptr) {
+        rows = a.rows + (int64_t)t * a.ld_rows;
+        if (threadIdx.x == 0) sm.n_valid = a.n_valid[t];
+    } else {  // 384 threads or more: one step
+        compact_selection<6>(p, t, a.idx + (int64_t)t * a.top_k, a.top_k, kTile, sm.rows,
+                             &sm.n_valid, sm.scratch);
+    }
+    __syncthreads();
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort;
     int32_t *status = p.status;
-    const int32_t n_valid = a.n_valid[t];
+    const int32_t n_valid = sm.n_valid;
     int32_t j0, j1;
     split_range(n_valid, split, a.splits, j0, j1);
     const int T = j1 - j0;
@@ -483,8 +482,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     } else if (warp >= 1) {
         // ---------------------------------------------- row producers ---
         // ring stage 2 holds Q until the softmax warps have moved it to TMEM
-        produce_rows<kKv>(p, a.rows + (int64_t)t * a.ld_rows + (int64_t)j0 * kTile, T,
-                          producer_index(warp),
+        produce_rows<kKv>(p, rows + j0 * kTile, T, producer_index(warp),
                           sm.kv, sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
     } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
@@ -637,22 +635,16 @@ int32_t sfa_splits(int32_t n_q, int32_t top_k) {
 int32_t sfa_rows_ld(int32_t top_k) { return (int32_t)round_up(top_k > 0 ? top_k : 1, kTile); }
 
 cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_k, int32_t splits,
-                           int32_t *rows, int32_t *n_valid, bool rows_ready, void *out,
+                           const int32_t *rows, const int32_t *n_valid, void *out,
                            int32_t out_dtype, float *lse, float *o_part, float *lse_part,
                            cudaStream_t s) {
     if (p.n_q == 0) return cudaSuccess;
-    const int32_t ld_rows = sfa_rows_ld(top_k);
     cudaError_t e;
-    if (!rows_ready) {
-        count_launch();
-        e = launch_pdl(sfa_rows_kernel, dim3(static_cast<unsigned>(p.n_q)), dim3(kRowsThreads), 0,
-                       s, p, idx, top_k, ld_rows, rows, n_valid);
-        if (e != cudaSuccess) return e;
-    }
     CUtensorMap tq;
     if (!encode_tmap_2d(&tq, 2, p.q, kD, (uint64_t)p.n_q * 128, kD * 2, 64, kHeadsCta, true))
         return cudaErrorInvalidValue;
-    SfaArgs a{p, rows, n_valid, ld_rows, splits, out, out_dtype, lse, o_part, lse_part};
+    SfaArgs a{p,     rows, n_valid,   sfa_rows_ld(top_k), idx,    top_k,
+              splits, out,  out_dtype, lse,                o_part, lse_part};
     const size_t smem = sizeof(SfaSmem) + 1024;
     const auto kernel = p.kv_dtype == SA_BF16    ? sfa_mma_kernel<SA_BF16>
                         : p.kv_dtype == SA_E4M3  ? sfa_mma_kernel<SA_E4M3>
