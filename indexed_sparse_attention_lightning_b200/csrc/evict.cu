@@ -4,7 +4,7 @@
 // Of a sequence of n > budget tokens the first F, the last R and, between
 // them, the budget - F - R positions with the largest acc stay (ties to the
 // lower position).  Two kernels:
-//   select  one CTA, or a cluster of up to eight, per sequence: its positions'
+//   select  one CTA, or a cluster of up to sixteen, per sequence: its positions'
 //           acc in shared memory where they fit, the threshold of the middle
 //           part by an exact radix select on order-preserving keys (four 8-bit
 //           digits; the CTAs' histograms are added through distributed shared
@@ -47,7 +47,8 @@ struct EvictArgs {
     int32_t *src_pos;  // may be null
     int32_t *src_row;  // [batch, budget]
     int32_t *kept;     // [batch]
-    int32_t *status;
+    int32_t *fault;    // [batch]: SA_DETAIL_* of a skipped sequence, or 0
+    int32_t *status;   // written by the move kernel, from `fault`
 };
 
 // One pool's rows: `units` pieces of `unit` bytes (16, 8, 4, 2 or 1).
@@ -185,10 +186,8 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
         (int32_t)min(begin, (int64_t)span), (int32_t)min(begin + per, (int64_t)span), lo, hi, lane};
     if (want > 0) mine.fill();
     bad = __syncthreads_or(bad);
-    if (tid == 0 && rank == 0) {
-        if (!fits) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
-        if (bad) report(a.status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
-    }
+    if (tid == 0 && rank == 0)
+        a.fault[b] = !fits ? SA_DETAIL_BAD_POSITION : bad ? SA_DETAIL_BAD_PAGE : SA_DETAIL_NONE;
     const int32_t kept = bad ? 0 : min(span, a.budget);
 
     uint32_t threshold = 0xFFFFFFFFu;
@@ -392,6 +391,19 @@ evict_move_kernel(const EvictArgs a, const EvictFields fields, int32_t pieces, i
     }
     pdl_wait();
     const int32_t b = blockIdx.y, kept = a.kept[b];
+    // the status word: the first skipped sequence's fault
+    if (blockIdx.x == 0 && b == 0 && threadIdx.x < 32) {
+        int32_t first = a.batch;
+        for (int32_t i = lane; i < a.batch && first == a.batch; i += 32)
+            if (a.fault[i] != SA_DETAIL_NONE) first = i;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+        if (lane == 0) {
+            a.status[0] = first < a.batch ? SA_ERR_DEVICE_FAULT : SA_OK;
+            a.status[1] = first < a.batch ? a.fault[first] : SA_DETAIL_NONE;
+        }
+    }
     const int32_t *row_of = a.src_row + (int64_t)b * a.budget;
     const int32_t *table = a.dst_table + (int64_t)b * a.dst_max_pages;
     const int32_t step = gridDim.x * (kMoveThreads / 32) * rows;
@@ -517,6 +529,7 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     a.src_pos = src_pos;
     a.src_row = reinterpret_cast<int32_t *>(base + kStatusBytes);
     a.kept = reinterpret_cast<int32_t *>(base + evict_kept_offset(src->batch, budget));
+    a.fault = a.kept + src->batch;
     a.status = reinterpret_cast<int32_t *>(base);
     // CTAs per sequence: while they fill no more than the GPU, and each has at
     // least 4096 positions (64 sequences of 32K: 159 us with two, 171 with one; 2 of

@@ -12,7 +12,7 @@
 namespace sa {
 
 // Workspace of sa_evict_tokens: status | src_row int32 [batch, budget] |
-// kept int32 [batch].
+// kept int32 [batch] | fault int32 [batch].
 inline size_t evict_kept_offset(int32_t batch, int32_t budget) {
     return kStatusBytes + (size_t)round_up((int64_t)batch * budget * 4, 256);
 }

@@ -316,17 +316,43 @@ __device__ __forceinline__ void store_values(void *dst, int64_t i, bool bf16,
     }
 }
 
-// Physical row of a token, or -1 after reporting why it has none.
+// Physical row of a token, or -1 and why it has none.
 __device__ __forceinline__ int64_t token_row(const int32_t *page_table, int32_t batch,
                                              int32_t max_pages, int32_t num_pages, int32_t seq,
-                                             int32_t pos, int32_t *status, bool reporter) {
-    if (seq < 0 || seq >= batch || pos < 0 || (pos >> 6) >= max_pages) {
-        if (reporter) report(status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_POSITION);
-        return -1;
-    }
+                                             int32_t pos, int32_t &detail) {
+    detail = SA_DETAIL_BAD_POSITION;
+    if (seq < 0 || seq >= batch || pos < 0 || (pos >> 6) >= max_pages) return -1;
     const int64_t row = phys_row(page_table, max_pages, num_pages, seq, pos);
-    if (row < 0 && reporter) report(status, SA_ERR_DEVICE_FAULT, SA_DETAIL_BAD_PAGE);
+    detail = row < 0 ? SA_DETAIL_BAD_PAGE : SA_DETAIL_NONE;
     return row;
+}
+
+// Calls of at most this many tokens need no cleared status word: their first CTA
+// looks every token up once more and writes the word, error or not (a clearing
+// memset in front costs a call of 64 tokens about 2 us on either side).
+constexpr int32_t kStatusTokens = 2048;
+
+// Called by every thread of the first CTA of such a launch.
+__device__ void write_status(const int32_t *page_table, int32_t batch, int32_t max_pages,
+                             int32_t num_pages, int32_t n, const int32_t *seq, const int32_t *pos,
+                             int32_t *status) {
+    __shared__ int32_t first_s[kWarpTokens];
+    int32_t first = INT32_MAX;  // (token << 2 | detail) of the first one that has no row
+    for (int32_t i = threadIdx.x; i < n; i += kWarpThreads) {
+        int32_t detail;
+        (void)token_row(page_table, batch, max_pages, num_pages, __ldg(seq + i), __ldg(pos + i),
+                        detail);
+        if (detail != SA_DETAIL_NONE) first = min(first, i << 2 | detail);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+    if ((threadIdx.x & 31) == 0) first_s[threadIdx.x >> 5] = first;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWarpTokens; ++w) first = min(first, first_s[w]);
+        status[0] = first == INT32_MAX ? SA_OK : SA_ERR_DEVICE_FAULT;
+        status[1] = first == INT32_MAX ? SA_DETAIL_NONE : first & 3;
+    }
 }
 
 // A warp takes `block` consecutive tokens: its lanes look their rows up at once,
@@ -362,6 +388,9 @@ append_fp4_kernel(const AppendParams p, int32_t block) {
     const int32_t D = p.d_latent + p.d_rope, chunks = p.d_latent / 16;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * block;
     const int32_t count = (int32_t)min((int64_t)block, p.n_new - t0);
+    if (p.set_status && blockIdx.x == 0)
+        write_status(p.page_table, p.batch, p.max_pages, p.num_pages, p.n_new, p.seq, p.pos,
+                     p.status);
     if (count <= 0) return;
     int32_t my_seq = 0, my_pos = 0;
     if (lane < count) {
@@ -379,9 +408,12 @@ append_fp4_kernel(const AppendParams p, int32_t block) {
             if (lane < chunks) raw[u].load(p.kv_new, s0 + 16 * lane);
             if (8 * lane < p.d_rope) raw_rope[u].load(p.kv_new, s0 + p.d_latent + 8 * lane);
         }
-        if (u0 == 0 && lane < count)  // while the first rows are on their way
+        if (u0 == 0 && lane < count) {  // while the first rows are on their way
+            int32_t detail;
             my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages, my_seq, my_pos,
-                               p.status, true);
+                               detail);
+            if (my_row < 0 && !p.set_status) report(p.status, SA_ERR_DEVICE_FAULT, detail);
+        }
 #pragma unroll
         for (int u = 0; u < kTokens; ++u) {
             const int64_t row = __shfl_sync(0xffffffffu, my_row, (u0 + u) & 31);
@@ -478,17 +510,23 @@ struct LatentPiece {
 template <int kKv, bool kWide>
 __global__ void __launch_bounds__(kWarpThreads)
 read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
-            const int32_t *__restrict__ pos_of, void *out, bool out_bf16, int32_t block) {
+            const int32_t *__restrict__ pos_of, void *out, bool out_bf16, int32_t block,
+            bool set_status) {
     constexpr int kTokens = kKv == SA_F32 ? 2 : 4;
     const int lane = threadIdx.x & 31;
     const int32_t dl = p.d_latent, dr = p.d_rope, D = dl + dr;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarpTokens + (threadIdx.x >> 5)) * block;
     const int32_t count = (int32_t)min((int64_t)block, n - t0);
+    if (set_status && blockIdx.x == 0)
+        write_status(p.page_table, p.batch, p.max_pages, p.num_pages, n, seq_of, pos_of, p.status);
     if (count <= 0) return;
     int64_t my_row = -1;
-    if (lane < count)
+    if (lane < count) {
+        int32_t detail;
         my_row = token_row(p.page_table, p.batch, p.max_pages, p.num_pages,
-                           __ldg(seq_of + t0 + lane), __ldg(pos_of + t0 + lane), p.status, true);
+                           __ldg(seq_of + t0 + lane), __ldg(pos_of + t0 + lane), detail);
+        if (my_row < 0 && !set_status) report(p.status, SA_ERR_DEVICE_FAULT, detail);
+    }
     if constexpr (!kWide) {
         for (int32_t u = 0; u < count; ++u) {
             const int64_t row = __shfl_sync(0xffffffffu, my_row, u);
@@ -564,11 +602,14 @@ cudaError_t launch_read_kv(const PathParams &p, int32_t n, const int32_t *seq, c
     const int32_t block = token_block(n);
     const auto kernel = wide ? read_kernel<kKv, true> : read_kernel<kKv, false>;
     count_launch();
-    kernel<<<token_grid(n, block), kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16, block);
+    kernel<<<token_grid(n, block), kWarpThreads, 0, s>>>(p, n, seq, pos, out, out_bf16, block,
+                                                      read_sets_status(n));
     return cudaGetLastError();
 }
 
 }  // namespace
+
+bool read_sets_status(int32_t n) { return n > 0 && n <= kStatusTokens; }
 
 cudaError_t launch_read(const PathParams &p, int32_t n, const int32_t *seq, const int32_t *pos,
                         void *out, int32_t out_dtype, cudaStream_t s) {
@@ -615,9 +656,16 @@ static void launch_append_fp4(const AppendParams &p, cudaStream_t s) {
     kernel<<<token_grid(p.n_new, block), kWarpThreads, 0, s>>>(p, block);
 }
 
+bool append_sets_status(int32_t kv_dtype, int32_t n_new, const void *k_new, const void *kv_new) {
+    // with index keys a second kernel reports too
+    return is_fp4(kv_dtype) && kv_new != nullptr && k_new == nullptr && n_new > 0 &&
+           n_new <= kStatusTokens;
+}
+
 cudaError_t launch_append(const AppendParams &params, cudaStream_t s) {
     if (params.n_new <= 0) return cudaSuccess;
     AppendParams p = params;
+    p.set_status = append_sets_status(p.kv_dtype, p.n_new, p.k_new, p.kv_new);
     if (is_fp4(p.kv_dtype) && p.kv_new != nullptr) {
         if (p.kv_dtype == SA_MXFP4) launch_append_fp4<SA_MXFP4>(p, s);
         else launch_append_fp4<SA_NVFP4>(p, s);

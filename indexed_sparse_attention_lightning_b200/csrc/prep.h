@@ -40,9 +40,15 @@ struct AppendParams {
     int32_t kv_scale_dims;  // e4m3, 4 bits: latent dims per scale (one token per scale)
     // status word
     int32_t *status;
+    bool set_status;  // see append_sets_status
 };
 
 cudaError_t launch_append(const AppendParams &p, cudaStream_t s);
+
+// Whether the launch writes the status word itself, error or not (a short call:
+// its first CTA looks at every token), so that nothing has to clear it first.
+bool append_sets_status(int32_t kv_dtype, int32_t n_new, const void *k_new, const void *kv_new);
+bool read_sets_status(int32_t n);
 
 // Latent + rope rows of tokens (seq[i], pos[i]) of the cache in `p` (its query
 // fields are unused) -> out [n, d_latent + d_rope], bf16 or fp32.

@@ -207,10 +207,10 @@ Layout make_layout(const sa_query *q, int32_t top_k, int32_t batch) {
     return l;
 }
 
-// sa_evict_tokens: status | physical source rows [batch, budget] | kept [batch]
+// sa_evict_tokens: see evict.h
 size_t evict_workspace(const sa_cache *c, int32_t budget) {
     if (budget <= 0) return 0;
-    return align_up(evict_kept_offset(c->batch, budget) + sizeof(int32_t) * (size_t)c->batch);
+    return align_up(evict_kept_offset(c->batch, budget) + 2 * sizeof(int32_t) * (size_t)c->batch);
 }
 
 // Physical rows and positions that fit 32 bits (with room for a block's step).
@@ -511,7 +511,9 @@ sa_status sa_append_tokens(const sa_cache *cache, const sa_new_tokens *tokens, v
     }
     if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = clear_status(workspace, s)) != SA_OK) return st;
+    const bool set_by_kernel = append_sets_status(cache->kv_dtype, tokens->n_new, tokens->k_index,
+                                                  tokens->kv);
+    if (!set_by_kernel && (st = clear_status(workspace, s)) != SA_OK) return st;
     if (tokens->n_new == 0 || (!tokens->k_index && !tokens->kv)) return SA_OK;
     AppendParams p{};
     p.page_table = cache->page_table;
@@ -552,7 +554,7 @@ sa_status sa_read_tokens(const sa_cache *cache, int32_t n, const int32_t *seq, c
     if (n > 0 && (!seq || !pos || !out || !aligned16(out))) return SA_ERR_INVALID_ARG;
     if ((st = check_workspace(workspace, workspace_bytes, kStatusBytes)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = clear_status(workspace, s)) != SA_OK) return st;
+    if (!read_sets_status(n) && (st = clear_status(workspace, s)) != SA_OK) return st;
     return cuda_status(launch_read(cache_params(cache, workspace), n, seq, pos, out, out_dtype, s));
 }
 
@@ -601,10 +603,9 @@ sa_status sa_evict_tokens(const sa_cache *src, const float *acc, int64_t ld_acc,
         return SA_ERR_UNSUPPORTED;
     if ((st = check_workspace(workspace, workspace_bytes, evict_workspace(src, budget))) != SA_OK)
         return st;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if ((st = clear_status(workspace, s)) != SA_OK) return st;
     return cuda_status(launch_evict(src, acc, ld_acc, budget, keep_first, keep_last, dst, acc_out,
-                                    ld_out, src_pos, workspace, s));
+                                    ld_out, src_pos, workspace,
+                                    static_cast<cudaStream_t>(stream)));
 }
 
 sa_status sa_device_status(const void *workspace, size_t workspace_bytes, void *stream,

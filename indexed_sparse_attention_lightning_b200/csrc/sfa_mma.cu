@@ -26,7 +26,7 @@
 // over it: every stage carries its own P, and the softmax of the next tile
 // never waits for P V of this one to release a shared P buffer.
 //
-// Roles (384 threads, 672 for a 4-bit latent; one CTA per SM):
+// Roles (384 threads, 416 for a 4-bit latent; one CTA per SM):
 //   warp 0     lane 0 loads Q by TMA (into the third ring stage; this copy
 //              starts before the wait on the top-K kernel); then the warp
 //              issues the MMAs, S of tile n + 1 before P V of tile n, and
@@ -35,7 +35,7 @@
 //              in the addresses) into a 3-stage ring freed by each tile's P V;
 //              random 1152-byte rows reach shared memory fastest this way (an
 //              e4m3 or 4-bit latent is loaded, decoded to bf16 and stored, the
-//              4-bit one with the help of warps 12-20);
+//              4-bit one with the help of warp 12);
 //   warps 8-11 move Q into TMEM, then run the online softmax.  Warp 8 + j
 //              owns heads 16j .. 16j + 15 and reads their S rows with 16-lane
 //              loads: thread i holds heads 16j + i/4 and 16j + i/4 + 8, keys
@@ -133,8 +133,11 @@ struct SfaArgs {
     float *lse_part;         // [n_q, splits, 128]      (splits > 1)
 };
 
+template <int kKv>
+constexpr int kProducers = is_fp4(kKv) ? kFp4AttnWarps : kProducerWarps;
+
 template <int kKv>  // sa_dtype of the latent cache
-__global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
+__global__ void __launch_bounds__(cta_threads(kProducers<kKv>), 1)
 sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     SfaSmem &sm = *reinterpret_cast<SfaSmem *>(align1024(smem_raw));
@@ -146,7 +149,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.kv_full[s], kFullArrivals<kKv>);
+            mbar_init(&sm.kv_full[s], 32 * kProducers<kKv>);
             mbar_init(&sm.kv_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) mbar_init(&sm.s_full[b], 1);
@@ -482,8 +485,9 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     } else if (warp >= 1) {
         // ---------------------------------------------- row producers ---
         // ring stage 2 holds Q until the softmax warps have moved it to TMEM
-        produce_rows<kKv>(p, rows + j0 * kTile, T, producer_index(warp),
-                          sm.kv, sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
+        produce_rows<kKv, kProducers<kKv>>(p, rows + j0 * kTile, T, producer_index(warp), sm.kv,
+                                           sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag,
+                                           status);
     } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
         // The whole warp waits and computes descriptors, one elected lane issues.
@@ -652,7 +656,8 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                                                  : sfa_mma_kernel<SA_NVFP4>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
+    const int threads =
+        cta_threads(is_fp4(p.kv_dtype) ? kProducers<SA_MXFP4> : kProducers<SA_BF16>);
     const int64_t grid = 2 * (int64_t)p.n_q * splits;
     count_launch();
     e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, s, tq, a);

@@ -282,8 +282,11 @@ __device__ __forceinline__ void produce_e4m3_pairs(const PathParams &p, const in
     }
 }
 
+template <int kKv>
+constexpr int kProducers = is_fp4(kKv) ? kFp4WeightsWarps : kProducerWarps;
+
 template <int kKv>  // sa_dtype of the latent cache
-__global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
+__global__ void __launch_bounds__(cta_threads(kProducers<kKv>), 1)
 weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p, int32_t splits,
                    const float *__restrict__ lse, int32_t ld, const int32_t *__restrict__ rows,
                    const int32_t *__restrict__ n_valid_of, float *__restrict__ w) {
@@ -294,7 +297,7 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&sm.kv_full[s], kFullArrivals<kKv>);
+            mbar_init(&sm.kv_full[s], 32 * kProducers<kKv>);
             mbar_init(&sm.kv_empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -426,8 +429,9 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
         if constexpr (kKv == SA_E4M3)
             produce_e4m3_pairs(p, tile_rows, T, warp - 1, sm, abort_flag, status);
         else
-            produce_rows<kKv>(p, tile_rows, T, producer_index(warp), sm.kv, sm.kv_full, sm.kv_empty,
-                              &sm.q_ready, 1, abort_flag, status);
+            produce_rows<kKv, kProducers<kKv>>(p, tile_rows, T, producer_index(warp), sm.kv,
+                                               sm.kv_full, sm.kv_empty, &sm.q_ready, 1,
+                                               abort_flag, status);
     } else if (T > 0) {
         // the whole warp waits and computes descriptors, one lane issues
         constexpr uint32_t id_s = instr_desc(kHeads, kTile, 1 /*bf16*/, 0, 0);
@@ -499,7 +503,8 @@ cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t to
     const int32_t tiles =
         (int32_t)ceil_div(top_k, p.kv_dtype == SA_E4M3 ? kKeysOf<SA_E4M3> : kTile);
     const int32_t splits = std::max(1, std::min(tiles, num_sms() / p.n_q));
-    const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
+    const int threads =
+        cta_threads(is_fp4(p.kv_dtype) ? kProducers<SA_MXFP4> : kProducers<SA_BF16>);
     count_launch();
     return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(threads), smem,
                       s, tq, p, splits, lse, ld, rows, n_valid, w);

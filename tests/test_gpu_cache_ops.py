@@ -89,7 +89,7 @@ def logits(wl, t, sel):
     kv = values(wl)[row_of(wl, int(wl.q_seq[t]), sel)]
     q, sm = q_values(wl)[t], wl.spec.softmax_scale
     z = (q @ kv.T) * sm
-    size = (np.abs(q) @ np.abs(kv).T) * sm
+    size = (np.abs(q) @ np.abs(kv).T) * abs(sm)
     dz = 2 * EPS * (kv.shape[1] + 2) * size + 4 * EPS * np.abs(z)
     if wl.spec.kv_dtype == "e4m3":
         dz = dz + 2.0 ** -16 * size
@@ -188,6 +188,115 @@ def test_read_tokens_of_every_pool(kv, tile):
     assert api.read_tokens(cache, none, none)[0].shape == (0, wl.spec.d_latent + wl.spec.d_rope)
 
 
+@pytest.mark.parametrize("n", [2048, 2049, 8001])
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_append_and_read_many_tokens(fmt, inp, n):
+    """Several tokens a warp, ragged at the end, with bad ones among them."""
+    wl = make(fmt, (2500, 64, 8000), d_latent=64, d_rope=8, heads=16)
+    cache, _ = api.upload(wl)
+    rng = np.random.default_rng(12)
+    every = np.concatenate([[(b, p) for p in range(64 * int((wl.page_table[b] >= 0).sum()))]
+                            for b in range(3)])
+    pick = every[rng.permutation(len(every))[:n]].astype(np.int32)
+    seq, pos = pick[:, 0].copy(), pick[:, 1].copy()
+    bad = rng.random(n) < 0.01
+    bad[[0, n - 1]] = True
+    seq[bad] = 3
+    x = np.concatenate([np.resize(_rows(5, n=300, d=64), (n, 64)),
+                        rng.standard_normal((n, 8)).astype(np.float32)], axis=1)
+    t = torch.from_numpy(x).to(torch.bfloat16 if inp == "bf16" else torch.float32)
+    seq_t, pos_t = torch.from_numpy(seq).cuda(), torch.from_numpy(pos).cuda()
+    ws = api.append_tokens(cache, seq_t, pos_t, kv=t.cuda())
+    assert api.device_status(ws) == (_abi.SA_ERR_DEVICE_FAULT, _abi.SA_DETAIL_BAD_POSITION)
+    want, skipped = oracle.append_tokens(_pools(wl), _layout(wl), seq, pos, None,
+                                         t.float().numpy())
+    assert len(skipped) == bad.sum()
+    same_bytes(_device_pools(cache), want)
+    rows = values(dataclasses.replace(wl, **want))
+    exp = np.zeros((n, 72))
+    for i in np.flatnonzero(~bad):
+        exp[i] = rows[row_of(wl, seq[i], pos[i])]
+    for out_dtype in ("bf16", "f32"):
+        back, ws = api.read_tokens(cache, seq_t, pos_t, out_dtype=out_dtype)
+        assert api.device_status(ws) == (_abi.SA_ERR_DEVICE_FAULT, _abi.SA_DETAIL_BAD_POSITION)
+        assert torch.equal(back.cpu(), torch.from_numpy(exp).to(back.dtype))
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+def test_nvfp4_codes_next_to_every_border(inp):
+    """For each scale byte the values on, and next to, each border between two codes,
+    and the largest values that take this byte."""
+    scales = oracle.fp4_scale_decode("nvfp4", np.arange(1, 127, dtype=np.uint8)).astype(np.float64)
+    borders = np.array([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0])
+    step = 2.0 ** -8 if inp == "bf16" else 2.0 ** -24
+    dtype = torch.bfloat16 if inp == "bf16" else torch.float32
+    near = (borders[:, None] * (1 + step * np.arange(-3, 4))[None]).ravel()
+    tops = [(1 + step * k) * 6 for k in range(-4, 5)]
+    rows = []
+    for i, top in enumerate(tops):
+        signs = np.where((np.arange(near.size) + i) % 2, -1.0, 1.0)
+        x = (signs * near)[None] * scales[:, None]
+        x = np.concatenate([x, np.zeros((x.shape[0], -x.shape[1] % 15))], axis=1)
+        g = x.reshape(len(scales), -1, 15)
+        lead = np.broadcast_to((top * scales)[:, None, None], g.shape[:2] + (1,))
+        rows.append(np.concatenate([lead, g], axis=2).reshape(len(scales), -1))
+    x = torch.from_numpy(np.concatenate(rows).astype(np.float32)).to(dtype)  # [n, 64]
+    assert x.shape[1] == 64
+    n = x.shape[0]
+    wl = make("nvfp4", (n,), d_latent=64, d_rope=8, heads=16)
+    cache, _ = api.upload(wl)
+    x = torch.cat([x, torch.zeros((n, 8), dtype=dtype)], dim=1)
+    seq, pos = np.zeros(n, np.int32), np.arange(n, dtype=np.int32)
+    ws = api.append_tokens(cache, torch.from_numpy(seq).cuda(), torch.from_numpy(pos).cuda(),
+                           kv=x.cuda())
+    assert api.device_status(ws) == OK
+    want, _ = oracle.append_tokens(_pools(wl), _layout(wl), seq, pos, None, x.float().numpy())
+    same_bytes(_device_pools(cache), want)
+
+
+def test_status_words_need_no_clearing():
+    """A call sets its status whatever the workspace held, on short and on long
+    calls, after garbage and after an error."""
+    wl = make("mxfp4", (5000, 300), heads=16, d_latent=64, d_rope=8)
+    cache, _ = api.upload(wl)
+    acc = torch.rand((2, 5000), device="cuda")
+    spare = sorted(set(range(wl.num_pages)) - set(wl.page_table.ravel().tolist()))[:2]
+    dst = dataclasses.replace(
+        cache, page_table=torch.tensor(spare, dtype=torch.int32, device="cuda").reshape(2, 1),
+        seq_len=torch.zeros(2, dtype=torch.int32, device="cuda"))
+    bad_dst = dataclasses.replace(dst, page_table=dst.page_table + wl.num_pages)
+    need = max(api.workspace_size(cache, None, 64, u) for u in (_abi.SA_WS_APPEND,
+                                                                 _abi.SA_WS_EVICT))
+    ws = api.workspace(need)
+    bad_page = (_abi.SA_ERR_DEVICE_FAULT, _abi.SA_DETAIL_BAD_PAGE)
+    bad_pos = (_abi.SA_ERR_DEVICE_FAULT, _abi.SA_DETAIL_BAD_POSITION)
+    for n in (0, 1, 2048, 2049, 4000):
+        seq = torch.zeros(n, dtype=torch.int32, device="cuda")
+        pos = torch.arange(n, dtype=torch.int32, device="cuda")
+        off = seq.clone()
+        off[n // 2:] = 2
+        kv = torch.randn((n, 72), device="cuda")
+        keys = torch.randn((n, wl.spec.d_index), device="cuda")
+        for garbage in (True, False):
+            calls = [lambda s: api.append_tokens(cache, s, pos, kv=kv, ws=ws),
+                     lambda s: api.read_tokens(cache, s, pos, ws=ws),
+                     lambda s: api.append_tokens(cache, s, pos, k_index=keys, kv=kv, ws=ws),
+                     lambda s: api.append_tokens(cache, s, pos, k_index=keys, ws=ws)]
+            for call in calls:
+                for s, want in ((seq, OK), (off, bad_pos if n else OK), (seq, OK)):
+                    if garbage:
+                        ws.fill_(0xA5)
+                    call(s)
+                    assert api.device_status(ws) == want
+    for d, want in ((dst, OK), (bad_dst, bad_page), (dst, OK)):
+        for garbage in (True, False):
+            if garbage:
+                ws.fill_(0xA5)
+            api.evict_tokens(cache, acc, 64, d, 1, 1, ws=ws)
+            assert api.device_status(ws) == want
+
+
 def test_read_tokens_reports_a_bad_page():
     wl = make("mxfp4", (130,), heads=16)
     wl.page_table[0, 1] = wl.num_pages
@@ -245,6 +354,16 @@ def test_attention_over_4_bits(fmt, heads, dl, dr, lens, K, out_dtype):
         out, lse = api.sparse_mla_attn(cache, queries, idx_t, K, out_dtype=out_dtype, ws=ws)
         assert api.device_status(ws) == OK
         check_attention(wl, idx, out, lse, out_dtype)
+
+
+@pytest.mark.parametrize("sm_scale", [-0.05, 0.0, -0.0, 4.0])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_attention_over_4_bits_with_other_softmax_scales(fmt, sm_scale):
+    wl = make(fmt, (900, 65), heads=128, sm_scale=sm_scale)
+    idx = selection(wl, 300, 7, holes=True)
+    cache, queries, idx_t = upload(wl, idx)
+    out, lse = api.sparse_mla_attn(cache, queries, idx_t, 300, out_dtype="f32")
+    check_attention(wl, idx, out, lse, "f32")
 
 
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
@@ -348,6 +467,21 @@ def test_weights_of_a_decode_step(kv, tile):
     check_weights(wl, selection(wl, 600, 5))
     check_weights(wl, selection(wl, 600, 6, holes=True, order="shuffled"), decay=0.5,
                   inplace=True, ld=1400)
+
+
+@pytest.mark.parametrize("sm_scale", [-0.05, 0.0])
+@pytest.mark.parametrize("kv", ["bf16", "e4m3", "mxfp4"])
+def test_weights_with_other_softmax_scales(kv, sm_scale):
+    wl = make(kv, (900, 65), heads=128, sm_scale=sm_scale)
+    check_weights(wl, selection(wl, 300, 7, holes=True))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
+def test_weights_of_more_queries_than_sms(kv):
+    """Every CTA takes all of a query's rows; K of one row, of whole tiles, and odd."""
+    wl = make(kv, (1000,), heads=128, queries=("prefill", 700, 300))
+    for K in (1, 64, 193):
+        check_weights(wl, selection(wl, K, 6, order="shuffled" if K == 64 else "ascending"))
 
 
 @pytest.mark.parametrize("heads,dl,dr", [(1, 64, 16), (7, 96, 8), (20, 512, 64), (130, 32, 0)])
@@ -547,6 +681,21 @@ def test_evict_long_sequences():
     acc = np.exp(rng.standard_normal((2, 70001))).astype(np.float32)
     acc[rng.random(acc.shape) < 0.7] = 0
     evict_case(wl, acc, 9001, 64, 1000)
+
+
+@pytest.mark.parametrize("lens,width", [((5000, 900), 16 * 48 * 1024 + 128),
+                                        ((9, 50000) + 78 * (150,), 50000)])
+def test_evict_without_keys_in_shared_memory(lens, width):
+    """Rows of sums too wide for the shared memory of a sequence's CTAs: sixteen of
+    them for two sequences, one for eighty."""
+    wl = make("mxfp4", lens, heads=16, d_latent=64, d_rope=8, d_index=32)
+    pages = -(-width // 64)
+    table = np.full((len(lens), pages), -1, np.int32)
+    table[:, :wl.max_pages] = wl.page_table
+    wl = dataclasses.replace(wl, page_table=table)
+    acc = np.random.default_rng(8).standard_normal((len(lens), width)).astype(np.float32)
+    acc[:, ::3] = 0
+    evict_case(wl, acc, 130, 4, 30)
 
 
 def test_evict_short_sequences_may_keep_their_pages():
