@@ -51,7 +51,7 @@ struct EvictArgs {
     int32_t *status;   // written by the move kernel, from `fault`
 };
 
-// One pool's rows: `units` pieces of `unit` bytes (16, 8, 4, 2 or 1).
+// One pool's rows: `units` pieces of `unit` bytes (16, 4, 2 or 1).
 struct EvictField {
     const uint8_t *src;
     uint8_t *dst;
@@ -459,9 +459,13 @@ evict_move_kernel(const EvictArgs a, const EvictFields fields, int32_t pieces, i
     }
 }
 
+// The unit divides the row and both pools' addresses (the fp32 scales of an e4m3
+// latent may start at any float).
 void add_field(EvictFields &fs, const void *src, const void *dst, int64_t row_bytes) {
     if (row_bytes <= 0) return;
-    const int32_t unit = row_bytes % 16 == 0 ? 16 : row_bytes % 4 == 0 ? 4 : row_bytes % 2 ? 1 : 2;
+    const uintptr_t all = reinterpret_cast<uintptr_t>(src) | reinterpret_cast<uintptr_t>(dst) |
+                          static_cast<uintptr_t>(row_bytes);
+    const int32_t unit = all % 16 == 0 ? 16 : all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
     fs.f[fs.n++] = EvictField{static_cast<const uint8_t *>(src),
                               static_cast<uint8_t *>(const_cast<void *>(dst)), unit,
                               (int32_t)(row_bytes / unit)};

@@ -202,8 +202,8 @@ Layout make_layout(const sa_query *q, int32_t top_k, int32_t batch) {
     l.wt_w = align_up(l.wt_kept + wt_bytes);
     l.wt_n_valid = align_up(l.wt_w + wt_bytes);
     l.wt_starts = align_up(l.wt_n_valid + sizeof(int32_t) * nq);
-    l.wt_total =
-        align_up(l.wt_starts + sizeof(int32_t) * nq * (size_t)weights_starts_ld(q->n_q, batch, q->max_visible));
+    const size_t starts_ld = (size_t)weights_starts_ld(q->n_q, batch, q->max_visible);
+    l.wt_total = align_up(l.wt_starts + sizeof(int32_t) * nq * starts_ld);
     return l;
 }
 
@@ -217,6 +217,12 @@ size_t evict_workspace(const sa_cache *c, int32_t budget) {
 bool rows_fit_32(const sa_cache *c) {
     constexpr int64_t kLimit = (int64_t(1) << 31) - 8192;
     return (int64_t)c->num_pages * kPageSize < kLimit && (int64_t)c->max_pages * kPageSize < kLimit;
+}
+
+// Whether two arrays of 4-byte elements share memory.
+bool overlap(const void *a, int64_t n_a, const void *b, int64_t n_b) {
+    const auto x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + 4 * static_cast<uint64_t>(n_b) && y < x + 4 * static_cast<uint64_t>(n_a);
 }
 
 // Whether two caches hold rows of the same formats and sizes.
@@ -569,6 +575,9 @@ sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *query, co
     if (query->n_q > 0 && (!idx || !lse)) return SA_ERR_INVALID_ARG;
     if (!acc_out || ld_acc <= 0 || (query->n_q > 0 && ld_acc < query->max_visible))
         return SA_ERR_INVALID_ARG;
+    const int64_t sums = cache->batch * ld_acc;
+    if (acc_in && acc_in != acc_out && overlap(acc_in, sums, acc_out, sums))
+        return SA_ERR_INVALID_ARG;
     if (!rows_fit_32(cache) || (int64_t)cache->batch * cache->max_pages >= (int64_t(1) << 31))
         return SA_ERR_UNSUPPORTED;
     const Layout l = make_layout(query, top_k, cache->batch);
@@ -596,9 +605,13 @@ sa_status sa_evict_tokens(const sa_cache *src, const float *acc, int64_t ld_acc,
     if (src->kv_dtype == SA_E4M3 && src->kv_scale_tokens != 1) return SA_ERR_UNSUPPORTED;
     if (!acc || ld_acc <= 0 || budget <= 0 || keep_first < 0 || keep_last < 0 ||
         (int64_t)keep_first + keep_last > budget ||
-        (int64_t)dst->max_pages * dst->page_size < budget || src->seq_len == dst->seq_len)
+        (int64_t)dst->max_pages * dst->page_size < budget)
         return SA_ERR_INVALID_ARG;
-    if (acc_out && (acc_out == acc || ld_out < budget)) return SA_ERR_INVALID_ARG;
+    // the CTAs of a sequence read its length and sums more than once
+    const int64_t batch = src->batch;
+    if (overlap(src->seq_len, batch, dst->seq_len, batch)) return SA_ERR_INVALID_ARG;
+    if (acc_out && (ld_out < budget || overlap(acc, batch * ld_acc, acc_out, batch * ld_out)))
+        return SA_ERR_INVALID_ARG;
     if (!rows_fit_32(src) || !rows_fit_32(dst) || src->batch > kMaxQueries)
         return SA_ERR_UNSUPPORTED;
     if ((st = check_workspace(workspace, workspace_bytes, evict_workspace(src, budget))) != SA_OK)

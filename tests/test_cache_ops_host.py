@@ -142,7 +142,8 @@ def test_accumulate_weights_refusals(L):
     assert weigh(L, c, q, ws=FAKE + 16, nb=need) == _abi.SA_ERR_WORKSPACE
     assert weigh(L, c, q, acc=None) == _abi.SA_ERR_WORKSPACE     # acc_in may be absent
     for bad in ({"idx": None}, {"lse": None}, {"out": None}, {"k": 0}, {"k": -5}, {"ld": 0},
-                {"ld": 255}, {"decay": float("nan")}, {"decay": float("inf")}):
+                {"ld": 255}, {"decay": float("nan")}, {"decay": float("inf")},
+                {"acc": FAKE + 4}, {"acc": FAKE - 4 * (2 * 256 - 1)}):
         assert weigh(L, c, q, **bad) == _abi.SA_ERR_INVALID_ARG, bad
     assert weigh(L, c, good_query(q=None)) == _abi.SA_ERR_INVALID_ARG
     assert weigh(L, c, good_query(sm_scale=float("nan"))) == _abi.SA_ERR_INVALID_ARG
@@ -166,9 +167,11 @@ def test_evict_tokens_refusals(L):
     assert evict(L, c, d, acc_out=None, ld_out=0, src_pos=None) == _abi.SA_ERR_WORKSPACE
     for bad in ({"acc": None}, {"ld": 0}, {"budget": 0}, {"first": -1}, {"last": -1},
                 {"first": 65}, {"budget": 257}, {"ld_out": 127}, {"acc_out": FAKE},
+                {"acc_out": FAKE + 4 * (2 * 256 - 1)}, {"acc_out": FAKE - 4 * (2 * 128 - 1)},
                 {"first": 2 ** 31 - 1, "last": 2 ** 31 - 1}):
         assert evict(L, c, d, **bad) == _abi.SA_ERR_INVALID_ARG, bad
-    for other in ({"seq_len": FAKE}, {"batch": 3}, {"d_latent": 256}, {"d_rope": 32},
+    assert evict(L, c, d, acc_out=FAKE + 4 * 2 * 256) == _abi.SA_ERR_WORKSPACE
+    for other in ({"seq_len": FAKE}, {"seq_len": FAKE + 4}, {"seq_len": FAKE - 4}, {"batch": 3}, {"d_latent": 256}, {"d_rope": 32},
                   {"d_index": 64}, {"index_dtype": _abi.SA_BF16}, {"kv_dtype": _abi.SA_F32},
                   {"max_pages": 1}):
         bad_dst = good_cache(**{"seq_len": FAKE << 1, "page_table": FAKE << 1, **other})

@@ -479,7 +479,7 @@ def test_weights_with_other_softmax_scales(kv, sm_scale):
 @pytest.mark.parametrize("kv", ["bf16", "nvfp4"])
 def test_weights_of_more_queries_than_sms(kv):
     """Every CTA takes all of a query's rows; K of one row, of whole tiles, and odd."""
-    wl = make(kv, (1000,), heads=128, queries=("prefill", 700, 300))
+    wl = make(kv, (400,), heads=128, queries=("prefill", 240, 160))
     for K in (1, 64, 193):
         check_weights(wl, selection(wl, K, 6, order="shuffled" if K == 64 else "ascending"))
 
@@ -649,6 +649,32 @@ def test_evict_moves_the_right_rows(kv, index, kw):
     acc = rng.standard_normal((6, 2500)).astype(np.float32)
     acc[:, rng.random(2500) < 0.6] = 0.0                    # ties
     evict_case(wl, acc, 128, 3, 40)
+
+
+def test_evict_scales_that_start_at_any_float():
+    """Four fp32 scales a row, their pools 4 bytes off a 16-byte boundary."""
+    wl = make("e4m3", (400, 90), heads=16, kv_scale_tile=(1, 128))
+    acc = np.random.default_rng(9).random((2, 400)).astype(np.float32)
+    cache, _ = api.upload(wl)
+    flat = torch.empty(cache.kv_scale.numel() + 1, device="cuda")
+    odd = flat[1:].view(cache.kv_scale.shape)
+    odd.copy_(cache.kv_scale)
+    assert odd.data_ptr() % 16 == 4
+    out = torch.zeros_like(flat)[1:].view(odd.shape)
+    lens = torch.zeros(2, dtype=torch.int32, device="cuda")
+    table = torch.arange(4, dtype=torch.int32, device="cuda").reshape(2, 2)
+    dst = dataclasses.replace(cache, page_table=table, seq_len=lens,
+                              k_index=torch.zeros_like(cache.k_index),
+                              k_index_scale=torch.zeros_like(cache.k_index_scale),
+                              kv=torch.zeros_like(cache.kv),
+                              kv_rope=torch.zeros_like(cache.kv_rope), kv_scale=out)
+    api.evict_tokens(dataclasses.replace(cache, kv_scale=odd), torch.from_numpy(acc).cuda(), 100,
+                     dst, 1, 10)
+    assert lens.tolist() == [100, 90]
+    rows = out.view(-1, 4).cpu().numpy()
+    scales = wl.kv_scale.reshape(-1, 4)
+    for b, keep in enumerate((keep_ref(400, acc[0], 100, 1, 10), np.arange(90))):
+        assert np.array_equal(rows[128 * b:128 * b + keep.size], scales[row_of(wl, b, keep)])
 
 
 @pytest.mark.parametrize("budget,first,last", [(1, 0, 0), (1, 1, 0), (1, 0, 1), (64, 32, 32),
