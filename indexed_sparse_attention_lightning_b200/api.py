@@ -42,7 +42,10 @@ def _need(t, name: str, dtype=None, shape=None, optional: bool = False) -> None:
         if optional:
             return
         raise SaError(_abi.SA_ERR_INVALID_ARG, f"{name} is required")
-    if dtype is None and type(t) is torch.Tensor and t.is_cuda and t.is_contiguous():
+    # the usual case first: a call checks a dozen tensors
+    if (type(t) is torch.Tensor and t.is_cuda and t.is_contiguous() and
+            (dtype is None or t.dtype is dtype or (type(dtype) is tuple and t.dtype in dtype)) and
+            (shape is None or t.shape == shape)):
         return
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise SaError(_abi.SA_ERR_INVALID_ARG, f"{name} must be a CUDA tensor")
@@ -78,16 +81,16 @@ def _need_sums(t, name: str, batch: int, min_cols: int) -> int:
 
 def _need_here(where: str, *tensors) -> None:
     """The kernels run on the current device: refuse tensors of another one."""
-    here = torch.cuda.current_device()
+    here = torch._C._cuda_getDevice()
     for t in tensors:
-        if t is not None and t.device.index != here:
+        if t is not None and t.get_device() != here:
             raise SaError(_abi.SA_ERR_INVALID_ARG, f"{where}: a tensor is on {t.device}, the "
                                                    f"current device is cuda:{here}")
 
 
 def _stream(stream) -> int:
     if stream is None:  # the raw handle: a Stream object costs 3 us
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream
 
 
@@ -114,12 +117,15 @@ class DeviceCache:
     def struct(self) -> SaCache:
         _need(self.page_table, "page_table", torch.int32)
         _need(self.seq_len, "seq_len", torch.int32)
-        for name in ("k_index", "k_index_scale", "kv", "kv_rope", "kv_scale"):
-            _need(getattr(self, name), name, optional=True)
+        _need(self.k_index, "k_index", optional=True)
+        _need(self.k_index_scale, "k_index_scale", optional=True)
+        _need(self.kv, "kv", optional=True)
+        _need(self.kv_rope, "kv_rope", optional=True)
+        _need(self.kv_scale, "kv_scale", optional=True)
         # in the order of the struct's fields: by keyword the construction takes twice as long
+        batch, max_pages = self.page_table.shape
         return SaCache(
-            _ptr(self.page_table), _ptr(self.seq_len), self.page_table.shape[0],
-            self.page_table.shape[1], self.num_pages, self.page_size,
+            _ptr(self.page_table), _ptr(self.seq_len), batch, max_pages, self.num_pages, self.page_size,
             _abi.DTYPES[self.index_dtype], _ptr(self.k_index), _ptr(self.k_index_scale),
             self.d_index, _abi.DTYPES[self.kv_dtype], _ptr(self.kv), _ptr(self.kv_rope),
             _ptr(self.kv_scale), self.d_latent, self.d_rope, int(self.kv_scale_tile[0]),
@@ -290,6 +296,7 @@ def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tenso
         ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_ATTN), idx.device)
     _need(idx, "idx", torch.int32, (queries.n_q, top_k))
     _need(ws, "ws")
+    _need_here("sparse_mla_attn", cache.kv, queries.q, idx, out, lse, ws)
     c, q = cache.struct(), queries.struct()
     check(_abi.lib().sa_sparse_mla_attn(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
                                         _ptr(out), _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws),
@@ -432,8 +439,7 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
     index keys [n_new, d_index] and latent + rope rows [n_new, d_latent + d_rope],
     both bfloat16 or both float32 (either may be None).  Returns the workspace,
     whose status word records skipped tokens (see device_status)."""
-    ins = [t for t in (k_index, kv) if t is not None]
-    if len({t.dtype for t in ins}) > 1:
+    if k_index is not None and kv is not None and k_index.dtype != kv.dtype:
         raise SaError(_abi.SA_ERR_INVALID_ARG, "append_tokens: k_index and kv dtypes differ")
     n_new = int(seq.numel())
     _need(seq, "seq", torch.int32, (n_new,))
@@ -442,7 +448,8 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
           optional=True)
     _need(kv, "kv", (torch.bfloat16, torch.float32), (n_new, cache.d_latent + cache.d_rope),
           optional=True)
-    dt = _in_dtype(ins[0]) if ins else _abi.SA_BF16
+    rows = kv if kv is not None else k_index
+    dt = _abi.SA_BF16 if rows is None else _in_dtype(rows)
     c = cache.struct()
     if ws is None:
         n = _abi.lib().sa_workspace_size(ctypes.byref(c), None, 0, _abi.SA_WS_APPEND)
@@ -450,8 +457,8 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
             raise SaError(_abi.SA_ERR_INVALID_ARG, "sa_workspace_size")
         ws = workspace(n, seq.device)
     _need(ws, "ws")
-    t = SaNewTokens(n_new=n_new, seq=_ptr(seq), pos=_ptr(pos), in_dtype=dt,
-                    k_index=_ptr(k_index), kv=_ptr(kv))
+    _need_here("append_tokens", cache.kv, seq, pos, k_index, kv, ws)
+    t = SaNewTokens(n_new, _ptr(seq), _ptr(pos), dt, _ptr(k_index), _ptr(kv))
     check(_abi.lib().sa_append_tokens(ctypes.byref(c), ctypes.byref(t), _ptr(ws), ws.numel(),
                                       _stream(stream)),
           "sa_append_tokens")
