@@ -219,7 +219,8 @@ SA_API sa_status sa_topk(const float *scores, int64_t ld_scores, const int32_t *
  *   z_s = sm_scale * q[t,h,:] . kv[s,:]   (latent + rope; an e4m3 latent is
  *                                          scaled by its page-tile scale)
  *   out[t,h,:] = sum_s softmax(z)_s * kv[s, 0:d_latent],  lse[t,h] = log sum_s exp(z_s)
- * out: device [n_q, heads, d_latent] in out_dtype (SA_BF16 or SA_F32);
+ * out: device [n_q, heads, d_latent] in out_dtype (SA_BF16 or SA_F32), 16-byte
+ * aligned for a bf16 query of 128 heads x (512 + 64) dims and top_k <= 2048;
  * lse: device fp32 [n_q, heads] (may be NULL).  A query with no valid index
  * gets out = 0 and lse = -inf. */
 SA_API sa_status sa_sparse_mla_attn(const sa_cache *cache, const sa_query *query, const int32_t *idx,

@@ -269,24 +269,31 @@ __device__ __forceinline__ void compact_rows(const PathParams &p, int32_t t, con
 // entries by 512 threads, four each: 9 instead of 11 us with cold caches).  With
 // `kept` it also writes the positions behind rows[0, *n_valid).  `scratch`:
 // kCompactScratch ints; kEntries times the warps of the CTA are at most 128.
+// `first`: this thread's entries of the first step, from load_entries before.
 constexpr int kCompactScratch = 128 + 2;
+template <int kEntries>
+__device__ __forceinline__ void load_entries(const int32_t *sel, int32_t K, int64_t r0,
+                                             int32_t (&s)[kEntries]) {
+#pragma unroll
+    for (int j = 0; j < kEntries; ++j) {
+        const int64_t k = r0 + j * blockDim.x + threadIdx.x;
+        s[j] = k < K ? sel[k] : -1;
+    }
+}
 template <int kEntries>
 __device__ __forceinline__ void compact_selection(const PathParams &p, int32_t t,
                                                   const int32_t *sel, int32_t K, int32_t tile,
                                                   int32_t *rows, int32_t *n_valid,
-                                                  int32_t *scratch, int32_t *kept = nullptr) {
+                                                  int32_t *scratch, int32_t (&first)[kEntries],
+                                                  int32_t *kept = nullptr) {
     const int nwarps = blockDim.x >> 5, w = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int32_t seq = __ldg(p.q_seq + t);
     const bool seq_ok = seq >= 0 && seq < p.batch;
     int32_t V = -1;  // known after the first loads are on their way
     int32_t base = 0;
     for (int64_t r0 = 0; r0 < K; r0 += kEntries * blockDim.x) {
-        int32_t s[kEntries], v[kEntries];
-#pragma unroll
-        for (int j = 0; j < kEntries; ++j) {
-            const int64_t k = r0 + j * blockDim.x + threadIdx.x;
-            s[j] = k < K ? sel[k] : -1;
-        }
+        int32_t (&s)[kEntries] = first, v[kEntries];
+        if (r0 > 0) load_entries(sel, K, r0, s);
 #pragma unroll
         for (int j = 0; j < kEntries; ++j) {
             v[j] = -1;

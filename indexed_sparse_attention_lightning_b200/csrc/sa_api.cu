@@ -233,6 +233,12 @@ bool same_format(const sa_cache *a, const sa_cache *b) {
            a->kv_scale_tokens == b->kv_scale_tokens && a->kv_scale_dims == b->kv_scale_dims;
 }
 
+// The tensor-core attention stores 16 bytes at a time; the CUDA-core one single
+// values, wherever `out` starts.
+bool out_fits(const sa_cache *c, const sa_query *q, int32_t top_k, const void *out) {
+    return q->n_q == 0 || aligned16(out) || !sfa_mma_supported(make_params(c, q, nullptr), top_k);
+}
+
 // Sparse attention: the tensor-core kernel for its shape, CUDA cores otherwise.
 sa_status run_attention(const PathParams &p, const Layout &l, bool fused, bool rows_ready,
                         void *ws, const int32_t *idx, int32_t top_k, void *out,
@@ -357,6 +363,7 @@ sa_status sa_sparse_mla_attn(const sa_cache *cache, const sa_query *query, const
     if (top_k <= 0 || top_k > kMaxTopK) return SA_ERR_INVALID_ARG;
     if (out_dtype != SA_BF16 && out_dtype != SA_F32) return SA_ERR_UNSUPPORTED;
     if (query->n_q > 0 && (!idx || !out)) return SA_ERR_INVALID_ARG;
+    if (!out_fits(cache, query, top_k, out)) return SA_ERR_INVALID_ARG;
     const Layout l = make_layout(query, top_k, cache->batch);
     if ((st = check_workspace(workspace, workspace_bytes, l.attn_total)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -383,6 +390,7 @@ static sa_status decode_impl(const sa_cache *cache, const sa_query *query, int32
     if (top_k <= 0 || top_k > kMaxTopK) return SA_ERR_INVALID_ARG;
     if (out_dtype != SA_BF16 && out_dtype != SA_F32) return SA_ERR_UNSUPPORTED;
     if (query->n_q > 0 && !out && !cand) return SA_ERR_INVALID_ARG;
+    if (!out_fits(cache, query, top_k, out)) return SA_ERR_INVALID_ARG;
     const Layout l = make_layout(query, top_k, cache->batch);
     if ((st = check_workspace(workspace, workspace_bytes, l.decode_total)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);

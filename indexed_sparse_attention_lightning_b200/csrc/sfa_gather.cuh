@@ -41,8 +41,11 @@ __device__ __forceinline__ uint4 fp4_order(const uint4 x) {
     return make_uint4(__byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632),
                       __byte_perm(x.y, x.w, 0x5410), __byte_perm(x.y, x.w, 0x7632));
 }
-__host__ __device__ constexpr int fp4_place(int dim) {
-    return (dim & ~7) + 2 * (dim & 3) + ((dim >> 2) & 1);
+
+// And back.
+__device__ __forceinline__ uint4 fp4_natural(uint4 x) {
+    return make_uint4(__byte_perm(x.x, x.y, 0x5410), __byte_perm(x.z, x.w, 0x5410),
+                      __byte_perm(x.x, x.y, 0x7632), __byte_perm(x.z, x.w, 0x7632));
 }
 
 __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {

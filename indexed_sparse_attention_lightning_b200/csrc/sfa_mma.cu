@@ -43,8 +43,8 @@
 //              maximum takes two shuffles and P goes to shared memory in
 //              bf16 pairs.  O is rescaled in TMEM (16-lane accesses with the
 //              same thread-to-head mapping, leaving Q and S alone) only when a
-//              head's running maximum grows by more than 2^8; finally lanes
-//              16-31 read O with 32-lane loads and write O / l.
+//              head's running maximum grows by more than 2^8; finally they
+//              write O / l, with the help of warps 4-7 (write_output).
 // The fused decode gets the selection's physical rows from the top-K kernel;
 // otherwise every CTA turns its query's positions into rows itself, in shared
 // memory, while Q is on its way (a kernel in front of this one took 9 us).  All
@@ -71,6 +71,11 @@ constexpr float kRescaleLog2 = 8.0f;
 // (h/8)*kGroupBytes + 8*1024 + (h%8)*128 (+ swizzle), the K-major A operand of
 // P V with 8-head groups kGroupBytes apart.
 constexpr uint32_t kPOffset = (kBlocks - 1) * 1024;  // the rope block
+// The output's way through shared memory: 128 columns of 16 rows per warp, fp32
+// or bf16, each row with eight columns of space behind it.
+constexpr int kOutCols = 128, kOutBytes = 16 * (kOutCols + 8) * 4;
+static_assert(8 * kOutBytes <= (int)kStageBytes, "the eight warps' rows fit in a stage");
+constexpr int kOutBarrier = 1;  // the eight warps that write the output
 
 struct SfaSmem {
     // ring stage: 8 groups of 8 rows; a group holds the 9 column blocks of its
@@ -83,6 +88,7 @@ struct SfaSmem {
     uint64_t s_full[2], p_full[kStages], o_final, q_full, q_ready;
     uint32_t tmem_base;
     int abort;
+    float inv[kHeadsCta];  // 1 / l
     int32_t n_valid, scratch[kCompactScratch];
     int32_t rows[kMaxK];  // the selection's physical rows, whole tiles
 };
@@ -136,6 +142,102 @@ struct SfaArgs {
 template <int kKv>
 constexpr int kProducers = is_fp4(kKv) ? kFp4AttnWarps : kProducerWarps;
 
+// Columns [256 half, 256 half + 256) of O / l of heads 16j .. 16j + 15 (warp 8 +
+// j, and 4 + j for the second half; both see TMEM lanes 32j and up), 128 columns
+// at a time through shared memory (stage 0: every MMA is done, and a CTA without
+// tiles has only Q's copy in flight, into stage 2), so that a store of the warp
+// writes whole lines of two rows.  It takes 4000 cycles for bf16 and 6900 for
+// fp32, the first pass twice the second; one warp per 16 heads, storing 16 bytes
+// of 16 rows at a time, took 6000 and 10500.
+template <int kKv>
+__device__ __forceinline__ void write_output(SfaSmem &sm, const SfaArgs &a, int t, int split,
+                                             int hh, int j, int half, bool any, uint32_t tmem_o) {
+    const int lane = lane_id(), q4 = lane & 3;
+    const float inv_a = sm.inv[16 * j + (lane >> 2)], inv_b = sm.inv[16 * j + (lane >> 2) + 8];
+    const bool part = a.splits > 1, wide = part || a.out_dtype == SA_F32;
+    const int bytes = wide ? 4 : 2;
+    const int stride = kOutCols * bytes + 8 * bytes;  // no two lanes of a store in one bank
+    uint8_t *buf = sm.kv[0] + (4 * half + j) * kOutBytes;
+    const int64_t row0 =
+        (part ? (int64_t)t * a.splits + split : t) * 128 + kHeadsCta * hh + 16 * j;
+    uint8_t *dst =
+        (part ? reinterpret_cast<uint8_t *>(a.o_part) : static_cast<uint8_t *>(a.out)) +
+        row0 * (kDl * bytes);
+#pragma unroll 1
+    for (int c = 256 * half; c < 256 * half + 256; c += kOutCols) {
+        uint32_t v[2][32] = {};
+        if (any) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) tmem_ld_16x256b_x8(tmem_o + c + 64 * h, v[h]);
+            tmem_wait_ld_keep(v[0]);
+            tmem_wait_ld_keep(v[1]);
+        }
+        // columns 8i + 2 q4 and the next one of two heads
+        uint8_t *ra = buf + (lane >> 2) * stride + 2 * q4 * bytes, *rb = ra + 8 * stride;
+        if (wide) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t *x = v[i >> 3] + 4 * (i & 7);
+                *reinterpret_cast<float2 *>(ra + 32 * i) = make_float2(
+                    __uint_as_float(x[0]) * inv_a, __uint_as_float(x[1]) * inv_a);
+                *reinterpret_cast<float2 *>(rb + 32 * i) = make_float2(
+                    __uint_as_float(x[2]) * inv_b, __uint_as_float(x[3]) * inv_b);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const uint32_t *x = v[i >> 3] + 4 * (i & 7);
+                *reinterpret_cast<__nv_bfloat162 *>(ra + 16 * i) = __floats2bfloat162_rn(
+                    __uint_as_float(x[0]) * inv_a, __uint_as_float(x[1]) * inv_a);
+                *reinterpret_cast<__nv_bfloat162 *>(rb + 16 * i) = __floats2bfloat162_rn(
+                    __uint_as_float(x[2]) * inv_b, __uint_as_float(x[3]) * inv_b);
+            }
+        }
+        __syncwarp();
+        // eight columns per lane, two rows at a time; of a 4-bit latent in the order
+        // of the stages
+        const uint8_t *from = buf + (lane >> 4) * stride + 8 * bytes * (lane & 15);
+        uint8_t *to = dst + ((lane >> 4) * kDl + c + 8 * (lane & 15)) * bytes;
+        if (wide) {
+            const int turn = (lane >> 2) & 1;  // so that eight lanes' pieces meet all banks once
+#pragma unroll
+            for (int r = 0; r < 16; r += 8) {
+                uint4 x[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 *f =
+                        reinterpret_cast<const uint4 *>(from + (r + 2 * i) * stride);
+                    const uint4 y0 = f[turn], y1 = f[1 - turn];
+                    const uint4 lo = turn ? y1 : y0, hi = turn ? y0 : y1;
+                    x[i][0] = is_fp4(kKv) ? make_uint4(lo.x, lo.z, hi.x, hi.z) : lo;
+                    x[i][1] = is_fp4(kKv) ? make_uint4(lo.y, lo.w, hi.y, hi.w) : hi;
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint4 *d = reinterpret_cast<uint4 *>(to + (r + 2 * i) * (kDl * 4));
+                    if (part) {  // in the workspace: aligned to 32 bytes
+                        store_32_bytes(d, x[i][0], x[i][1]);
+                    } else {
+                        d[0] = x[i][0];
+                        d[1] = x[i][1];
+                    }
+                }
+            }
+        } else {
+            uint4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                x[i] = *reinterpret_cast<const uint4 *>(from + 2 * i * stride);
+                if (is_fp4(kKv)) x[i] = fp4_natural(x[i]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4 *>(to + 2 * i * (kDl * 2)) = x[i];
+        }
+        __syncwarp();
+    }
+}
+
 template <int kKv>  // sa_dtype of the latent cache
 __global__ void __launch_bounds__(cta_threads(kProducers<kKv>), 1)
 sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
@@ -146,6 +248,13 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     const int unit = blockIdx.x >> 1;
     const int t = unit / a.splits, split = unit % a.splits;
     const int warp = warp_id(), lane = lane_id();
+    // the selection's entries, 384 threads or more: one step
+    const int32_t *sel = a.idx + (int64_t)t * a.top_k;
+    int32_t entries[6];
+    if (a.rows == nullptr) {
+        pdl_wait();
+        load_entries(sel, a.top_k, 0, entries);
+    }
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -173,14 +282,13 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
             tma_load_2d(sm.kv[2] + b * (kHeadsCta * 128), &tm_q, 64 * b, t * 128 + kHeadsCta * hh,
                         &sm.q_full);
     }
-    pdl_wait();  // the selection comes from the kernel before
     const int32_t *rows = sm.rows;
     if (a.rows != nullptr) {
+        pdl_wait();  // they come from the kernel before
         rows = a.rows + (int64_t)t * a.ld_rows;
         if (threadIdx.x == 0) sm.n_valid = a.n_valid[t];
-    } else {  // 384 threads or more: one step
-        compact_selection<6>(p, t, a.idx + (int64_t)t * a.top_k, a.top_k, kTile, sm.rows,
-                             &sm.n_valid, sm.scratch);
+    } else {
+        compact_selection(p, t, sel, a.top_k, kTile, sm.rows, &sm.n_valid, sm.scratch, entries);
     }
     __syncthreads();
     const uint32_t tmem = sm.tmem_base;
@@ -412,60 +520,13 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
         const float inv_a = (ok && l_a > 0.f) ? 1.f / l_a : 0.f;
         const float inv_b = (ok && l_b > 0.f) ? 1.f / l_b : 0.f;
-        // 32-lane loads: lane 16 + r receives the O row of head 16j + r, whose
-        // sums sit in thread 4(r % 8) (as its first head for r < 8)
-        const int r_o = lane & 15;
-        const float inv_ra = __shfl_sync(0xffffffffu, inv_a, 4 * (r_o & 7));
-        const float inv_rb = __shfl_sync(0xffffffffu, inv_b, 4 * (r_o & 7));
-        const float inv_o = r_o < 8 ? inv_ra : inv_rb;
-        const bool o_lane = lane >= 16;
-        const int head = kHeadsCta * hh + 16 * j + r_o;
-        const int64_t row = (int64_t)t * 128 + head;
-#pragma unroll 2  // two TMEM loads in flight: measured faster than one
-        for (int c = 0; c < kDl / 32; ++c) {
-            float v[32];
-            if (ok && T > 0) {
-                tmem_ld32(tmem + lane_lo + 32 * c, v);
-                tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) v[i] = 0.f;
-            }
-            if (!o_lane) continue;
-            // column c of a 4-bit latent's output holds the dim whose place is c
-            auto o_at = [&](int i) { return v[is_fp4(kKv) ? fp4_place(i) : i] * inv_o; };
-            const int dv = 32 * c;
-            if (a.splits == 1) {
-                if (a.out_dtype == SA_BF16) {
-                    uint32_t w[16];
-#pragma unroll
-                    for (int i = 0; i < 32; i += 2) {
-                        __nv_bfloat162 b2 =
-                            __floats2bfloat162_rn(o_at(i), o_at(i + 1));
-                        w[i / 2] = *reinterpret_cast<uint32_t *>(&b2);
-                    }
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(a.out) +
-                                                           row * kDl + dv);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-                } else {
-                    float4 *dst =
-                        reinterpret_cast<float4 *>(static_cast<float *>(a.out) + row * kDl + dv);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        dst[i] = make_float4(o_at(4 * i), o_at(4 * i + 1), o_at(4 * i + 2),
-                                             o_at(4 * i + 3));
-                }
-            } else {
-                const int64_t prow_i = ((int64_t)t * a.splits + split) * 128 + head;
-                float4 *dst = reinterpret_cast<float4 *>(a.o_part + prow_i * kDl + dv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    dst[i] = make_float4(o_at(4 * i), o_at(4 * i + 1), o_at(4 * i + 2),
-                                         o_at(4 * i + 3));
-            }
+        // the helpers write the second half of the columns
+        if (q4 == 0) {
+            sm.inv[ha] = inv_a;
+            sm.inv[hb] = inv_b;
         }
+        named_barrier(kOutBarrier, 256);
+        write_output<kKv>(sm, a, t, split, hh, j, 0, ok && T > 0, tmem + lane_hi);
         if (q4 == 0) {
             const float lse_a = (ok && l_a > 0.f) ? (m_a + log2f(l_a)) * kLn2 : -INFINITY;
             const float lse_b = (ok && l_b > 0.f) ? (m_b + log2f(l_b)) * kLn2 : -INFINITY;
@@ -488,6 +549,13 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         produce_rows<kKv, kProducers<kKv>>(p, rows + j0 * kTile, T, producer_index(warp), sm.kv,
                                            sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag,
                                            status);
+        if (warp >= 4 && warp < 8) {  // their rows done, they help with the output
+            const bool done = T > 0 && warp_wait(&sm.o_final, 0, abort_flag, status);
+            tc_fence_after();
+            named_barrier(kOutBarrier, 256);
+            write_output<kKv>(sm, a, t, split, hh, warp - 4, 1, done,
+                              tmem + (static_cast<uint32_t>(32 * (warp - 4) + kLaneO) << 16));
+        }
     } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
         // The whole warp waits and computes descriptors, one elected lane issues.
@@ -573,6 +641,18 @@ sfa_combine_kernel(const float *__restrict__ o_part, const float *__restrict__ l
     __shared__ float w_s[kMaxSplits];
     const int64_t row = blockIdx.x;  // t * 128 + head
     const int64_t t = row >> 7, head = row & 127;
+    const float4 *src = reinterpret_cast<const float4 *>(o_part + (t * splits * 128 + head) * kDl) +
+                        threadIdx.x;
+    const int64_t stride = 128 * kDl / 4;  // one split, in float4
+    // sixteen splits' rows in flight, the first ones while the weights are computed
+    constexpr int kAhead = 16;
+    float4 v[kAhead];
+    auto load = [&](int s0) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)
+            if (s0 + i < splits) v[i] = src[(s0 + i) * stride];
+    };
+    load(0);
     if (threadIdx.x < splits) w_s[threadIdx.x] = lse_part[(t * splits + threadIdx.x) * 128 + head];
     __syncthreads();
     if (threadIdx.x < 32) {
@@ -595,17 +675,17 @@ sfa_combine_kernel(const float *__restrict__ o_part, const float *__restrict__ l
     }
     __syncthreads();
     float acc[4] = {0.f, 0.f, 0.f, 0.f};
-    const float4 *src = reinterpret_cast<const float4 *>(o_part + (t * splits * 128 + head) * kDl) +
-                        threadIdx.x;
-    const int64_t stride = 128 * kDl / 4;  // one split, in float4
-#pragma unroll 8
-    for (int s = 0; s < splits; ++s) {
-        const float w = w_s[s];
-        const float4 v = src[s * stride];
-        acc[0] += w * v.x;
-        acc[1] += w * v.y;
-        acc[2] += w * v.z;
-        acc[3] += w * v.w;
+    for (int s0 = 0; s0 < splits; s0 += kAhead) {
+        if (s0 > 0) load(s0);
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (s0 + i >= splits) break;
+            const float w = w_s[s0 + i];
+            acc[0] += w * v[i].x;
+            acc[1] += w * v[i].y;
+            acc[2] += w * v[i].z;
+            acc[3] += w * v[i].w;
+        }
     }
     if (out_dtype == SA_BF16) {
         __nv_bfloat162 a = __floats2bfloat162_rn(acc[0], acc[1]);

@@ -48,8 +48,10 @@ weights_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t
     __shared__ int32_t n_s;
     const int t = blockIdx.x;
     int32_t *pos = kept + (int64_t)t * ld;
-    compact_selection<4>(p, t, idx + (int64_t)t * K, K, kTile, rows + (int64_t)t * ld, &n_s,
-                         scratch, pos);
+    const int32_t *sel = idx + (int64_t)t * K;
+    int32_t entries[4];
+    load_entries(sel, K, 0, entries);
+    compact_selection(p, t, sel, K, kTile, rows + (int64_t)t * ld, &n_s, scratch, entries, pos);
     __syncthreads();
     const int32_t n = n_s;
     int32_t *st = starts + (int64_t)t * ld_starts;

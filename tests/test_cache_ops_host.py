@@ -187,6 +187,21 @@ def test_evict_tokens_refusals(L):
         _abi.SA_ERR_UNSUPPORTED
 
 
+@pytest.mark.parametrize("fmt", [{}, {"kv_dtype": _abi.SA_MXFP4, **FP4}])
+def test_attention_refuses_an_output_its_stores_cannot_reach(L, fmt):
+    c, q = good_cache(**fmt), good_query()
+    ws = _abi.SA_ERR_WORKSPACE                                   # all else in order
+    for out, k, want in ((FAKE, 2048, ws), (FAKE + 8, 2048, _abi.SA_ERR_INVALID_ARG),
+                         (FAKE + 2, 1, _abi.SA_ERR_INVALID_ARG), (FAKE + 8, 2049, ws)):
+        assert L.sa_sparse_mla_attn(ctypes.byref(c), ctypes.byref(q), FAKE, k, out,
+                                    _abi.SA_BF16, None, FAKE, 8, None) == want
+        assert L.sa_decode(ctypes.byref(c), ctypes.byref(q), k, None, out, _abi.SA_BF16, None,
+                           FAKE, 8, None) == want
+    few = good_query(heads=16)                                   # the CUDA-core kernel
+    assert L.sa_sparse_mla_attn(ctypes.byref(c), ctypes.byref(few), FAKE, 64, FAKE + 8,
+                                _abi.SA_BF16, None, FAKE, 8, None) == ws
+
+
 def test_new_names_are_bound():
     assert _abi.DTYPES["mxfp4"] == 4 and _abi.DTYPES["nvfp4"] == 5
     assert torch.uint8 is not None and len(set(_abi.EXPORTS)) == len(_abi.EXPORTS)
