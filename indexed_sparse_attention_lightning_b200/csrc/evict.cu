@@ -68,9 +68,15 @@ __device__ __forceinline__ uint32_t keep_key(float a) {
     return a != a ? 0xFFFFFFFFu : order_key(a);
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
-                     : "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 // A word of shared memory of the cluster's CTA `rank`, at this CTA's address `p`.
 __device__ __forceinline__ int32_t peer_word(const int32_t *p, int rank) {
@@ -299,43 +305,59 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
     int32_t gt_before = gt_s[warp], eq_before = eq_s[warp];
     gt_before += peer_sum(&totals[0], rank, ctas);
     eq_before += peer_sum(&totals[1], rank, ctas);
-    if (ctas > 1) cluster_sync();  // no CTA leaves while another reads its shared memory
+    if (ctas > 1) cluster_arrive();  // this CTA has read the others' shared memory
 
     // ascending emission: a warp's entries start behind all earlier ones that stay
     int32_t on = eq_before;                    // entries on the threshold so far
     int32_t slot = gt_before + min(on, ties);  // kept entries so far
     const uint32_t below = (1u << lane) - 1u;
-    for (int32_t i0 = w0; i0 < w1; i0 += kSelectStep) {
-        const uint4 k4 = want > 0 ? mine.keys(i0) : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
-        int32_t rank_on = on;  // entries on the threshold before this lane's
-        bool tie[4], keep[4];
+    constexpr int kSteps = 4;  // whose pages and sums are loaded together
+    for (int32_t g0 = w0; g0 < w1; g0 += kSteps * kSelectStep) {
+        int32_t page[kSteps];
+        float sum[kSteps][4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            tie[e] = k[e] != 0u && k[e] == threshold && want > 0;
-            const uint32_t bits = __ballot_sync(0xffffffffu, tie[e]);
-            rank_on += __popc(bits & below);
-            on += __popc(bits);
-        }
-        int32_t at = slot;
+        for (int u = 0; u < kSteps; ++u) {
+            const int32_t i = g0 + u * kSelectStep + 4 * lane;
+            page[u] = i < w1 ? __ldg(st + (i >> 6)) : 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int32_t i = i0 + 4 * lane + e;
-            keep[e] = k[e] > threshold || (tie[e] && rank_on < ties) ||
-                      (i < w1 && (i < lo || i >= hi));
-            rank_on += tie[e];
-            const uint32_t bits = __ballot_sync(0xffffffffu, keep[e]);
-            at += __popc(bits & below);
-            slot += __popc(bits);
+            for (int e = 0; e < 4; ++e)
+                sum[u][e] = a.acc_out != nullptr && i + e < w1 ? __ldg(acc + i + e) : 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (!keep[e]) continue;
-            const int32_t i = i0 + 4 * lane + e;
-            a.src_row[out0 + at] = __ldg(st + (i >> 6)) * 64 + (i & 63);
-            if (a.src_pos != nullptr) a.src_pos[out0 + at] = i;
-            if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = __ldg(acc + i);
-            ++at;
+        for (int u = 0; u < kSteps; ++u) {
+            const int32_t i0 = g0 + u * kSelectStep;
+            if (i0 >= w1) break;
+            const uint4 k4 = want > 0 ? mine.keys(i0) : make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+            int32_t rank_on = on;  // entries on the threshold before this lane's
+            bool tie[4], keep[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                tie[e] = k[e] != 0u && k[e] == threshold && want > 0;
+                const uint32_t bits = __ballot_sync(0xffffffffu, tie[e]);
+                rank_on += __popc(bits & below);
+                on += __popc(bits);
+            }
+            int32_t at = slot;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int32_t i = i0 + 4 * lane + e;
+                keep[e] = k[e] > threshold || (tie[e] && rank_on < ties) ||
+                          (i < w1 && (i < lo || i >= hi));
+                rank_on += tie[e];
+                const uint32_t bits = __ballot_sync(0xffffffffu, keep[e]);
+                at += __popc(bits & below);
+                slot += __popc(bits);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (!keep[e]) continue;
+                const int32_t i = i0 + 4 * lane + e;
+                a.src_row[out0 + at] = page[u] * 64 + (i & 63);
+                if (a.src_pos != nullptr) a.src_pos[out0 + at] = i;
+                if (a.acc_out != nullptr) a.acc_out[(int64_t)b * a.ld_out + at] = sum[u][e];
+                ++at;
+            }
         }
     }
     const int32_t first = rank * kSelectThreads + tid;
@@ -349,6 +371,8 @@ evict_select_kernel(const EvictArgs a, int32_t ctas, int32_t cache_per) {
         a.kept[b] = kept;
         a.dst_len[b] = kept;
     }
+    __syncwarp();
+    if (ctas > 1) cluster_wait();  // no CTA leaves while another reads its shared memory
 }
 
 // blockIdx.y: the sequence.  One warp moves `rows` consecutive kept tokens at a

@@ -160,8 +160,8 @@ struct Layout {
         lse_part;
     size_t indexer_total, decode_total;
     size_t attn_o_part, attn_lse_part, attn_total;
-    // accumulated weights: status | rows | kept | w [n_q, weights_ld] each |
-    // n_valid [n_q] | starts [n_q, weights_starts_ld]
+    // accumulated weights: status | rows [n_q, weights_splits, weights_ld] | kept and w
+    // [n_q, weights_ld] each | n_valid [n_q] | starts [n_q, weights_starts_ld]
     size_t wt_rows, wt_kept, wt_w, wt_n_valid, wt_starts, wt_total;
 };
 
@@ -169,7 +169,7 @@ size_t part_bytes(size_t nq, int32_t splits, size_t per) {
     return splits > 1 ? per * nq * (size_t)splits : 0;
 }
 
-Layout make_layout(const sa_query *q, int32_t top_k, int32_t batch) {
+Layout make_layout(const sa_query *q, int32_t top_k, const sa_cache *c) {
     Layout l{};
     const size_t nq = q->n_q > 0 ? (size_t)q->n_q : 0;
     l.ld = round_up(q->max_visible > 0 ? q->max_visible : 1, 128);
@@ -197,12 +197,13 @@ Layout make_layout(const sa_query *q, int32_t top_k, int32_t batch) {
     l.attn_lse_part = align_up(l.attn_o_part + o_bytes);
     l.attn_total = align_up(l.attn_lse_part + lse_bytes);
     const size_t wt_bytes = 4 * nq * (size_t)weights_ld(top_k);
+    const size_t wt_splits = (size_t)weights_splits(q->n_q, top_k, c->kv_dtype);
     l.wt_rows = align_up(kStatusBytes);
-    l.wt_kept = align_up(l.wt_rows + wt_bytes);
+    l.wt_kept = align_up(l.wt_rows + wt_splits * wt_bytes);
     l.wt_w = align_up(l.wt_kept + wt_bytes);
     l.wt_n_valid = align_up(l.wt_w + wt_bytes);
     l.wt_starts = align_up(l.wt_n_valid + sizeof(int32_t) * nq);
-    const size_t starts_ld = (size_t)weights_starts_ld(q->n_q, batch, q->max_visible);
+    const size_t starts_ld = (size_t)weights_starts_ld(q->n_q, c->batch, q->max_visible);
     l.wt_total = align_up(l.wt_starts + sizeof(int32_t) * nq * starts_ld);
     return l;
 }
@@ -312,7 +313,7 @@ size_t sa_workspace_size(const sa_cache *cache, const sa_query *query, int32_t t
     if ((uses & (SA_WS_TOPK | SA_WS_DECODE | SA_WS_ATTN | SA_WS_WEIGHTS)) &&
         (top_k <= 0 || top_k > kMaxTopK))
         return 0;
-    const Layout l = make_layout(query, top_k, cache->batch);
+    const Layout l = make_layout(query, top_k, cache);
     size_t need = kStatusBytes;
     if (uses & SA_WS_INDEXER) need = std::max(need, l.indexer_total);
     if (uses & SA_WS_ATTN) need = std::max(need, l.attn_total);
@@ -329,7 +330,7 @@ sa_status sa_indexer_score(const sa_cache *cache, const sa_query *query, float *
     if (st != SA_OK) return st;
     if ((st = check_query(query, cache, true, false)) != SA_OK) return st;
     if (query->n_q > 0 && (!scores || ld_scores < query->max_visible)) return SA_ERR_INVALID_ARG;
-    const Layout l = make_layout(query, 1, cache->batch);
+    const Layout l = make_layout(query, 1, cache);
     if ((st = check_workspace(workspace, workspace_bytes, l.indexer_total)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = clear_status(workspace, s)) != SA_OK) return st;
@@ -364,7 +365,7 @@ sa_status sa_sparse_mla_attn(const sa_cache *cache, const sa_query *query, const
     if (out_dtype != SA_BF16 && out_dtype != SA_F32) return SA_ERR_UNSUPPORTED;
     if (query->n_q > 0 && (!idx || !out)) return SA_ERR_INVALID_ARG;
     if (!out_fits(cache, query, top_k, out)) return SA_ERR_INVALID_ARG;
-    const Layout l = make_layout(query, top_k, cache->batch);
+    const Layout l = make_layout(query, top_k, cache);
     if ((st = check_workspace(workspace, workspace_bytes, l.attn_total)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = clear_status(workspace, s)) != SA_OK) return st;
@@ -391,7 +392,7 @@ static sa_status decode_impl(const sa_cache *cache, const sa_query *query, int32
     if (out_dtype != SA_BF16 && out_dtype != SA_F32) return SA_ERR_UNSUPPORTED;
     if (query->n_q > 0 && !out && !cand) return SA_ERR_INVALID_ARG;
     if (!out_fits(cache, query, top_k, out)) return SA_ERR_INVALID_ARG;
-    const Layout l = make_layout(query, top_k, cache->batch);
+    const Layout l = make_layout(query, top_k, cache);
     if ((st = check_workspace(workspace, workspace_bytes, l.decode_total)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     auto mark = [&](int i) -> sa_status {
@@ -588,7 +589,7 @@ sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *query, co
         return SA_ERR_INVALID_ARG;
     if (!rows_fit_32(cache) || (int64_t)cache->batch * cache->max_pages >= (int64_t(1) << 31))
         return SA_ERR_UNSUPPORTED;
-    const Layout l = make_layout(query, top_k, cache->batch);
+    const Layout l = make_layout(query, top_k, cache);
     if ((st = check_workspace(workspace, workspace_bytes, l.wt_total)) != SA_OK) return st;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if ((st = clear_status(workspace, s)) != SA_OK) return st;

@@ -4,12 +4,13 @@
 // For query t and its selected rows s (the attention's own selection and lse):
 //     w[t,s] = sum_h exp(sm_scale * q[t,h,:] . kv[s,:] - lse[t,h])
 //     acc_out[b,s] = decay * acc_in[b,s] + sum_{t of b} w[t,s]
-// Three kernels: rows (each query's selection as physical rows and positions),
-// weights (one fp32 w per selected entry; on the tensor cores for the
-// attention's production shape, on CUDA cores otherwise) and sum.  Sums over queries are taken
-// in the order of t without atomics between CTAs, so results are reproducible:
-// in the sum kernel each warp owns a range of one sequence's positions, keeps
-// its sums in shared memory and walks the queries in order.
+// For the attention's production shape two kernels: weights (each query's
+// selection as physical rows and positions, then one fp32 w per selected entry, on
+// the tensor cores) and sum; for other shapes a rows kernel in front of a weights
+// kernel on CUDA cores.  Sums over queries are taken in the order of t without
+// atomics between CTAs, so results are reproducible: in the sum kernel each warp
+// owns a range of one sequence's positions, keeps its sums in shared memory and
+// walks the queries in order.
 #include "common.cuh"
 #include "internal.h"
 #include "sfa_gather.cuh"
@@ -34,9 +35,26 @@ static_assert(SumFew::kRange == 1 << 10 && SumMany::kRange == 1 << 8, "range_log
 bool sum_many(int32_t n_q, int32_t batch) { return n_q > 16 * (int64_t)batch; }
 
 // ------------------------------------------------------------------- rows ---
-// starts[t, c] = first kept entry of query t at or past position c * range
-// (the last column: all of them); starts[t, 0] = -1 where the kept positions
-// do not ascend strictly.
+// What the sum kernel needs to find a query's entries, from its n kept positions
+// (by `count` threads of one CTA): starts[c] = first kept entry at or past position
+// c * range (the last column: all of them).  starts[0], which would be 0, is the
+// caller's 0, or -1 where the kept positions do not ascend strictly.
+__device__ __forceinline__ void write_starts(const int32_t *pos, int32_t n, int32_t *starts,
+                                             int32_t ld_starts, int32_t range_log2, int32_t thread,
+                                             int32_t count) {
+    for (int32_t i = thread; i <= n; i += count) {
+        const int32_t at = i < n ? pos[i] : -1, before = i > 0 ? pos[i - 1] : -1;
+        if (i > 0 && i < n && before >= at) {
+            starts[0] = -1;
+            continue;
+        }
+        const int32_t c0 = i > 0 ? (before >> range_log2) + 1 : 1;
+        const int32_t c1 = i < n ? at >> range_log2 : ld_starts - 1;
+        for (int32_t c = c0; c <= c1; ++c) starts[c] = i;
+    }
+}
+
+// For the CUDA-core kernel; the tensor-core one compacts its selection itself.
 constexpr int kRowsThreads = 512;
 __global__ void __launch_bounds__(kRowsThreads)
 weights_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, int32_t ld,
@@ -47,30 +65,15 @@ weights_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t
     __shared__ int32_t scratch[kCompactScratch];
     __shared__ int32_t n_s;
     const int t = blockIdx.x;
-    int32_t *pos = kept + (int64_t)t * ld;
+    int32_t *pos = kept + (int64_t)t * ld, *st = starts + (int64_t)t * ld_starts;
     const int32_t *sel = idx + (int64_t)t * K;
     int32_t entries[4];
     load_entries(sel, K, 0, entries);
+    if (threadIdx.x == 0) st[0] = 0;
     compact_selection(p, t, sel, K, kTile, rows + (int64_t)t * ld, &n_s, scratch, entries, pos);
     __syncthreads();
-    const int32_t n = n_s;
-    int32_t *st = starts + (int64_t)t * ld_starts;
-    int32_t falls = 0;
-    for (int32_t i = threadIdx.x; i <= n; i += kRowsThreads) {
-        const int32_t at = i < n ? pos[i] : -1, before = i > 0 ? pos[i - 1] : -1;
-        if (i > 0 && i < n && before >= at) {
-            falls = 1;
-            continue;
-        }
-        const int32_t c0 = i > 0 ? (before >> range_log2) + 1 : 0;
-        const int32_t c1 = i < n ? at >> range_log2 : ld_starts - 1;
-        for (int32_t c = c0; c <= c1; ++c) st[c] = i;
-    }
-    falls = __syncthreads_or(falls);
-    if (threadIdx.x == 0) {
-        n_valid[t] = n;
-        if (falls) st[0] = -1;
-    }
+    write_starts(pos, n_s, st, ld_starts, range_log2, threadIdx.x, kRowsThreads);
+    if (threadIdx.x == 0) n_valid[t] = n_s;
 }
 
 // ---------------------------------------------------- weights, any shape ---
@@ -145,9 +148,14 @@ cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t l
 // of its tiles: S = Q K^T with M = 128 heads, N = 64 keys, K = 576, Q in TMEM
 // (288 columns), two S buffers behind it.  There is no P V, so a row is gathered
 // once per query, and a stage is free again as soon as its S is done.
-//   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2,
-//               before the wait on the rows kernel), then issues the MMAs;
-//   warps 1-7   gather the rows (sfa_gather.cuh; with warps 12-20 for a 4-bit latent);
+//   all         turn the query's selection into rows, each CTA for itself while Q
+//               is on its way (64 queries 51.6 us, with a kernel in front 53.7; 256
+//               queries, two CTAs after one another, 128 and 126.5);
+//   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2), then
+//               the warp issues the MMAs;
+//   warps 1-7   gather the rows (sfa_gather.cuh; with warps 12-20 for a 4-bit
+//               latent); those of the query's first CTA then note where each range
+//               of positions starts, for the sum kernel;
 //   warps 8-11  move Q into TMEM (warp 8 + j: heads 32j .. 32j + 31, one per
 //               lane), then read S with 16-lane loads, so that a thread holds
 //               four heads of sixteen keys: exp2 of the logits minus the heads'
@@ -177,6 +185,7 @@ struct WeightsSmem {
     uint64_t s_full[2], s_empty[2], q_full, q_ready, done;
     uint32_t tmem_base;
     int abort;
+    int32_t n_valid, scratch[kCompactScratch];
 };
 static_assert(sizeof(WeightsSmem) + 1024 <= 232448, "shared memory budget of one CTA");
 
@@ -227,7 +236,7 @@ __device__ __forceinline__ void produce_e4m3_pairs(const PathParams &p, const in
             }
         }
     };
-    auto rows_of = [&](int n) { return n < T ? __ldg(tile_rows + n * kKeys + lane) : 0; };
+    auto rows_of = [&](int n) { return n < T ? tile_rows[n * kKeys + lane] : 0; };
     int32_t rows1 = rows_of(1);
     if (T > 0) load(rows_of(0), code, rp, sc);
     for (int n = 0; n < T; ++n) {
@@ -289,13 +298,21 @@ constexpr int kProducers = is_fp4(kKv) ? kFp4WeightsWarps : kProducerWarps;
 
 template <int kKv>  // sa_dtype of the latent cache
 __global__ void __launch_bounds__(cta_threads(kProducers<kKv>), 1)
-weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p, int32_t splits,
-                   const float *__restrict__ lse, int32_t ld, const int32_t *__restrict__ rows,
-                   const int32_t *__restrict__ n_valid_of, float *__restrict__ w) {
+weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
+                   const int32_t *__restrict__ idx, int32_t K, int32_t splits,
+                   const float *__restrict__ lse, int32_t ld, int32_t ld_starts,
+                   int32_t range_log2, int32_t *rows_of, int32_t *kept, int32_t *n_valid_of,
+                   int32_t *starts_of, float *__restrict__ w) {
     extern __shared__ uint8_t smem_raw[];
     WeightsSmem &sm = *reinterpret_cast<WeightsSmem *>(align1024(smem_raw));
     const int t = blockIdx.x / splits, split = blockIdx.x % splits;
     const int warp = warp_id(), lane = lane_id();
+    const int32_t *sel = idx + (int64_t)t * K;
+    int32_t *rows = rows_of + (int64_t)blockIdx.x * ld;  // this CTA's own
+    int32_t *pos = kept + (int64_t)t * ld, *starts = starts_of + (int64_t)t * ld_starts;
+    int32_t entries[6];
+    pdl_wait();
+    load_entries(sel, K, 0, entries);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -324,11 +341,14 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
                 tma_load_2d(sm.kv[1 + half] + b * (64 * 128), &tm_q, 64 * b,
                             t * kHeads + 64 * half, &sm.q_full);
     }
-    pdl_wait();  // rows and counts come from the rows kernel
+    if (threadIdx.x == 0 && split == 0) starts[0] = 0;
+    compact_selection(p, t, sel, K, kTile, rows, &sm.n_valid, sm.scratch, entries,
+                      split == 0 ? pos : nullptr);
+    __syncthreads();
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort;
     int32_t *status = p.status;
-    const int32_t n_valid = n_valid_of[t];
+    const int32_t n_valid = sm.n_valid;
     int32_t j0, j1;
     constexpr int kKeys = kKeysOf<kKv>;
     split_range<kKeys>(n_valid, split, splits, j0, j1);
@@ -427,13 +447,19 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
             }
         }
     } else if (warp >= 1) {
-        const int32_t *tile_rows = rows + (int64_t)t * ld + (int64_t)j0 * kKeys;
+        const int32_t *tile_rows = rows + (int64_t)j0 * kKeys;
         if constexpr (kKv == SA_E4M3)
             produce_e4m3_pairs(p, tile_rows, T, warp - 1, sm, abort_flag, status);
         else
             produce_rows<kKv, kProducers<kKv>>(p, tile_rows, T, producer_index(warp), sm.kv,
                                                sm.kv_full, sm.kv_empty, &sm.q_ready, 1,
                                                abort_flag, status);
+        if (split == 0) {
+            const int32_t thread = 32 * producer_index(warp) + lane;
+            write_starts(pos, n_valid, starts, ld_starts, range_log2, thread,
+                         32 * kProducers<kKv>);
+            if (thread == 0) n_valid_of[t] = n_valid;
+        }
     } else if (T > 0) {
         // the whole warp waits and computes descriptors, one lane issues
         constexpr uint32_t id_s = instr_desc(kHeads, kTile, 1 /*bf16*/, 0, 0);
@@ -487,9 +513,10 @@ bool weights_mma_supported(const PathParams &p) {
            p.d_rope == kDr;
 }
 
-cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t top_k, int32_t ld,
-                               const int32_t *rows, const int32_t *n_valid, float *w,
-                               cudaStream_t s) {
+cudaError_t launch_weights_mma(const PathParams &p, const int32_t *idx, int32_t top_k,
+                               const float *lse, int32_t ld, int32_t ld_starts,
+                               int32_t range_log2, int32_t *rows, int32_t *kept, int32_t *n_valid,
+                               int32_t *starts, float *w, cudaStream_t s) {
     CUtensorMap tq;
     if (!encode_tmap_2d(&tq, 2, p.q, kD, (uint64_t)p.n_q * kHeads, kD * 2, 64, 64, true))
         return cudaErrorInvalidValue;
@@ -501,15 +528,13 @@ cudaError_t launch_weights_mma(const PathParams &p, const float *lse, int32_t to
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    // one CTA per SM: split a query's tiles while there are SMs without one
-    const int32_t tiles =
-        (int32_t)ceil_div(top_k, p.kv_dtype == SA_E4M3 ? kKeysOf<SA_E4M3> : kTile);
-    const int32_t splits = std::max(1, std::min(tiles, num_sms() / p.n_q));
+    const int32_t splits = weights_splits(p.n_q, top_k, p.kv_dtype);
     const int threads =
         cta_threads(is_fp4(p.kv_dtype) ? kProducers<SA_MXFP4> : kProducers<SA_BF16>);
     count_launch();
     return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(threads), smem,
-                      s, tq, p, splits, lse, ld, rows, n_valid, w);
+                      s, tq, p, idx, top_k, splits, lse, ld, ld_starts, range_log2, rows, kept,
+                      n_valid, starts, w);
 }
 
 // -------------------------------------------------------------------- sum ---
@@ -648,6 +673,14 @@ cudaError_t launch_weights_sum(const PathParams &p, int32_t ld, int32_t ld_start
 
 }  // namespace
 
+// one CTA per SM: split a query's tiles while there are SMs without one
+int32_t weights_splits(int32_t n_q, int32_t top_k, int32_t kv_dtype) {
+    if (n_q <= 0 || top_k <= 0) return 1;
+    const int32_t tiles =
+        (int32_t)ceil_div(top_k, kv_dtype == SA_E4M3 ? kKeysOf<SA_E4M3> : kTile);
+    return std::max(1, std::min(tiles, num_sms() / n_q));
+}
+
 int32_t weights_ld(int32_t top_k) { return (int32_t)round_up(top_k > 0 ? top_k : 1, kTile); }
 
 int32_t weights_starts_ld(int32_t n_q, int32_t batch, int32_t max_visible) {
@@ -664,14 +697,16 @@ cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, i
     const int32_t ld = weights_ld(top_k);
     const int32_t ld_starts = weights_starts_ld(p.n_q, p.batch, p.max_visible);
     cudaError_t e;
-    if (p.n_q > 0) {
+    const int32_t range_log2 = many ? 8 : 10;
+    if (p.n_q > 0 && weights_mma_supported(p)) {
+        e = launch_weights_mma(p, idx, top_k, lse, ld, ld_starts, range_log2, rows, kept, n_valid,
+                               starts, w, s);
+        if (e != cudaSuccess) return e;
+    } else if (p.n_q > 0) {
         count_launch();
         e = launch_pdl(weights_rows_kernel, dim3((unsigned)p.n_q), dim3(kRowsThreads), 0, s, p, idx,
-                       top_k, ld, ld_starts, many ? 8 : 10, rows, kept, n_valid, starts);
-        if (e != cudaSuccess) return e;
-        e = weights_mma_supported(p)
-                ? launch_weights_mma(p, lse, top_k, ld, rows, n_valid, w, s)
-                : launch_weights_simt(p, lse, ld, rows, n_valid, w, s);
+                       top_k, ld, ld_starts, range_log2, rows, kept, n_valid, starts);
+        if (e == cudaSuccess) e = launch_weights_simt(p, lse, ld, rows, n_valid, w, s);
         if (e != cudaSuccess) return e;
     }
     return many ? launch_weights_sum<SumMany>(p, ld, ld_starts, kept, n_valid, starts, w, acc_in,
