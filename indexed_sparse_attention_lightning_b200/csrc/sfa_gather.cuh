@@ -3,6 +3,8 @@
 // sparse attention (sfa_mma.cu) and the accumulated weights (weights.cu).
 #pragma once
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "internal.h"
 #include "sm100.cuh"
@@ -54,22 +56,54 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-// Eight codes of one word times a scale -> eight bf16 in fp4_order.  The sign,
-// exponent and mantissa bits of an e2m1 code, put at bits 15 and 8..6, are a
-// bf16 of the code's value times 2^-126 (its two subnormals are bf16's too);
-// that times 2^126 and the scale has at most 6 significant bits, so both
+// 4-bit rows lie in the stages times 2^-9: the logits' factor and the output take
+// 2^9, and Q's rope 2^-9 (fp4_rope).  The sign, exponent and mantissa bits of an
+// e2m1 code, put at bits 15 and 8..6, are a bf16 of the code's value times 2^-126
+// (its two subnormals are bf16's too).  So one product with scale times 2^117, which
+// bf16 holds for scales up to 2^9 (every NVFP4 scale), makes the value; with larger
+// ones (kOnce false) it takes two.  A value has at most 6 significant bits, so the
 // products are exact unless they leave bf16's range.
-__device__ __forceinline__ uint4 fp4_to_bf16(uint32_t w, uint32_t scale2) {
+// The decoding warps bound the kernels by their instructions: 64 queries over
+// MXFP4 take 66 us, with two products everywhere 68; 512 over NVFP4 398 and 403; the
+// weights of 256 over MXFP4 119 and 126.
+constexpr float kFp4Up = 512.0f;
+__device__ __forceinline__ uint4 fp4_rope(uint4 x) {
+    constexpr uint32_t kDown = 0x3B003B00u;  // 2^-9, twice
+    return make_uint4(bf16x2_mul(x.x, kDown), bf16x2_mul(x.y, kDown), bf16x2_mul(x.z, kDown),
+                      bf16x2_mul(x.w, kDown));
+}
+
+// The factor of codes with this scale byte, twice.  No branches: with them the
+// attention of 64 queries over MXFP4 took 83 us instead of 68.
+template <int kKv, bool kOnce>
+__device__ __forceinline__ uint32_t fp4_factor(uint32_t byte) {
+    if constexpr (kKv == SA_NVFP4) {
+        const __nv_bfloat162 s = __float2bfloat162_rn(fp4_scale_value(kKv, byte) * 0x1p117f);
+        return *reinterpret_cast<const uint32_t *>(&s);
+    } else {
+        // an E8M0 byte is the exponent of a bf16 (0: its subnormal 2^-127; 255: NaN)
+        const uint32_t one =
+            kOnce ? (byte + 117) << 7 : byte << 7 | ((byte - 1) >> 31 | (byte + 1) >> 8) << 6;
+        return __byte_perm(one, one, 0x1010);
+    }
+}
+// Whether kOnce holds for the byte (NVFP4: always).
+__device__ __forceinline__ bool fp4_once(uint32_t byte) { return byte <= 127 + 9; }
+
+// Eight codes of one word -> eight bf16 in fp4_order.
+template <bool kOnce>
+__device__ __forceinline__ uint4 fp4_to_bf16(uint32_t w, uint32_t factor) {
     constexpr uint32_t kSign = 0x80008000u, kMag = 0x01C001C0u;
-    constexpr uint32_t kUp = 0x7E807E80u;  // 2^126, twice
-    const uint32_t p0 = ((w << 12) & kSign) | ((w << 6) & kMag);
-    const uint32_t p1 = ((w << 8) & kSign) | ((w << 2) & kMag);
-    const uint32_t p2 = ((w << 4) & kSign) | ((w >> 2) & kMag);
-    const uint32_t p3 = (w & kSign) | ((w >> 6) & kMag);
-    return make_uint4(bf16x2_mul(bf16x2_mul(p0, kUp), scale2),
-                      bf16x2_mul(bf16x2_mul(p1, kUp), scale2),
-                      bf16x2_mul(bf16x2_mul(p2, kUp), scale2),
-                      bf16x2_mul(bf16x2_mul(p3, kUp), scale2));
+    constexpr uint32_t kUp = 0x7A007A00u;  // 2^117, twice
+    uint32_t p[4] = {((w << 12) & kSign) | ((w << 6) & kMag),
+                     ((w << 8) & kSign) | ((w << 2) & kMag),
+                     ((w << 4) & kSign) | ((w >> 2) & kMag), (w & kSign) | ((w >> 6) & kMag)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (!kOnce) p[i] = bf16x2_mul(p[i], kUp);
+        p[i] = bf16x2_mul(p[i], factor);
+    }
+    return make_uint4(p[0], p[1], p[2], p[3]);
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
@@ -177,6 +211,29 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
         const int rk = 4 * pw + (lane >> 3);
         const uint32_t rope_at = (rk >> 3) * kGroupBytes + (kBlocks - 1) * 1024 + (rk & 7) * 128 +
                                  (((lane & 7) ^ (rk & 7)) << 4);
+        auto decode = [&](auto once, uint8_t *stage) {
+            constexpr bool kOnce = decltype(once)::value;
+#pragma unroll
+            for (int i = 0; i < kSlots; ++i) {
+                uint8_t *dst = stage + i * (kWarps / 4 * kGroupBytes);
+                // scales of the pieces in the order they are decoded
+                uint32_t s0 = sb[i], s1 = sb[i];
+                if (kScales == 2) {
+                    s0 = flip ? sb[i] >> 8 : sb[i] & 255u;
+                    s1 = flip ? sb[i] & 255u : sb[i] >> 8;
+                }
+                const uint32_t f0 = fp4_factor<kKv, kOnce>(s0), f1 = fp4_factor<kKv, kOnce>(s1);
+                const bool swap = turn & 1;
+                const uint32_t w0 = swap ? code[i][0].y : code[i][0].x;
+                const uint32_t w1 = swap ? code[i][0].x : code[i][0].y;
+                const uint32_t w2 = swap ? code[i][1].y : code[i][1].x;
+                const uint32_t w3 = swap ? code[i][1].x : code[i][1].y;
+                *reinterpret_cast<uint4 *>(dst + piece[0]) = fp4_to_bf16<kOnce>(w0, f0);
+                *reinterpret_cast<uint4 *>(dst + piece[1]) = fp4_to_bf16<kOnce>(w1, f0);
+                *reinterpret_cast<uint4 *>(dst + piece[2]) = fp4_to_bf16<kOnce>(w2, f1);
+                *reinterpret_cast<uint4 *>(dst + piece[3]) = fp4_to_bf16<kOnce>(w3, f1);
+            }
+        };
         int32_t lo, hi, lo1, hi1;
         row_pair(0, lo, hi);
         row_pair(1, lo1, hi1);
@@ -207,28 +264,14 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             }
             if (!stage_free(n)) break;
             uint8_t *stage = stages[st];
+            if constexpr (kKv == SA_NVFP4) {
+                decode(std::true_type(), stage);
+            } else {
+                uint32_t most = sb[0];
 #pragma unroll
-            for (int i = 0; i < kSlots; ++i) {
-                uint8_t *dst = stage + i * (kWarps / 4 * kGroupBytes);
-                // scales of the pieces in the order they are decoded
-                uint32_t s0 = sb[i], s1 = sb[i];
-                if (kScales == 2) {
-                    s0 = flip ? sb[i] >> 8 : sb[i] & 255u;
-                    s1 = flip ? sb[i] & 255u : sb[i] >> 8;
-                }
-                const __nv_bfloat162 a = __float2bfloat162_rn(fp4_scale_value(kKv, s0));
-                const __nv_bfloat162 b = __float2bfloat162_rn(fp4_scale_value(kKv, s1));
-                const uint32_t a2 = *reinterpret_cast<const uint32_t *>(&a);
-                const uint32_t b2 = *reinterpret_cast<const uint32_t *>(&b);
-                const bool swap = turn & 1;
-                const uint32_t w0 = swap ? code[i][0].y : code[i][0].x;
-                const uint32_t w1 = swap ? code[i][0].x : code[i][0].y;
-                const uint32_t w2 = swap ? code[i][1].y : code[i][1].x;
-                const uint32_t w3 = swap ? code[i][1].x : code[i][1].y;
-                *reinterpret_cast<uint4 *>(dst + piece[0]) = fp4_to_bf16(w0, a2);
-                *reinterpret_cast<uint4 *>(dst + piece[1]) = fp4_to_bf16(w1, a2);
-                *reinterpret_cast<uint4 *>(dst + piece[2]) = fp4_to_bf16(w2, b2);
-                *reinterpret_cast<uint4 *>(dst + piece[3]) = fp4_to_bf16(w3, b2);
+                for (int i = 1; i < kSlots; ++i) most = max(most, sb[i]);
+                if (__all_sync(0xffffffffu, fp4_once(most))) decode(std::true_type(), stage);
+                else decode(std::false_type(), stage);
             }
 #pragma unroll
             for (int i = 0; i < kRopes; ++i)

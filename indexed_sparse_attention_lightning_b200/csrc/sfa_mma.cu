@@ -88,7 +88,7 @@ struct SfaSmem {
     uint64_t s_full[2], p_full[kStages], o_final, q_full, q_ready;
     uint32_t tmem_base;
     int abort;
-    float inv[kHeadsCta];  // 1 / l
+    float inv[kHeadsCta];  // 1 / l (4 bits: times kFp4Up)
     int32_t n_valid, scratch[kCompactScratch];
     int32_t rows[kMaxK];  // the selection's physical rows, whole tiles
 };
@@ -321,7 +321,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         uint4 x = *reinterpret_cast<const uint4 *>(qr + ((c ^ (h & 7)) << 4));
-                        if (is_fp4(kKv) && b < kBlocks - 1) x = fp4_order(x);
+                        if (is_fp4(kKv)) x = b < kBlocks - 1 ? fp4_order(x) : fp4_rope(x);
                         v[4 * c] = x.x;
                         v[4 * c + 1] = x.y;
                         v[4 * c + 2] = x.z;
@@ -339,7 +339,7 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         // ----------------------------------------------- online softmax ---
         // The loop never leaves early: after a failed wait (a timeout raised
         // the abort flag) it keeps going without waiting or touching TMEM.
-        const float sl2 = p.sm_scale * kLog2e;
+        const float sl2 = p.sm_scale * kLog2e * (is_fp4(kKv) ? kFp4Up : 1.0f);
         // this lane's row of the P matrices it addresses
         const uint32_t p_row = lane & 7, p_key = lane >> 3;
         const uint32_t p_at = 2 * j * kGroupBytes + p_row * 128;
@@ -518,8 +518,9 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         l_a += __shfl_xor_sync(0xffffffffu, l_a, 2);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 1);
         l_b += __shfl_xor_sync(0xffffffffu, l_b, 2);
-        const float inv_a = (ok && l_a > 0.f) ? 1.f / l_a : 0.f;
-        const float inv_b = (ok && l_b > 0.f) ? 1.f / l_b : 0.f;
+        constexpr float kUp = is_fp4(kKv) ? kFp4Up : 1.f;
+        const float inv_a = (ok && l_a > 0.f) ? 1.f / l_a * kUp : 0.f;
+        const float inv_b = (ok && l_b > 0.f) ? 1.f / l_b * kUp : 0.f;
         // the helpers write the second half of the columns
         if (q4 == 0) {
             sm.inv[ha] = inv_a;

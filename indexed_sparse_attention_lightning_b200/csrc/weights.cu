@@ -370,7 +370,7 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
 #pragma unroll
                     for (int c = 0; c < 8; ++c) {
                         uint4 x = *reinterpret_cast<const uint4 *>(qr + ((c ^ (hr & 7)) << 4));
-                        if (is_fp4(kKv) && b < kBlocks - 1) x = fp4_order(x);
+                        if (is_fp4(kKv)) x = b < kBlocks - 1 ? fp4_order(x) : fp4_rope(x);
                         v[4 * c] = x.x;
                         v[4 * c + 1] = x.y;
                         v[4 * c + 2] = x.z;
@@ -384,7 +384,7 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm.q_ready);  // also frees ring stages 1 and 2
         }
-        const float sl2 = p.sm_scale * kLog2e;
+        const float sl2 = p.sm_scale * kLog2e * (is_fp4(kKv) ? kFp4Up : 1.0f);
         // this thread's heads in S: 32j + lane / 4 + 8i; one with nothing selected
         // (lse = -inf) adds nothing
         float minus[4];

@@ -391,6 +391,26 @@ def test_attention_over_mxfp4_scales_of_every_size():
     check_attention(wl, idx, out, lse, "f32")
 
 
+@pytest.mark.parametrize("lo,hi", [(4, 40), (120, 137), (130, 150), (127, 200), (0, 252)])
+def test_mxfp4_scales_beyond_the_usual(lo, hi):
+    """Scales 2^(lo - 127) .. 2^(hi - 128), mixed within rows and between the rows of a
+    tile, with logits of order one: values small, on both sides of the one-product
+    bound, and far past it (6 x 2^124 is the largest, below fp32's 2^128)."""
+    wl = make("mxfp4", (400, 90), heads=128, top_k=200)
+    rng = np.random.default_rng(4)
+    sc = rng.integers(lo, hi, wl.kv_scale.shape).astype(np.uint8)
+    one = rng.random(sc.shape[:2]) < 0.3                     # rows of one small scale
+    sc[one] = max(lo, min(hi - 1, 126))
+    wl = dataclasses.replace(wl, kv_scale=sc)
+    sm = float(np.float32(0.05 * 2.0 ** (127 - max(hi, 120))))
+    wl = dataclasses.replace(wl, spec=dataclasses.replace(wl.spec, sm_scale=sm))
+    idx = selection(wl, 200, 9)
+    cache, queries, idx_t = upload(wl, idx)
+    out, lse = api.sparse_mla_attn(cache, queries, idx_t, 200, out_dtype="f32")
+    check_attention(wl, idx, out, lse, "f32")
+    check_weights(wl, idx, acc=np.zeros((2, 400), np.float32))
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_fused_decode_over_4_bits(fmt):
     """sa_decode selects and attends like the oracle, and like its own steps."""
