@@ -28,7 +28,7 @@
 //
 // Roles (384 threads, 416 for a 4-bit latent; one CTA per SM):
 //   warp 0     lane 0 loads Q by TMA (into the third ring stage; this copy
-//              starts before the wait on the top-K kernel); then the warp
+//              starts before the wait on the top-K kernel); then one lane
 //              issues the MMAs, S of tile n + 1 before P V of tile n, and
 //              commits them to mbarriers;
 //   warps 1-7  copy the selected rows (16-byte cp.async, the swizzle applied
@@ -559,23 +559,26 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
         }
     } else if (T > 0) {
         // ------------------------------------------------- MMA issuer ---
-        // The whole warp waits and computes descriptors, one elected lane issues.
+        // One elected lane waits and issues: with the whole warp waiting and meeting
+        // again around each branch, in a sub-partition that two producers and a
+        // softmax warp keep busy, the steps between the MMAs took 500 of 2700 cycles a
+        // tile (512 queries: 375 us over MXFP4 and 363 over bf16, so 395 and 384).
         // S of the next tile goes out before P V of this one, so that the tensor
         // pipe works while the softmax does; the two then alternate.
         const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
         constexpr uint32_t id_s = instr_desc(64, kTile, 1 /*bf16*/, 0, 0);
         constexpr uint32_t id_pv = instr_desc(64, 256, 1 /*bf16*/, 0, 1);
-        bool ok = warp_wait(&sm.q_ready, 0, abort_flag, status);
-        for (int n = 0; ok && n <= T; ++n) {
-            if (n < T) {  // S(n): its S buffer is free since P V (n - 2) was issued
-                const int st = n % kStages;
-                ok = warp_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
-                if (!ok) break;
-                if constexpr (kKv == SA_BF16) fence_proxy_async_smem();  // cp.async rows
-                tc_fence_after();
-                const uint32_t d = tm + kColS + kTile * (n & 1);
-                const uint32_t stage = smem_u32(sm.kv[st]);
-                if (elect_one()) {
+        if (elect_one()) {
+            bool ok = mbar_wait(&sm.q_ready, 0, abort_flag, status);
+            for (int n = 0; ok && n <= T; ++n) {
+                if (n < T) {  // S(n): its S buffer is free since P V (n - 2) was issued
+                    const int st = n % kStages;
+                    ok = mbar_wait(&sm.kv_full[st], (n / kStages) & 1, abort_flag, status);
+                    if (!ok) break;
+                    if constexpr (kKv == SA_BF16) fence_proxy_async_smem();  // cp.async rows
+                    tc_fence_after();
+                    const uint32_t d = tm + kColS + kTile * (n & 1);
+                    const uint32_t stage = smem_u32(sm.kv[st]);
 #pragma unroll  // 36 MMAs straight-line: measured faster than a loop over the blocks
                     for (int b = 0; b < kBlocks; ++b) {
                         const uint64_t bd = desc_kmajor_sw128_sbo(stage + b * 1024, kGroupBytes);
@@ -586,16 +589,13 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                     }
                     mma_commit(&sm.s_full[n & 1]);
                 }
-                __syncwarp();
-            }
-            if (n > 0) {  // P V (n - 1)
-                const int np = n - 1, st = np % kStages;
-                const uint32_t stage = smem_u32(sm.kv[st]);
-                const uint64_t ad = desc_kmajor_sw128_sbo(stage + kPOffset, kGroupBytes);
-                ok = warp_wait(&sm.p_full[st], (np / kStages) & 1, abort_flag, status);
-                if (!ok) break;
-                tc_fence_after();  // P's writers have fenced for the tensor core
-                if (elect_one()) {
+                if (n > 0) {  // P V (n - 1)
+                    const int np = n - 1, st = np % kStages;
+                    const uint32_t stage = smem_u32(sm.kv[st]);
+                    const uint64_t ad = desc_kmajor_sw128_sbo(stage + kPOffset, kGroupBytes);
+                    ok = mbar_wait(&sm.p_full[st], (np / kStages) & 1, abort_flag, status);
+                    if (!ok) break;
+                    tc_fence_after();  // P's writers have fenced for the tensor core
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
 #pragma unroll
@@ -608,9 +608,9 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
                     }
                     mma_commit(&sm.kv_empty[st]);
                 }
-                __syncwarp();
             }
         }
+        __syncwarp();
         // o_final: every MMA issued above (all P V of the tiles) has completed;
         // after a timeout too, so that TMEM is never released under an MMA
         if (elect_one()) mma_commit(&sm.o_final);

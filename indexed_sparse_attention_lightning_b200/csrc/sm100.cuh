@@ -374,9 +374,9 @@ __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
 
 // One lane of the warp, the same one every time; every lane calls it.
 //
-// MMAs and their commits are issued in an `if (elect_one())` branch of a warp
-// whose lanes all compute the operands: the compiler then keeps descriptors
-// and addresses in uniform registers.  One CTA per SM, M = 128, bf16 K = 16 from
+// MMAs and their commits are issued in an `if (elect_one())` branch of a
+// converged warp (a loop with its waits may lie inside): the compiler then keeps
+// descriptors and addresses in uniform registers.  One CTA per SM, M = 128, bf16 K = 16 from
 // tensor memory, back to back: 32 cycles an MMA at N = 64 and 17 at N = 32, the
 // tensor pipe's own rate; in an `if (lane == 0)` branch any N up to 64 takes 48.
 // (Predicating the instructions on the election instead of branching is not
