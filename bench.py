@@ -696,7 +696,7 @@ def run_ours(args, rank: int, world: int, dist):
     shared = [csrc + f for f in ("common.cuh", "sm100.cuh", "internal.h")]
     kernel_src = {"indexer": [csrc + "indexer_mma.cu", csrc + "plan.cu"] + shared,
                   "topk": [csrc + "topk.cu"] + shared,
-                  "attention": [csrc + "sfa_mma.cu"] + shared}
+                  "attention": [csrc + "sfa_mma.cu", csrc + "sfa_gather.cuh"] + shared}
     traffic = traffic_for(dom_name, kernel_src[dom_name], sp.name)
 
     cpu = None

@@ -26,14 +26,12 @@ constexpr int kChunksPerRow = kD * 2 / 16;  // 72 sixteen-byte pieces of a row
 constexpr uint32_t kGroupBytes = kBlocks * 1024;             // 9216
 constexpr uint32_t kStageBytes = (kTile / 8) * kGroupBytes;  // 73728
 
-// Producer warps of a 4-bit latent, whose rows are decoded: eight next to the
-// attention's softmax, which more of them slow down (512 queries: 420 us with
-// eight, 481 with sixteen), sixteen in the weights kernel (256 queries: 125 us
-// against 137).
-constexpr int kFp4AttnWarps = 8, kFp4WeightsWarps = 16;
-// Warps of a CTA: 0 (Q and MMA), 1-7 (rows), 8-11 (TMEM readers), 12 and up (rows).
-constexpr int cta_threads(int producers) { return 32 * (5 + producers); }
-__device__ __forceinline__ int producer_index(int warp) { return warp < 8 ? warp - 1 : warp - 5; }
+// A 4-bit latent takes one more producer warp, the CTA's last: its rows are
+// decoded, and eight warps of key pairs share a tile evenly.  Sixteen take issue
+// slots from the attention's softmax and MMA warps (512 queries over NVFP4 383 us
+// with eight, 491 with sixteen) and give the weights kernel nothing (119 and 120).
+constexpr int kFp4Warps = 8;
+__device__ __forceinline__ int producer_index(int warp) { return warp < 8 ? warp - 1 : 7; }
 
 // The latent dims of a 4-bit row lie in the stage with each group of eight
 // reordered: place 2i holds dim i, place 2i + 1 dim i + 4 (i < 4), the order in
@@ -137,7 +135,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
     return __all_sync(0xffffffffu, ok) != 0;
 }
 
-// Row producers (kWarps warps: kProducerWarps, or 8 or 16 for 4 bits): tiles
+// Row producers (kProducerWarps or, for 4 bits, kFp4Warps warps): tiles
 // 0 .. T - 1 of tile_rows (physical rows, whole tiles, in global or shared
 // memory) go through the ring.
 // Stage `q_stage` and those behind it hold Q until q_ready completes.
@@ -151,7 +149,7 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 // lane's sixteen bytes of codes and its scales).  Row indices are loaded one
 // iteration before they are used, so no global load latency sits between a
 // freed stage and its copies.
-template <int kKv, int kWarps>
+template <int kKv>
 __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t *tile_rows, int T,
                                              int pw, uint8_t (*stages)[kStageBytes],
                                              uint64_t *kv_full, uint64_t *kv_empty,
@@ -166,26 +164,23 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
         return n != q_stage || warp_wait(q_ready, 0, abort_flag, status);
     };
     if constexpr (is_fp4(kKv)) {
-        // Warp pw takes key pairs pw, pw + kWarps, ... of a tile, each half of the
-        // warp one key; lane c of a half decodes dims 32c .. 32c + 31.  The four
-        // 16-byte pieces of a lane's dims go out in an order that turns with the
-        // 64-dim block, so that each eight lanes of a store, which go together, meet
-        // all banks once.
-        static_assert(kWarps == 8 || kWarps == 16, "whole key pairs, one or two rope pieces");
-        constexpr int kSlots = kTile / 2 / kWarps;
+        // Warp pw takes key pairs pw, pw + 8, pw + 16, pw + 24 of a tile, each half
+        // of the warp one key; lane c of a half decodes dims 32c .. 32c + 31.  The
+        // four 16-byte pieces of a lane's dims go out in an order that turns with
+        // the 64-dim block, so that each eight lanes of a store, which go together,
+        // meet all banks once.
+        constexpr int kSlots = kTile / 2 / kFp4Warps;
         constexpr int kScales = 32 / fp4_group(kKv);  // scale bytes of a lane's dims
-        constexpr int kRopes = 16 / kWarps;           // rope pieces of a lane
         const uint8_t *scales = reinterpret_cast<const uint8_t *>(p.kv_scale);
         const int half = lane >> 4, c = lane & 15;
         const int turn = (c >> 1) & 3, flip = turn >> 1;
-        const int key = 2 * pw + half;  // of slot 0; slot i: key + 2 kWarps i
+        const int key = 2 * pw + half;  // of slot 0; slot i: key + 16 i
         uint2 code[kSlots][2];
         uint32_t sb[kSlots];
         auto load = [&](int32_t lo, int32_t hi, uint2 (*x)[2], uint32_t *s) {
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
-                const int32_t r = __shfl_sync(0xffffffffu, 2 * i < kSlots ? lo : hi,
-                                              (key + 2 * kWarps * i) & 31);
+                const int32_t r = __shfl_sync(0xffffffffu, i < 2 ? lo : hi, (key + 16 * i) & 31);
                 const uint2 *src =
                     reinterpret_cast<const uint2 *>(kv + (int64_t)r * (kDl / 2) + 16 * c);
                 x[i][0] = __ldg(src + flip);
@@ -199,15 +194,14 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             lo = n < T ? tile_rows[n * kTile + lane] : 0;
             hi = n < T ? tile_rows[n * kTile + 32 + lane] : 0;
         };
-        // where this lane's pieces go in slot 0's row; a slot is kWarps / 4 groups on
+        // where this lane's pieces go in slot 0's row; slot i is 2 i groups on
         const int sw = key & 7;
         const uint32_t row_at = (key >> 3) * kGroupBytes + sw * 128;
         uint32_t piece[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
             piece[j] = row_at + (c >> 1) * 1024 + (((4 * (c & 1) + (j ^ turn)) ^ sw) << 4);
-        // rope: 16-byte piece lane % 8 of key 4 pw + lane / 8, with eight warps also 32
-        // keys on
+        // rope: 16-byte piece lane % 8 of keys 4 pw + lane / 8 and 32 more
         const int rk = 4 * pw + (lane >> 3);
         const uint32_t rope_at = (rk >> 3) * kGroupBytes + (kBlocks - 1) * 1024 + (rk & 7) * 128 +
                                  (((lane & 7) ^ (rk & 7)) << 4);
@@ -215,7 +209,7 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             constexpr bool kOnce = decltype(once)::value;
 #pragma unroll
             for (int i = 0; i < kSlots; ++i) {
-                uint8_t *dst = stage + i * (kWarps / 4 * kGroupBytes);
+                uint8_t *dst = stage + i * (2 * kGroupBytes);
                 // scales of the pieces in the order they are decoded
                 uint32_t s0 = sb[i], s1 = sb[i];
                 if (kScales == 2) {
@@ -246,19 +240,16 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
             row_pair(n + 2, lo2, hi2);
             if (n + 1 < T) {
                 load(lo1, hi1, next_code, next_sb);
-                // a 32-byte sector of the next rope rows per thread of eight warps
-                if (kWarps == 8 || pw < 8) {
-                    const int32_t r = __shfl_sync(0xffffffffu, pw < 4 ? lo1 : hi1,
-                                                  (8 * pw + (lane >> 2)) & 31);
-                    prefetch_line_l2(rope + (int64_t)r * (kDr * 2) + (lane & 3) * 32);
-                }
+                // a 32-byte sector of a rope row per thread
+                const int32_t r = __shfl_sync(0xffffffffu, pw < 4 ? lo1 : hi1,
+                                              (8 * pw + (lane >> 2)) & 31);
+                prefetch_line_l2(rope + (int64_t)r * (kDr * 2) + (lane & 3) * 32);
             }
             // this tile's rope pieces: in L2 since the last tile, used after the codes
-            uint4 rope_piece[kRopes];
+            uint4 rope_piece[2];
 #pragma unroll
-            for (int i = 0; i < kRopes; ++i) {
-                const int32_t r =
-                    __shfl_sync(0xffffffffu, (kRopes == 1 ? pw < 8 : i == 0) ? lo : hi, rk & 31);
+            for (int i = 0; i < 2; ++i) {
+                const int32_t r = __shfl_sync(0xffffffffu, i == 0 ? lo : hi, rk);
                 rope_piece[i] = __ldg(
                     reinterpret_cast<const uint4 *>(rope + (int64_t)r * (kDr * 2)) + (lane & 7));
             }
@@ -274,7 +265,7 @@ __device__ __forceinline__ void produce_rows(const PathParams &p, const int32_t 
                 else decode(std::false_type(), stage);
             }
 #pragma unroll
-            for (int i = 0; i < kRopes; ++i)
+            for (int i = 0; i < 2; ++i)
                 *reinterpret_cast<uint4 *>(stage + rope_at + i * 4 * kGroupBytes) = rope_piece[i];
             fence_proxy_async_smem();
             mbar_arrive(&kv_full[st]);

@@ -140,7 +140,9 @@ struct SfaArgs {
 };
 
 template <int kKv>
-constexpr int kProducers = is_fp4(kKv) ? kFp4AttnWarps : kProducerWarps;
+constexpr int kProducers = is_fp4(kKv) ? kFp4Warps : kProducerWarps;
+template <int kKv>
+constexpr int kCtaThreads = 32 * (5 + kProducers<kKv>);
 
 // Columns [256 half, 256 half + 256) of O / l of heads 16j .. 16j + 15 (warp 8 +
 // j, and 4 + j for the second half; both see TMEM lanes 32j and up), 128 columns
@@ -239,7 +241,7 @@ __device__ __forceinline__ void write_output(SfaSmem &sm, const SfaArgs &a, int 
 }
 
 template <int kKv>  // sa_dtype of the latent cache
-__global__ void __launch_bounds__(cta_threads(kProducers<kKv>), 1)
+__global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
 sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     extern __shared__ uint8_t smem_raw[];
     SfaSmem &sm = *reinterpret_cast<SfaSmem *>(align1024(smem_raw));
@@ -547,9 +549,8 @@ sfa_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const SfaArgs a) {
     } else if (warp >= 1) {
         // ---------------------------------------------- row producers ---
         // ring stage 2 holds Q until the softmax warps have moved it to TMEM
-        produce_rows<kKv, kProducers<kKv>>(p, rows + j0 * kTile, T, producer_index(warp), sm.kv,
-                                           sm.kv_full, sm.kv_empty, &sm.q_ready, 2, abort_flag,
-                                           status);
+        produce_rows<kKv>(p, rows + j0 * kTile, T, producer_index(warp), sm.kv, sm.kv_full,
+                          sm.kv_empty, &sm.q_ready, 2, abort_flag, status);
         if (warp >= 4 && warp < 8) {  // their rows done, they help with the output
             const bool done = T > 0 && warp_wait(&sm.o_final, 0, abort_flag, status);
             tc_fence_after();
@@ -737,8 +738,7 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                                                  : sfa_mma_kernel<SA_NVFP4>;
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    const int threads =
-        cta_threads(is_fp4(p.kv_dtype) ? kProducers<SA_MXFP4> : kProducers<SA_BF16>);
+    const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
     const int64_t grid = 2 * (int64_t)p.n_q * splits;
     count_launch();
     e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(threads), smem, s, tq, a);

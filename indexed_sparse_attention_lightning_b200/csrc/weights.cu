@@ -153,9 +153,9 @@ cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t l
 //               queries, two CTAs after one another, 128 and 126.5);
 //   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2), then
 //               the warp issues the MMAs;
-//   warps 1-7   gather the rows (sfa_gather.cuh; with warps 12-20 for a 4-bit
-//               latent); those of the query's first CTA then note where each range
-//               of positions starts, for the sum kernel;
+//   warps 1-7   gather the rows (sfa_gather.cuh; with warp 12 for a 4-bit latent);
+//               those of the query's first CTA then note where each range of
+//               positions starts, for the sum kernel;
 //   warps 8-11  move Q into TMEM (warp 8 + j: heads 32j .. 32j + 31, one per
 //               lane), then read S with 16-lane loads, so that a thread holds
 //               four heads of sixteen keys: exp2 of the logits minus the heads'
@@ -294,10 +294,12 @@ __device__ __forceinline__ void produce_e4m3_pairs(const PathParams &p, const in
 }
 
 template <int kKv>
-constexpr int kProducers = is_fp4(kKv) ? kFp4WeightsWarps : kProducerWarps;
+constexpr int kProducers = is_fp4(kKv) ? kFp4Warps : kProducerWarps;
+template <int kKv>
+constexpr int kCtaThreads = 32 * (5 + kProducers<kKv>);
 
 template <int kKv>  // sa_dtype of the latent cache
-__global__ void __launch_bounds__(cta_threads(kProducers<kKv>), 1)
+__global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
 weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
                    const int32_t *__restrict__ idx, int32_t K, int32_t splits,
                    const float *__restrict__ lse, int32_t ld, int32_t ld_starts,
@@ -451,9 +453,8 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
         if constexpr (kKv == SA_E4M3)
             produce_e4m3_pairs(p, tile_rows, T, warp - 1, sm, abort_flag, status);
         else
-            produce_rows<kKv, kProducers<kKv>>(p, tile_rows, T, producer_index(warp), sm.kv,
-                                               sm.kv_full, sm.kv_empty, &sm.q_ready, 1,
-                                               abort_flag, status);
+            produce_rows<kKv>(p, tile_rows, T, producer_index(warp), sm.kv, sm.kv_full,
+                              sm.kv_empty, &sm.q_ready, 1, abort_flag, status);
         if (split == 0) {
             const int32_t thread = 32 * producer_index(warp) + lane;
             write_starts(pos, n_valid, starts, ld_starts, range_log2, thread,
@@ -529,8 +530,7 @@ cudaError_t launch_weights_mma(const PathParams &p, const int32_t *idx, int32_t 
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     const int32_t splits = weights_splits(p.n_q, top_k, p.kv_dtype);
-    const int threads =
-        cta_threads(is_fp4(p.kv_dtype) ? kProducers<SA_MXFP4> : kProducers<SA_BF16>);
+    const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
     count_launch();
     return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(threads), smem,
                       s, tq, p, idx, top_k, splits, lse, ld, ld_starts, range_log2, rows, kept,
