@@ -366,6 +366,23 @@ def test_attention_over_4_bits_with_other_softmax_scales(fmt, sm_scale):
     check_attention(wl, idx, out, lse, "f32")
 
 
+@pytest.mark.parametrize("fmt", ["mxfp4", "bf16", "e4m3"])
+def test_attention_with_many_queries_into_fp32(fmt):
+    """No key splits, fp32 output at a 16-byte boundary that is no 32-byte one."""
+    wl = make(fmt, (400,), heads=128, queries=("prefill", 300, 100), top_k=130)
+    idx = selection(wl, 130, 8)
+    cache, queries, idx_t = upload(wl, idx)
+    flat = torch.full((100 * 128 * 512 + 8,), 7.0, device="cuda")
+    out = flat[4:-4].view(100, 128, 512)
+    assert out.data_ptr() % 32 == 16
+    got, lse = api.sparse_mla_attn(cache, queries, idx_t, 130, out=out, out_dtype="f32")
+    assert torch.all(flat[:4] == 7) and torch.all(flat[-4:] == 7)
+    half, _ = api.sparse_mla_attn(cache, queries, idx_t, 130)
+    assert torch.equal(half, got.to(torch.bfloat16))
+    if fmt != "e4m3":        # its rows are rounded to bf16 before the product
+        check_attention(wl, idx, got, lse, "f32")
+
+
 @pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
 def test_attention_over_4_bits_with_many_queries(fmt):
     """More (query, half) pairs than SMs: no key splits."""
@@ -502,6 +519,14 @@ def test_weights_of_more_queries_than_sms(kv):
     wl = make(kv, (400,), heads=128, queries=("prefill", 240, 160))
     for K in (1, 64, 193):
         check_weights(wl, selection(wl, K, 6, order="shuffled" if K == 64 else "ascending"))
+
+
+@pytest.mark.parametrize("heads", [128, 16])
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4", "e4m3"])
+def test_weights_of_long_selections(kv, heads):
+    """More entries than a CTA's threads look up in one step."""
+    wl = make(kv, (5300, 700), heads=heads)
+    check_weights(wl, selection(wl, 5000, 6, holes=True))
 
 
 @pytest.mark.parametrize("heads,dl,dr", [(1, 64, 16), (7, 96, 8), (20, 512, 64), (130, 32, 0)])
