@@ -125,7 +125,8 @@ class DeviceCache:
         # in the order of the struct's fields: by keyword the construction takes twice as long
         batch, max_pages = self.page_table.shape
         return SaCache(
-            _ptr(self.page_table), _ptr(self.seq_len), batch, max_pages, self.num_pages, self.page_size,
+            _ptr(self.page_table), _ptr(self.seq_len), batch, max_pages, self.num_pages,
+            self.page_size,
             _abi.DTYPES[self.index_dtype], _ptr(self.k_index), _ptr(self.k_index_scale),
             self.d_index, _abi.DTYPES[self.kv_dtype], _ptr(self.kv), _ptr(self.kv_rope),
             _ptr(self.kv_scale), self.d_latent, self.d_rope, int(self.kv_scale_tile[0]),
