@@ -7,6 +7,8 @@ every step of the path in its own CUDA kernels.  Nothing here computes.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 from dataclasses import dataclass
 from typing import Optional
 
@@ -86,6 +88,30 @@ def _need_here(where: str, *tensors) -> None:
         if t is not None and t.get_device() != here:
             raise SaError(_abi.SA_ERR_INVALID_ARG, f"{where}: a tensor is on {t.device}, the "
                                                    f"current device is cuda:{here}")
+
+
+def _on_stream(f):
+    """An entry point's ``stream`` is the current stream while it runs: the buffers
+    that the binding makes itself are allocated and filled there, and a workspace
+    dropped on return goes back to that stream, behind the kernels that use it.
+    What it returns may be used on the caller's stream, which the allocator is told."""
+    at = list(inspect.signature(f).parameters).index("stream")
+
+    @functools.wraps(f)
+    def call(*args, **kwargs):
+        stream = args[at] if len(args) > at else kwargs.get("stream")
+        if stream is None:
+            return f(*args, **kwargs)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            made = f(*args, **kwargs)
+        if caller != stream:
+            for t in made if isinstance(made, tuple) else (made,):
+                if t is not None:
+                    t.record_stream(caller)
+        return made
+
+    return call
 
 
 def _stream(stream) -> int:
@@ -244,6 +270,7 @@ def device_status(ws: torch.Tensor, stream=None) -> tuple[int, int]:
 
 # -------------------------------------------------------------- entry points ---
 
+@_on_stream
 def indexer_score(cache: DeviceCache, queries: DeviceQueries, scores=None, ws=None,
                   stream=None) -> torch.Tensor:
     dev = queries.q_seq.device
@@ -261,6 +288,7 @@ def indexer_score(cache: DeviceCache, queries: DeviceQueries, scores=None, ws=No
     return scores
 
 
+@_on_stream
 def topk(scores: torch.Tensor, valid_len: torch.Tensor, top_k: int, max_valid: int,
          idx=None, ws=None, stream=None) -> torch.Tensor:
     n_q = scores.shape[0]
@@ -290,6 +318,7 @@ def _outputs(queries: DeviceQueries, d_latent: int, out, lse, out_dtype: str):
     return out, lse
 
 
+@_on_stream
 def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                     out=None, lse=None, out_dtype: str = "bf16", ws=None, stream=None):
     out, lse = _outputs(queries, cache.d_latent, out, lse, out_dtype)
@@ -306,6 +335,7 @@ def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tenso
     return out, lse
 
 
+@_on_stream
 def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse=None,
            idx=None, out_dtype: str = "bf16", ws=None, stream=None, phase_events=None):
     """Fused indexer -> top-K -> sparse attention.  Returns (out, lse, idx-or-None).
@@ -336,6 +366,7 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
 
 # -------------------------------------------- context-parallel decode steps ---
 
+@_on_stream
 def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
                      offset: torch.Tensor, score=None, pos=None, ws=None, stream=None):
     """This GPU's top_k of its context shard as (score fp32, position + offset
@@ -360,6 +391,7 @@ def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
     return score, pos, ws
 
 
+@_on_stream
 def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: torch.Tensor,
                      hi: torch.Tensor, idx_global=None, idx_local=None, stream=None):
     """All ranks' candidates [n_ranks, n_q, top_k] -> (global top-K positions,
@@ -384,6 +416,7 @@ def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: tor
     return idx_global, idx_local
 
 
+@_on_stream
 def combine_partials(o_part: torch.Tensor, lse_part: torch.Tensor, out=None, lse=None,
                      out_dtype: str = "bf16", stream=None):
     """Partial outputs [n_parts, n_q, heads, d] (fp32) with their lse [n_parts,
@@ -416,6 +449,7 @@ def _in_dtype(t: torch.Tensor) -> int:
     return _abi.DTYPES[_IN_DTYPES[t.dtype]]
 
 
+@_on_stream
 def quantize_index_query(q: torch.Tensor, out=None, scale=None, stream=None):
     """Indexer query [n_q, h_index, d_index] (bfloat16 or float32) -> (e4m3 codes
     uint8 [n_q, h_index, d_index], fp32 scales [n_q, h_index])."""
@@ -433,6 +467,7 @@ def quantize_index_query(q: torch.Tensor, out=None, scale=None, stream=None):
     return out, scale
 
 
+@_on_stream
 def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
                   k_index: Optional[torch.Tensor] = None, kv: Optional[torch.Tensor] = None,
                   ws=None, stream=None) -> torch.Tensor:
@@ -466,6 +501,7 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
     return ws
 
 
+@_on_stream
 def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=None,
                 out_dtype: str = "bf16", ws=None, stream=None):
     """Latent + rope rows of tokens (sequence, position) as the values the pool
@@ -492,6 +528,7 @@ def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=No
 
 # -------------------------------------- shrinking a cache by its attention ---
 
+@_on_stream
 def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                        lse: torch.Tensor, acc: Optional[torch.Tensor], decay: float = 1.0,
                        out=None, ws=None, stream=None) -> torch.Tensor:
@@ -522,6 +559,7 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
     return out
 
 
+@_on_stream
 def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: DeviceCache,
                  keep_first: int = 0, keep_last: int = 0, acc_out=None, src_pos=None, ws=None,
                  stream=None) -> torch.Tensor:
