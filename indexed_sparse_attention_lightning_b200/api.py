@@ -94,7 +94,8 @@ def _on_stream(f):
     """An entry point's ``stream`` is the current stream while it runs: the buffers
     that the binding makes itself are allocated and filled there, and a workspace
     dropped on return goes back to that stream, behind the kernels that use it.
-    What it returns may be used on the caller's stream, which the allocator is told."""
+    Results that it made may be used on the caller's stream, which the allocator is
+    told."""
     at = list(inspect.signature(f).parameters).index("stream")
 
     @functools.wraps(f)
@@ -106,8 +107,9 @@ def _on_stream(f):
         with torch.cuda.stream(stream):
             made = f(*args, **kwargs)
         if caller != stream:
+            given = {id(a) for a in args} | {id(a) for a in kwargs.values()}
             for t in made if isinstance(made, tuple) else (made,):
-                if t is not None:
+                if t is not None and id(t) not in given:
                     t.record_stream(caller)
         return made
 

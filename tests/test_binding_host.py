@@ -104,6 +104,14 @@ def test_buffers_belong_to_the_stream_of_the_call(name, monkeypatch):
     for t in got if isinstance(got, tuple) else (got,):
         if isinstance(t, Made):
             assert t.recorded == [MAIN]
+    if isinstance(got, Made):                           # the caller's own are the caller's
+        own = got.clone()
+        own.recorded = []
+        out = {"indexer_score": "scores", "topk": "idx", "accumulate_weights": "out",
+               "evict_tokens": "src_pos", "append_tokens": "ws"}[name]
+        assert getattr(api, name)(*args, **{out: own}, stream=SIDE) is own
+        assert own.recorded == []
+        world.launched.pop()
 
     world.made.clear()
     got = getattr(api, name)(*args)                     # on the current stream: nothing to tell
