@@ -3,6 +3,9 @@
 Argument marshalling only: torch tensors (device memory, streams) are turned
 into the C structs of ``include/sa.h`` and passed to the library, which runs
 every step of the path in its own CUDA kernels.  Nothing here computes.
+
+A call runs on the device of its tensors, which must all be on one, and on
+``stream`` (a torch.cuda.Stream of that device) or that device's current one.
 """
 from __future__ import annotations
 
@@ -82,34 +85,47 @@ def _need_sums(t, name: str, batch: int, min_cols: int) -> int:
 
 
 def _need_here(where: str, *tensors) -> None:
-    """The kernels run on the current device: refuse tensors of another one."""
+    """The kernels run on the current device, which is that of the entry point's
+    first argument (see _entry): refuse tensors of another one."""
     here = torch._C._cuda_getDevice()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise SaError(_abi.SA_ERR_INVALID_ARG, f"{where}: a tensor is on {t.device}, the "
-                                                   f"current device is cuda:{here}")
+                                                   f"call runs on cuda:{here}")
 
 
-def _on_stream(f):
-    """An entry point's ``stream`` is the current stream while it runs: the buffers
-    that the binding makes itself are allocated and filled there, and a workspace
-    dropped on return goes back to that stream, behind the kernels that use it.
-    Results that it made may be used on the caller's stream, which the allocator is
-    told."""
-    at = list(inspect.signature(f).parameters).index("stream")
+def _entry(f):
+    """An entry point runs on the device of its first argument, whichever is
+    current, and on its ``stream``, or that device's current one.  Both are made
+    current while it runs, so the buffers that the binding makes itself are allocated
+    and filled there, and a workspace dropped on return goes back to that stream,
+    behind the kernels that use it.  Results that it made may be used on the
+    caller's stream, which the allocator is told."""
+    names = list(inspect.signature(f).parameters)
+    at = names.index("stream")
 
     @functools.wraps(f)
     def call(*args, **kwargs):
+        first = args[0] if args else kwargs.get(names[0])
+        if isinstance(first, DeviceCache):
+            first = first.page_table
+        device = first.get_device() if isinstance(first, torch.Tensor) else -1
         stream = args[at] if len(args) > at else kwargs.get("stream")
         if stream is None:
-            return f(*args, **kwargs)
+            if device < 0 or device == torch._C._cuda_getDevice():
+                return f(*args, **kwargs)
+            with torch.cuda.device(device):
+                return f(*args, **kwargs)
+        if stream.device.index != device >= 0:
+            raise SaError(_abi.SA_ERR_INVALID_ARG, f"{f.__name__}: the stream is on "
+                                                   f"{stream.device}, the tensors on cuda:{device}")
         caller = torch.cuda.current_stream(stream.device)
         with torch.cuda.stream(stream):
             made = f(*args, **kwargs)
         if caller != stream:
             given = {id(a) for a in args} | {id(a) for a in kwargs.values()}
             for t in made if isinstance(made, tuple) else (made,):
-                if t is not None and id(t) not in given:
+                if isinstance(t, torch.Tensor) and id(t) not in given:
                     t.record_stream(caller)
         return made
 
@@ -263,6 +279,7 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
+@_entry
 def device_status(ws: torch.Tensor, stream=None) -> tuple[int, int]:
     """(status, detail) of the last call that used `ws`; synchronises the stream."""
     detail = ctypes.c_int32(0)
@@ -272,7 +289,7 @@ def device_status(ws: torch.Tensor, stream=None) -> tuple[int, int]:
 
 # -------------------------------------------------------------- entry points ---
 
-@_on_stream
+@_entry
 def indexer_score(cache: DeviceCache, queries: DeviceQueries, scores=None, ws=None,
                   stream=None) -> torch.Tensor:
     dev = queries.q_seq.device
@@ -284,13 +301,14 @@ def indexer_score(cache: DeviceCache, queries: DeviceQueries, scores=None, ws=No
     _need_rows(scores, "scores", queries.n_q, queries.max_visible)
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
+    _need_here("indexer_score", cache.k_index, queries.q_index, scores, ws)
     check(_abi.lib().sa_indexer_score(ctypes.byref(c), ctypes.byref(q), _ptr(scores),
                                       scores.stride(0), _ptr(ws), ws.numel(), _stream(stream)),
           "sa_indexer_score")
     return scores
 
 
-@_on_stream
+@_entry
 def topk(scores: torch.Tensor, valid_len: torch.Tensor, top_k: int, max_valid: int,
          idx=None, ws=None, stream=None) -> torch.Tensor:
     n_q = scores.shape[0]
@@ -302,6 +320,7 @@ def topk(scores: torch.Tensor, valid_len: torch.Tensor, top_k: int, max_valid: i
     _need(valid_len, "valid_len", torch.int32, (n_q,))
     _need(idx, "idx", torch.int32, (n_q, top_k))
     _need(ws, "ws")
+    _need_here("topk", valid_len, idx, ws)
     check(_abi.lib().sa_topk(_ptr(scores), scores.stride(0), _ptr(valid_len), n_q, max_valid,
                              top_k, _ptr(idx), _ptr(ws), ws.numel(), _stream(stream)),
           "sa_topk")
@@ -320,7 +339,7 @@ def _outputs(queries: DeviceQueries, d_latent: int, out, lse, out_dtype: str):
     return out, lse
 
 
-@_on_stream
+@_entry
 def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                     out=None, lse=None, out_dtype: str = "bf16", ws=None, stream=None):
     out, lse = _outputs(queries, cache.d_latent, out, lse, out_dtype)
@@ -328,8 +347,8 @@ def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tenso
         ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_ATTN), idx.device)
     _need(idx, "idx", torch.int32, (queries.n_q, top_k))
     _need(ws, "ws")
-    _need_here("sparse_mla_attn", cache.kv, queries.q, idx, out, lse, ws)
     c, q = cache.struct(), queries.struct()
+    _need_here("sparse_mla_attn", cache.kv, queries.q, idx, out, lse, ws)
     check(_abi.lib().sa_sparse_mla_attn(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
                                         _ptr(out), _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws),
                                         ws.numel(), _stream(stream)),
@@ -337,7 +356,7 @@ def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tenso
     return out, lse
 
 
-@_on_stream
+@_entry
 def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse=None,
            idx=None, out_dtype: str = "bf16", ws=None, stream=None, phase_events=None):
     """Fused indexer -> top-K -> sparse attention.  Returns (out, lse, idx-or-None).
@@ -351,6 +370,7 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
     _need(idx, "idx", torch.int32, (queries.n_q, top_k), optional=True)
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
+    _need_here("decode", cache.kv, queries.q, out, lse, idx, ws)
     args = (ctypes.byref(c), ctypes.byref(q), top_k, _ptr(idx), _ptr(out),
             _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
     if phase_events is None:
@@ -368,7 +388,7 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
 
 # -------------------------------------------- context-parallel decode steps ---
 
-@_on_stream
+@_entry
 def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
                      offset: torch.Tensor, score=None, pos=None, ws=None, stream=None):
     """This GPU's top_k of its context shard as (score fp32, position + offset
@@ -386,6 +406,7 @@ def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
     _need(pos, "pos", torch.int32, (n_q, top_k))
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
+    _need_here("local_candidates", cache.kv, queries.q, offset, score, pos, ws)
     check(_abi.lib().sa_local_candidates(ctypes.byref(c), ctypes.byref(q), top_k, _ptr(offset),
                                          _ptr(score), _ptr(pos), _ptr(ws), ws.numel(),
                                          _stream(stream)),
@@ -393,7 +414,7 @@ def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
     return score, pos, ws
 
 
-@_on_stream
+@_entry
 def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: torch.Tensor,
                      hi: torch.Tensor, idx_global=None, idx_local=None, stream=None):
     """All ranks' candidates [n_ranks, n_q, top_k] -> (global top-K positions,
@@ -411,6 +432,7 @@ def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: tor
         idx_local = torch.empty((n_q, top_k), dtype=torch.int32, device=score.device)
     _need(idx_global, "idx_global", torch.int32, (n_q, top_k))
     _need(idx_local, "idx_local", torch.int32, (n_q, top_k))
+    _need_here("merge_candidates", pos, lo, hi, idx_global, idx_local)
     check(_abi.lib().sa_merge_candidates(_ptr(score), _ptr(pos), n_ranks, n_q, top_k, _ptr(lo),
                                          _ptr(hi), _ptr(idx_global), _ptr(idx_local),
                                          _stream(stream)),
@@ -418,7 +440,7 @@ def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: tor
     return idx_global, idx_local
 
 
-@_on_stream
+@_entry
 def combine_partials(o_part: torch.Tensor, lse_part: torch.Tensor, out=None, lse=None,
                      out_dtype: str = "bf16", stream=None):
     """Partial outputs [n_parts, n_q, heads, d] (fp32) with their lse [n_parts,
@@ -433,6 +455,7 @@ def combine_partials(o_part: torch.Tensor, lse_part: torch.Tensor, out=None, lse
         lse = torch.empty((n_q, heads), dtype=torch.float32, device=o_part.device)
     _need(out, "out", dt, (n_q, heads, d))
     _need(lse, "lse", torch.float32, (n_q, heads))
+    _need_here("combine_partials", lse_part, out, lse)
     check(_abi.lib().sa_combine_partials(_ptr(o_part), _ptr(lse_part), n_parts, n_q, heads, d,
                                          _ptr(out), _abi.DTYPES[out_dtype], _ptr(lse),
                                          _stream(stream)),
@@ -451,7 +474,7 @@ def _in_dtype(t: torch.Tensor) -> int:
     return _abi.DTYPES[_IN_DTYPES[t.dtype]]
 
 
-@_on_stream
+@_entry
 def quantize_index_query(q: torch.Tensor, out=None, scale=None, stream=None):
     """Indexer query [n_q, h_index, d_index] (bfloat16 or float32) -> (e4m3 codes
     uint8 [n_q, h_index, d_index], fp32 scales [n_q, h_index])."""
@@ -463,13 +486,14 @@ def quantize_index_query(q: torch.Tensor, out=None, scale=None, stream=None):
         scale = torch.empty((n_q, h), dtype=torch.float32, device=q.device)
     _need(out, "out", torch.uint8, (n_q, h, d))
     _need(scale, "scale", torch.float32, (n_q, h))
+    _need_here("quantize_index_query", out, scale)
     check(_abi.lib().sa_quantize_index_query(_ptr(q), _in_dtype(q), n_q, h, d, _ptr(out),
                                              _ptr(scale), _stream(stream)),
           "sa_quantize_index_query")
     return out, scale
 
 
-@_on_stream
+@_entry
 def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
                   k_index: Optional[torch.Tensor] = None, kv: Optional[torch.Tensor] = None,
                   ws=None, stream=None) -> torch.Tensor:
@@ -503,7 +527,7 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
     return ws
 
 
-@_on_stream
+@_entry
 def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=None,
                 out_dtype: str = "bf16", ws=None, stream=None):
     """Latent + rope rows of tokens (sequence, position) as the values the pool
@@ -530,7 +554,7 @@ def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=No
 
 # -------------------------------------- shrinking a cache by its attention ---
 
-@_on_stream
+@_entry
 def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                        lse: torch.Tensor, acc: Optional[torch.Tensor], decay: float = 1.0,
                        out=None, ws=None, stream=None) -> torch.Tensor:
@@ -552,8 +576,8 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
     if ws is None:
         ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_WEIGHTS), idx.device)
     _need(ws, "ws")
-    _need_here("accumulate_weights", cache.kv, queries.q, idx, lse, acc, out, ws)
     c, q = cache.struct(), queries.struct()
+    _need_here("accumulate_weights", cache.kv, queries.q, idx, lse, acc, out, ws)
     check(_abi.lib().sa_accumulate_weights(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
                                            _ptr(lse), _ptr(acc), decay, _ptr(out), ld, _ptr(ws),
                                            ws.numel(), _stream(stream)),
@@ -561,7 +585,7 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
     return out
 
 
-@_on_stream
+@_entry
 def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: DeviceCache,
                  keep_first: int = 0, keep_last: int = 0, acc_out=None, src_pos=None, ws=None,
                  stream=None) -> torch.Tensor:
@@ -581,8 +605,8 @@ def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: Device
     if ws is None:
         ws = workspace(workspace_size(cache, None, budget, _abi.SA_WS_EVICT), acc.device)
     _need(ws, "ws")
-    _need_here("evict_tokens", cache.kv, dst.kv, dst.seq_len, acc, acc_out, src_pos, ws)
     c, d = cache.struct(), dst.struct()
+    _need_here("evict_tokens", cache.kv, dst.kv, dst.seq_len, acc, acc_out, src_pos, ws)
     check(_abi.lib().sa_evict_tokens(
         ctypes.byref(c), _ptr(acc), ld, budget, keep_first, keep_last, ctypes.byref(d),
         _ptr(acc_out), ld_out, _ptr(src_pos), _ptr(ws), ws.numel(), _stream(stream)),

@@ -1,5 +1,6 @@
 """The Python binding's own part, with the library and CUDA replaced by
-stand-ins: which stream its buffers are made on (no GPU)."""
+stand-ins: which stream its buffers are made on, which device a call runs on
+(no GPU)."""
 import types
 
 import pytest
@@ -7,87 +8,117 @@ import torch
 
 from indexed_sparse_attention_lightning_b200 import _abi, api
 
-MAIN, SIDE = (types.SimpleNamespace(cuda_stream=h, device="cpu") for h in (1, 2))
+MAIN, SIDE, FAR = (types.SimpleNamespace(cuda_stream=h, device=torch.device("cuda", d))
+                   for h, d in ((1, 0), (2, 0), (3, 1)))
 
 
-class Made(torch.Tensor):
-    """A tensor that the binding allocated; remembers record_stream()."""
+class Placed(torch.Tensor):
+    """A tensor that says which GPU it is on."""
+
+    def get_device(self):
+        return self.on
+
+
+def placed(t, device=0):
+    t = t.as_subclass(Placed)
+    t.on = device
+    return t
+
+
+class Made(Placed):
+    """One that the binding allocated; remembers record_stream()."""
 
     def record_stream(self, stream):
         self.__dict__.setdefault("recorded", []).append(stream)
 
 
 class World:
-    """The current stream, the tensors made and the streams launched on."""
+    """The current device and stream, the tensors made, and the streams and devices
+    launched on."""
 
     def __init__(self, monkeypatch):
-        self.current, self.made, self.launched = MAIN, [], []
+        self.device, self.current, self.made, self.launched, self.ran_on = 0, MAIN, [], [], []
         world = self
 
         class On:
-            def __init__(self, stream):
-                self.stream = stream
+            def __init__(self, where):
+                self.at = (where, world.current) if isinstance(where, int) else \
+                    (where.device.index, where)
 
             def __enter__(self):
-                self.before, world.current = world.current, self.stream
+                self.before = world.device, world.current
+                world.device, world.current = self.at
 
             def __exit__(self, *exc):
-                world.current = self.before
+                world.device, world.current = self.before
 
         class Lib:
             def __getattr__(self, name):
                 def call(*args):
                     if name == "sa_workspace_size":
                         return 4096
+                    if name == "sa_status_string":
+                        return b""
                     world.launched.append(next(a for a in reversed(args) if isinstance(a, int)))
+                    world.ran_on.append(world.device)
                     return _abi.SA_OK
                 return call
 
         def making(f):
             def make(*args, **kwargs):
                 t = f(*args, **kwargs).as_subclass(Made)
+                t.on = world.device
                 world.made.append((t, world.current))
                 return t
             return make
 
         lib = Lib()
         monkeypatch.setattr(torch.cuda, "stream", On)
+        monkeypatch.setattr(torch.cuda, "device", On)
+        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: world.device, raising=False)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: world.current)
         monkeypatch.setattr(_abi, "lib", lambda: lib)
         monkeypatch.setattr(api, "_need", lambda *a, **k: None)
         monkeypatch.setattr(api, "_need_rows", lambda *a, **k: None)
-        monkeypatch.setattr(api, "_need_here", lambda *a, **k: None)
         monkeypatch.setattr(api, "_stream", lambda s: (s or world.current).cuda_stream)
         for name in ("empty", "zeros", "full"):
             monkeypatch.setattr(torch, name, making(getattr(torch, name)))
 
 
-def given():
-    """Inputs of every entry point, made before the stand-ins."""
-    i32 = dict(dtype=torch.int32)
+def given(on=0):
+    """Inputs of every entry point on GPU `on`, made before the stand-ins."""
+    def zeros(*shape, dtype=torch.int32):
+        return placed(torch.zeros(shape, dtype=dtype), on)
+
+    f32 = dict(dtype=torch.float32)
     cache = api.DeviceCache(
-        page_table=torch.zeros((2, 4), **i32), seq_len=torch.zeros(2, **i32), num_pages=8,
-        index_dtype="e4m3", k_index=torch.zeros(1), k_index_scale=torch.zeros(1),
-        kv_dtype="bf16", kv=torch.zeros(1), kv_rope=None, kv_scale=None, d_index=128,
-        d_latent=512, d_rope=64)
+        page_table=zeros(2, 4), seq_len=zeros(2), num_pages=8, index_dtype="e4m3",
+        k_index=zeros(1), k_index_scale=zeros(1), kv_dtype="bf16", kv=zeros(1), kv_rope=None,
+        kv_scale=None, d_index=128, d_latent=512, d_rope=64)
     queries = api.DeviceQueries(
-        q_seq=torch.zeros(2, **i32), q_pos=torch.zeros(2, **i32), max_visible=200,
-        q_index=torch.zeros(1), q_index_scale=torch.zeros(1), w=torch.zeros(1), h_index=64,
-        q_dtype="bf16", q=torch.zeros(1), heads=128, sm_scale=0.04)
-    idx, lse, sums = torch.zeros((2, 8), **i32), torch.zeros((2, 128)), torch.zeros((2, 256))
-    n = torch.zeros(2, **i32)
-    score = torch.zeros((3, 2, 8))
+        q_seq=zeros(2), q_pos=zeros(2), max_visible=200, q_index=zeros(1),
+        q_index_scale=zeros(1), w=zeros(1), h_index=64, q_dtype="bf16", q=zeros(1), heads=128,
+        sm_scale=0.04)
+    idx, lse, sums, n = zeros(2, 8), zeros(2, 128, **f32), zeros(2, 256, **f32), zeros(2)
+    score = zeros(3, 2, 8, **f32)
     return {
         "indexer_score": (cache, queries), "topk": (lse, n, 8, 128),
         "sparse_mla_attn": (cache, queries, idx, 8), "decode": (cache, queries, 8),
         "local_candidates": (cache, queries, 8, n),
-        "merge_candidates": (score, score.int(), 8, n, n),
-        "combine_partials": (torch.zeros((3, 2, 4, 16)), torch.zeros((3, 2, 4))),
-        "quantize_index_query": (torch.zeros((2, 64, 128)),), "append_tokens": (cache, n, n),
+        "merge_candidates": (score, zeros(3, 2, 8), 8, n, n),
+        "combine_partials": (zeros(3, 2, 4, 16, **f32), zeros(3, 2, 4, **f32)),
+        "quantize_index_query": (zeros(2, 64, 128, **f32),), "append_tokens": (cache, n, n),
         "read_tokens": (cache, n, n),
         "accumulate_weights": (cache, queries, idx, 8, lse, None),
         "evict_tokens": (cache, sums, 64, cache),
     }
+
+
+# a tensor that each takes besides its first arguments
+EXTRA = {"indexer_score": "scores", "topk": "idx", "sparse_mla_attn": "out", "decode": "ws",
+         "local_candidates": "pos", "merge_candidates": "idx_local", "combine_partials": "lse",
+         "quantize_index_query": "scale", "append_tokens": "ws", "read_tokens": "out",
+         "accumulate_weights": "out", "evict_tokens": "src_pos"}
 
 
 @pytest.mark.parametrize("name", sorted(given()))
@@ -106,10 +137,8 @@ def test_buffers_belong_to_the_stream_of_the_call(name, monkeypatch):
             assert t.recorded == [MAIN]
     if isinstance(got, Made):                           # the caller's own are the caller's
         own = got.clone()
-        own.recorded = []
-        out = {"indexer_score": "scores", "topk": "idx", "accumulate_weights": "out",
-               "evict_tokens": "src_pos", "append_tokens": "ws"}[name]
-        assert getattr(api, name)(*args, **{out: own}, stream=SIDE) is own
+        own.on, own.recorded = 0, []
+        assert getattr(api, name)(*args, **{EXTRA[name]: own}, stream=SIDE) is own
         assert own.recorded == []
         world.launched.pop()
 
@@ -118,3 +147,37 @@ def test_buffers_belong_to_the_stream_of_the_call(name, monkeypatch):
     assert world.made and all(stream is MAIN for _, stream in world.made)
     assert world.launched == [SIDE.cuda_stream, MAIN.cuda_stream]
     assert not any(hasattr(t, "recorded") for t, _ in world.made)
+
+
+@pytest.mark.parametrize("name", sorted(given()))
+def test_a_call_runs_on_the_device_of_its_tensors(name, monkeypatch):
+    args = given(on=1)[name]
+    near, far = placed(torch.zeros((2, 256))), placed(torch.zeros((2, 256)), 1)
+    world = World(monkeypatch)
+    f = getattr(api, name)
+    f(*args)
+    assert world.ran_on == [1] and world.device == 0
+    assert world.made and all(t.on == 1 for t, _ in world.made)
+    f(*args, stream=FAR)
+    assert world.ran_on == [1, 1] and world.launched[1] == FAR.cuda_stream
+    assert (world.device, world.current) == (0, MAIN)
+    f(*args, **{EXTRA[name]: far})
+    assert world.ran_on == [1, 1, 1]
+    for bad in ({EXTRA[name]: near}, {"stream": SIDE}):     # of another device
+        with pytest.raises(api.SaError):
+            f(*args, **bad)
+    assert world.ran_on == [1, 1, 1] and world.device == 0
+
+
+def test_a_status_is_read_on_the_device_of_its_workspace(monkeypatch):
+    ws = placed(torch.zeros(256), 1)
+    world = World(monkeypatch)
+    monkeypatch.setattr(api, "_stream", lambda s: 100 + world.device)
+
+    class Lib:
+        def sa_device_status(self, p, n, stream, detail):
+            assert stream == 101
+            return 0
+
+    monkeypatch.setattr(_abi, "lib", lambda: Lib())
+    assert api.device_status(ws) == (0, 0) and world.device == 0
