@@ -339,6 +339,12 @@ def _outputs(queries: DeviceQueries, d_latent: int, out, lse, out_dtype: str):
     return out, lse
 
 
+def _to_store(out: torch.Tensor) -> torch.Tensor:
+    """Where the attention writes `out`: the tensor-core kernel stores 16 bytes at a
+    time, so an output off a 16-byte boundary is written elsewhere and copied."""
+    return out if out.data_ptr() & 15 == 0 else torch.empty_like(out)
+
+
 @_entry
 def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                     out=None, lse=None, out_dtype: str = "bf16", ws=None, stream=None):
@@ -349,10 +355,13 @@ def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tenso
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
     _need_here("sparse_mla_attn", cache.kv, queries.q, idx, out, lse, ws)
+    to = _to_store(out)
     check(_abi.lib().sa_sparse_mla_attn(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
-                                        _ptr(out), _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws),
+                                        _ptr(to), _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws),
                                         ws.numel(), _stream(stream)),
           "sa_sparse_mla_attn")
+    if to is not out:
+        out.copy_(to)
     return out, lse
 
 
@@ -371,7 +380,8 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
     _need_here("decode", cache.kv, queries.q, out, lse, idx, ws)
-    args = (ctypes.byref(c), ctypes.byref(q), top_k, _ptr(idx), _ptr(out),
+    to = _to_store(out)
+    args = (ctypes.byref(c), ctypes.byref(q), top_k, _ptr(idx), _ptr(to),
             _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
     if phase_events is None:
         check(_abi.lib().sa_decode(*args), "sa_decode")
@@ -383,6 +393,8 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
                 e.record(stream if stream is not None else torch.cuda.current_stream())
         handles = (ctypes.c_void_p * len(phase_events))(*[e.cuda_event for e in phase_events])
         check(_abi.lib().sa_decode_traced(*args, handles), "sa_decode_traced")
+    if to is not out:
+        out.copy_(to)
     return out, lse, idx
 
 

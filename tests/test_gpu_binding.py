@@ -1,5 +1,6 @@
 """GPU tests of the Python binding's own part: calls on another stream than the
-current one, with the buffers that the binding makes itself."""
+current one, with the buffers that the binding makes itself, and outputs off the
+boundary that the kernels store to."""
 import pytest
 import torch
 
@@ -80,3 +81,24 @@ def test_results_outlive_the_callers_use():
             torch.empty_like(other).copy_(other)
         torch.cuda.synchronize()
         assert torch.equal(copy, want)
+
+
+@pytest.mark.parametrize("n,heads", [(2, 128), (90, 128), (2, 16)])   # split keys, whole, CUDA cores
+@pytest.mark.parametrize("out_dtype,off", [("bf16", 4), ("bf16", 1), ("f32", 1), ("f32", 2)])
+def test_outputs_that_start_anywhere(n, heads, out_dtype, off):
+    wl = make("bf16", [200 + i for i in range(n)], heads=heads, h_index=64)
+    idx = selection(wl, 150, 5)
+    cache, queries, idx_t = upload(wl, idx)
+    dtype = torch.bfloat16 if out_dtype == "bf16" else torch.float32
+    want = [api.sparse_mla_attn(cache, queries, idx_t, 150, out_dtype=out_dtype)[0],
+            api.decode(cache, queries, 150, out_dtype=out_dtype)[0]]
+    for i, exp in enumerate(want):
+        room = torch.full((exp.numel() + 16,), 7.0, dtype=dtype, device="cuda")
+        out = room[off:off + exp.numel()].view(exp.shape)
+        assert out.data_ptr() % 16 != 0
+        if i == 0:
+            got, _ = api.sparse_mla_attn(cache, queries, idx_t, 150, out=out, out_dtype=out_dtype)
+        else:
+            got, _, _ = api.decode(cache, queries, 150, out=out, out_dtype=out_dtype)
+        assert got is out and torch.equal(out, exp)
+        assert torch.all(room[:off] == 7) and torch.all(room[off + exp.numel():] == 7)
