@@ -74,11 +74,13 @@ attn_simt_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K,
             row_s[tid] = row;
         }
         __syncthreads();
-        for (int e = tid; e < kRows * D; e += kThreads) {
-            const int r = e / D, dd = e - r * D;
-            const int64_t row = row_s[r];
-            rows_s[r * ldr + dd] = row >= 0 ? kv_value(p, row, dd) : 0.f;
-        }
+        with_kv_dtype(p, [&](auto kv) {
+            for (int e = tid; e < kRows * D; e += kThreads) {
+                const int r = e / D, dd = e - r * D;
+                const int64_t row = row_s[r];
+                rows_s[r * ldr + dd] = row >= 0 ? kv_value_of<kv.value>(p, row, dd) : 0.f;
+            }
+        });
         __syncthreads();
         for (int pr = tid; pr < HG * kRows; pr += kThreads) {
             const int h = pr / kRows, r = pr - h * kRows;

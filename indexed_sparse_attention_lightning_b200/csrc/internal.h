@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 #include <utility>
 
 #include "sa.h"
@@ -201,23 +202,38 @@ __device__ __forceinline__ float kv_scale_at(const PathParams &p, int64_t row, i
                  d / p.kv_scale_dims);
 }
 
-// Latent dim or rope dim dd of physical row `row`, as fp32, from any cache format.
-__device__ __forceinline__ float kv_value(const PathParams &p, int64_t row, int dd) {
+// Latent dim or rope dim dd of physical row `row`, as fp32, of a cache of dtype kKv.
+template <int kKv>
+__device__ __forceinline__ float kv_value_of(const PathParams &p, int64_t row, int dd) {
     const int D = p.d_latent + p.d_rope;
-    if (p.kv_dtype == SA_F32) return static_cast<const float *>(p.kv)[row * D + dd];
-    if (p.kv_dtype == SA_BF16)
+    if constexpr (kKv == SA_F32) return static_cast<const float *>(p.kv)[row * D + dd];
+    if constexpr (kKv == SA_BF16)
         return bf16_bits_to_float(static_cast<const uint16_t *>(p.kv)[row * D + dd]);
     if (dd >= p.d_latent)
         return bf16_bits_to_float(
             static_cast<const uint16_t *>(p.kv_rope)[row * p.d_rope + (dd - p.d_latent)]);
-    if (p.kv_dtype == SA_E4M3) {
+    if constexpr (kKv == SA_E4M3) {
         const uint8_t c = static_cast<const uint8_t *>(p.kv)[row * p.d_latent + dd];
         return e4m3x2_to_float2(c).x * kv_scale_at(p, row, dd);
     }
     const uint32_t two = static_cast<const uint8_t *>(p.kv)[(row * p.d_latent + dd) >> 1];
     const uint32_t sb = reinterpret_cast<const uint8_t *>(
-        p.kv_scale)[(row * p.d_latent + dd) / p.kv_scale_dims];
-    return e2m1x2_to_float2((dd & 1) ? two >> 4 : two & 15u).x * fp4_scale_value(p.kv_dtype, sb);
+        p.kv_scale)[(row * p.d_latent + dd) / fp4_group(kKv)];
+    return e2m1x2_to_float2((dd & 1) ? two >> 4 : two & 15u).x * fp4_scale_value(kKv, sb);
+}
+
+// f(dtype) with the cache's dtype as a constant: a loop over kv_value_of inside it
+// does not look at the dtype for every value (the CUDA-core attention of 8 queries,
+// 16 heads and 1000 bf16 rows: 1886 us with a look for each, 1599 without).
+template <typename F>
+__device__ __forceinline__ void with_kv_dtype(const PathParams &p, F f) {
+    switch (p.kv_dtype) {
+    case SA_F32: return f(std::integral_constant<int, SA_F32>());
+    case SA_BF16: return f(std::integral_constant<int, SA_BF16>());
+    case SA_E4M3: return f(std::integral_constant<int, SA_E4M3>());
+    case SA_MXFP4: return f(std::integral_constant<int, SA_MXFP4>());
+    default: return f(std::integral_constant<int, SA_NVFP4>());
+    }
 }
 
 // Physical cache rows of query t's selected positions sel[0, K): list order,

@@ -531,7 +531,7 @@ read_kernel(const PathParams p, int32_t n, const int32_t *__restrict__ seq_of,
         for (int32_t u = 0; u < count; ++u) {
             const int64_t row = __shfl_sync(0xffffffffu, my_row, u);
             for (int32_t i = lane; i < D; i += 32) {
-                const float v = row >= 0 ? kv_value(p, row, i) : 0.0f;
+                const float v = row >= 0 ? kv_value_of<kKv>(p, row, i) : 0.0f;
                 const int64_t o = (t0 + u) * D + i;
                 if (out_bf16) static_cast<__nv_bfloat16 *>(out)[o] = __float2bfloat16_rn(v);
                 else static_cast<float *>(out)[o] = v;

@@ -102,11 +102,13 @@ weights_simt_kernel(const PathParams p, const float *__restrict__ lse, int32_t l
     const int t = blockIdx.y, tid = threadIdx.x, lane = tid & 31, hw = tid >> 5;
     const int32_t k0 = blockIdx.x * kSimtRows, n = n_valid[t];
     if (k0 >= n) return;
-    for (int e = tid; e < kSimtRows * D; e += kSimtThreads) {
-        const int r = e / D, dd = e - r * D;
-        rows_s[r * ldr + dd] =
-            k0 + r < n ? kv_value(p, rows[(int64_t)t * ld + k0 + r], dd) : 0.0f;
-    }
+    with_kv_dtype(p, [&](auto kv) {
+        for (int e = tid; e < kSimtRows * D; e += kSimtThreads) {
+            const int r = e / D, dd = e - r * D;
+            rows_s[r * ldr + dd] =
+                k0 + r < n ? kv_value_of<kv.value>(p, rows[(int64_t)t * ld + k0 + r], dd) : 0.0f;
+        }
+    });
     float sum = 0.0f;
     for (int h0 = 0; h0 < p.heads; h0 += kSimtHeads) {
         const int hn = min(kSimtHeads, p.heads - h0);
