@@ -569,13 +569,15 @@ def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=No
 @_entry
 def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                        lse: torch.Tensor, acc: Optional[torch.Tensor], decay: float = 1.0,
-                       out=None, ws=None, stream=None) -> torch.Tensor:
+                       out=None, ws=None, stream=None, return_ws: bool = False):
     """Attention weight that each cached position received from these queries,
     summed over heads and queries, on top of ``decay * acc``: fp32 rows [batch,
     >= max_visible] per sequence.  ``idx`` and ``lse`` are the attention's own.
     ``acc`` may be None (zeros); ``out`` defaults to ``acc`` (in place), or to a
     new zero-filled [batch, max_visible].  Both are contiguous, with rows of the
-    same length; only positions below each sequence's length are written."""
+    same length; only positions below each sequence's length are written.
+    ``return_ws``: return (out, ws) instead of out; the workspace's status word
+    records skipped entries and sequences longer than the rows (see device_status)."""
     batch = int(cache.page_table.shape[0])
     if out is None:
         out = acc if acc is not None else torch.zeros(
@@ -594,20 +596,22 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
                                            _ptr(lse), _ptr(acc), decay, _ptr(out), ld, _ptr(ws),
                                            ws.numel(), _stream(stream)),
           "sa_accumulate_weights")
-    return out
+    return (out, ws) if return_ws else out
 
 
 @_entry
 def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: DeviceCache,
                  keep_first: int = 0, keep_last: int = 0, acc_out=None, src_pos=None, ws=None,
-                 stream=None) -> torch.Tensor:
+                 stream=None, return_ws: bool = False):
     """Keep at most ``budget`` tokens of every sequence -- the first
     ``keep_first``, the last ``keep_last`` and those of the largest ``acc``
     between -- and move them, in order, to the pages of ``dst`` (a cache of the
     same formats with its own page table and lengths, which are written; its
     pools may be the same).  ``acc_out`` [batch, >= budget] receives the kept
     sums, zeros behind them.  Returns the kept tokens' original positions,
-    int32 [batch, budget], ascending, padded with -1."""
+    int32 [batch, budget], ascending, padded with -1.  ``return_ws``: return
+    (positions, ws) instead; the workspace's status word records sequences that were
+    skipped whole (see device_status)."""
     batch = int(cache.page_table.shape[0])
     ld = _need_sums(acc, "acc", batch, 1)
     if src_pos is None:
@@ -623,4 +627,4 @@ def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: Device
         ctypes.byref(c), _ptr(acc), ld, budget, keep_first, keep_last, ctypes.byref(d),
         _ptr(acc_out), ld_out, _ptr(src_pos), _ptr(ws), ws.numel(), _stream(stream)),
         "sa_evict_tokens")
-    return src_pos
+    return (src_pos, ws) if return_ws else src_pos

@@ -102,3 +102,34 @@ def test_outputs_that_start_anywhere(n, heads, out_dtype, off):
             got, _, _ = api.decode(cache, queries, 150, out=out, out_dtype=out_dtype)
         assert got is out and torch.equal(out, exp)
         assert torch.all(room[:off] == 7) and torch.all(room[off + exp.numel():] == 7)
+
+
+def test_skipped_work_is_seen_without_a_workspace_of_ones_own():
+    wl = make("mxfp4", (300, 200), heads=128)
+    idx = selection(wl, 50, 3)
+    bad = idx.copy()
+    bad[1, 7] = 200                                     # not yet there
+    cache, queries, idx_t = upload(wl, idx)
+    bad_t = torch.from_numpy(bad).cuda()
+    _, lse = api.sparse_mla_attn(cache, queries, idx_t, 50)
+    acc = torch.rand((2, 300), device="cuda")
+    ok, fault = (_abi.SA_OK, 0), _abi.SA_ERR_DEVICE_FAULT
+    for i, want in ((idx_t, ok), (bad_t, (fault, _abi.SA_DETAIL_BAD_INDEX))):
+        out, ws = api.accumulate_weights(cache, queries, i, 50, lse, acc, return_ws=True,
+                                         out=torch.zeros_like(acc))
+        assert api.device_status(ws) == want
+        assert torch.equal(out, api.accumulate_weights(cache, queries, i, 50, lse, acc,
+                                                       out=torch.zeros_like(acc)))
+    pages = torch.arange(2, dtype=torch.int32, device="cuda").reshape(2, 1) + wl.num_pages
+    for c, want in ((cache, (fault, _abi.SA_DETAIL_BAD_PAGE)), (None, ok)):
+        if c is None:                                   # the pages exist now
+            cache.num_pages += 2
+            for k in ("k_index", "k_index_scale", "kv", "kv_rope", "kv_scale"):
+                t = getattr(cache, k)
+                setattr(cache, k, torch.cat([t, t[:2]]))
+        dst = api.DeviceCache(**{**vars(cache), "page_table": pages,
+                                 "seq_len": torch.zeros(2, dtype=torch.int32, device="cuda")})
+        pos, ws = api.evict_tokens(cache, acc, 64, dst, return_ws=True)
+        assert api.device_status(ws) == want
+        assert dst.seq_len.tolist() == ([0, 0] if want != ok else [64, 64])
+        assert torch.equal(pos, api.evict_tokens(cache, acc, 64, dst))
