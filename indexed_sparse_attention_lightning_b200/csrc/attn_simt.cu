@@ -154,11 +154,12 @@ attn_simt_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K,
 template <int HG>
 cudaError_t launch_hg(const PathParams &p, const int32_t *idx, int32_t K, void *out,
                       int32_t out_dtype, float *lse, cudaStream_t s) {
-    const int D = p.d_latent + p.d_rope;
-    size_t smem = sizeof(float) * ((size_t)HG * D + (size_t)kRows * (D + 1) + HG * kRows + 4 * HG) +
-                  sizeof(int64_t) * (kRows + 2);
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_simt_kernel<HG>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto bytes = [](size_t D) {
+        return sizeof(float) * (HG * D + kRows * (D + 1) + HG * kRows + 4 * HG) +
+               sizeof(int64_t) * (kRows + 2);
+    };
+    const size_t smem = bytes(p.d_latent + p.d_rope);
+    const cudaError_t e = allow_smem(attn_simt_kernel<HG>, bytes(kMaxRow));
     if (e != cudaSuccess) return e;
     dim3 grid(p.heads / HG, p.n_q);
     count_launch();

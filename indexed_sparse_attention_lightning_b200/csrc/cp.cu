@@ -221,8 +221,7 @@ cudaError_t launch_cp_merge(const float *cand_score, const int32_t *cand_pos, in
                             cudaStream_t s) {
     if (n_q == 0) return cudaSuccess;
     const size_t smem = sizeof(uint64_t) * (size_t)n_ranks * top_k;
-    cudaError_t e =
-        cudaFuncSetAttribute(merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(merge_kernel, sizeof(uint64_t) * cp_merge_max_candidates());
     if (e != cudaSuccess) return e;
     count_launch();
     return launch_pdl(merge_kernel, dim3(n_q), dim3(kMergeThreads), smem, s, cand_score, cand_pos,

@@ -569,8 +569,8 @@ cudaError_t launch_evict(const sa_cache *src, const float *acc, int64_t ld_acc, 
     const int32_t cache_per = per * kSelectWarps <= kSelectCached ? (int32_t)per : 0;
     const size_t smem = sizeof(uint32_t) * kSelectWarps * (size_t)cache_per;
     const auto select = cache_per > 0 ? evict_select_kernel<true> : evict_select_kernel<false>;
-    cudaError_t e = cudaFuncSetAttribute(select, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
+    cudaError_t e =
+        cache_per > 0 ? allow_smem(select, sizeof(uint32_t) * kSelectCached) : cudaSuccess;
     if (e == cudaSuccess && ctas > 8)
         e = cudaFuncSetAttribute(select, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;

@@ -738,8 +738,7 @@ cudaError_t launch_indexer_mma_t(const PathParams &p, const int32_t *vis, const 
     const int64_t max_tiles = (int64_t)n_units * ceil_div(p.max_visible, kKeys);
     const int64_t grid = std::min<int64_t>((int64_t)C::kCtasPerSm * num_sms(), max_tiles);
     const size_t smem = sizeof(IndexerSmem<kMode, kQb>) + 1024;
-    cudaError_t e = cudaFuncSetAttribute(indexer_mma_kernel<kMode, kQb>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    cudaError_t e = allow_smem(indexer_mma_kernel<kMode, kQb>, smem);
     if (e != cudaSuccess) return e;
     count_launch();
     return launch_pdl(indexer_mma_kernel<kMode, kQb>, dim3(static_cast<unsigned>(grid)),

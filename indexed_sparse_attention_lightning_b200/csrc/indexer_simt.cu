@@ -136,10 +136,12 @@ indexer_simt_kernel(const PathParams p, float *__restrict__ scores, int64_t ld) 
 cudaError_t launch_indexer_simt(const PathParams &p, float *scores, int64_t ld, cudaStream_t s) {
     if (p.n_q == 0 || p.max_visible == 0) return cudaSuccess;
     dim3 grid(static_cast<unsigned>(ceil_div(p.max_visible, kThreads)), p.n_q);
-    size_t smem = sizeof(float) * ((size_t)p.h_index * p.d_index + p.h_index);
+    const auto bytes = [](size_t heads, size_t dims) {
+        return sizeof(float) * (heads * dims + heads);
+    };
+    const size_t smem = bytes(p.h_index, p.d_index);
     auto go = [&](auto kernel) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem);
+        const cudaError_t e = allow_smem(kernel, bytes(kMaxIndexHeads, kMaxIndexDim));
         if (e != cudaSuccess) return e;
         count_launch();
         return launch_pdl(kernel, grid, dim3(kThreads), smem, s, p, scores, ld);

@@ -33,6 +33,18 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
+// Lets `kernel` be launched with up to `most` bytes of dynamic shared memory.  The
+// limit belongs to the function on the device, not to a launch or a host thread:
+// a kernel whose launches differ in size always gets its largest, or one thread's
+// smaller limit would have another's launch refused.
+template <typename... KArgs>
+cudaError_t allow_smem(void (*kernel)(KArgs...), size_t most) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+}
+
+// Limits of the shapes that the host checks let through.
+constexpr int kMaxLatent = 512, kMaxRow = 1024;  // d_latent, d_latent + d_rope
+constexpr int kMaxIndexHeads = 128, kMaxIndexDim = 256;
 
 // Everything a kernel needs to know about the paged caches and the queries.
 struct PathParams {

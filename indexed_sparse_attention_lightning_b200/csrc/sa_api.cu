@@ -45,12 +45,12 @@ sa_status check_cache(const sa_cache *c) {
     if (scaled && (!c->k_index_scale || !aligned16(c->k_index_scale))) return SA_ERR_INVALID_ARG;
     if (c->d_index <= 0 || c->d_index % 16 != 0) return SA_ERR_INVALID_ARG;
     if (c->index_dtype == SA_MXFP8 && c->d_index % 32 != 0) return SA_ERR_INVALID_ARG;
-    if (c->d_index > 256) return SA_ERR_UNSUPPORTED;
+    if (c->d_index > kMaxIndexDim) return SA_ERR_UNSUPPORTED;
     if (c->kv_dtype != SA_F32 && c->kv_dtype != SA_BF16 && c->kv_dtype != SA_E4M3 &&
         !is_fp4(c->kv_dtype))
         return SA_ERR_UNSUPPORTED;  // SA_MXFP8 names index data only
     if (c->d_latent <= 0 || c->d_rope < 0) return SA_ERR_INVALID_ARG;
-    if (c->d_latent > 512 || c->d_latent + c->d_rope > 1024) return SA_ERR_UNSUPPORTED;
+    if (c->d_latent > kMaxLatent || c->d_latent + c->d_rope > kMaxRow) return SA_ERR_UNSUPPORTED;
     if (c->kv_dtype == SA_E4M3) {
         if (!c->kv_scale || (c->d_rope > 0 && !c->kv_rope)) return SA_ERR_INVALID_ARG;
         if (c->kv_rope && !aligned16(c->kv_rope)) return SA_ERR_INVALID_ARG;
@@ -93,7 +93,7 @@ sa_status check_query(const sa_query *q, const sa_cache *c, bool need_index, boo
     if ((int64_t)q->max_visible > (int64_t)c->max_pages * c->page_size) return SA_ERR_INVALID_ARG;
     if (need_index) {
         if (!q->q_index || !q->w || q->h_index <= 0) return SA_ERR_INVALID_ARG;
-        if (q->h_index > 128) return SA_ERR_UNSUPPORTED;
+        if (q->h_index > kMaxIndexHeads) return SA_ERR_UNSUPPORTED;
         if (q->q_group < 0) return SA_ERR_INVALID_ARG;
         if ((c->index_dtype == SA_E4M3 || c->index_dtype == SA_MXFP8) && !q->q_index_scale)
             return SA_ERR_INVALID_ARG;

@@ -736,7 +736,7 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                         : p.kv_dtype == SA_E4M3  ? sfa_mma_kernel<SA_E4M3>
                         : p.kv_dtype == SA_MXFP4 ? sfa_mma_kernel<SA_MXFP4>
                                                  : sfa_mma_kernel<SA_NVFP4>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
     const int64_t grid = 2 * (int64_t)p.n_q * splits;

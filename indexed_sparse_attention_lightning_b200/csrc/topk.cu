@@ -822,8 +822,7 @@ cudaError_t launch_topk_hist(const float *scores, int64_t ld, const int32_t *vis
                              int32_t ld_rows, int32_t *n_valid, cudaStream_t s) {
     if (n_q == 0) return cudaSuccess;
     if (max_valid <= kSingleMaxV) {
-        cudaError_t e = cudaFuncSetAttribute(
-            topk_single_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSingleSmem);
+        cudaError_t e = allow_smem(topk_single_kernel, kSingleSmem);
         if (e != cudaSuccess) return e;
         count_launch();
         return launch_pdl(topk_single_kernel, dim3(n_q), dim3(kThreads), kSingleSmem, s, scores,
@@ -837,8 +836,7 @@ cudaError_t launch_topk_hist(const float *scores, int64_t ld, const int32_t *vis
                                vis, hist, top_k, sel, chunk_info, ld_chunks, counts, cand, cap);
     if (e != cudaSuccess) return e;
     const size_t smem = finalize_smem_bytes(cap);
-    e = cudaFuncSetAttribute(topk_finalize_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)smem);
+    e = allow_smem(topk_finalize_kernel, smem);  // `cap` is the same in every call
     if (e != cudaSuccess) return e;
     count_launch();
     return launch_pdl(topk_finalize_kernel, dim3(n_q), dim3(kThreads), smem, s, scores, ld, vis,

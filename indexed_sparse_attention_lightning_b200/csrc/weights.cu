@@ -134,11 +134,11 @@ weights_simt_kernel(const PathParams p, const float *__restrict__ lse, int32_t l
 cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t ld,
                                 const int32_t *rows, const int32_t *n_valid, float *w,
                                 cudaStream_t s) {
-    const int D = p.d_latent + p.d_rope;
-    const size_t smem = sizeof(float) * ((size_t)kSimtRows * (D + 1) + (size_t)kSimtHeads * D +
-                                         kSimtHeads * kSimtRows);
-    const cudaError_t e = cudaFuncSetAttribute(
-        weights_simt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const auto bytes = [](size_t D) {
+        return sizeof(float) * (kSimtRows * (D + 1) + kSimtHeads * D + kSimtHeads * kSimtRows);
+    };
+    const size_t smem = bytes(p.d_latent + p.d_rope);
+    const cudaError_t e = allow_smem(weights_simt_kernel, bytes(kMaxRow));
     if (e != cudaSuccess) return e;
     count_launch();
     return launch_pdl(weights_simt_kernel, dim3((unsigned)(ld / kSimtRows), (unsigned)p.n_q),
@@ -528,8 +528,7 @@ cudaError_t launch_weights_mma(const PathParams &p, const int32_t *idx, int32_t 
                         : p.kv_dtype == SA_E4M3  ? weights_mma_kernel<SA_E4M3>
                         : p.kv_dtype == SA_MXFP4 ? weights_mma_kernel<SA_MXFP4>
                                                  : weights_mma_kernel<SA_NVFP4>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = allow_smem(kernel, smem);
     if (e != cudaSuccess) return e;
     const int32_t splits = weights_splits(p.n_q, top_k, p.kv_dtype);
     const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
