@@ -10,8 +10,6 @@ A call runs on the device of its tensors, which must all be on one, and on
 from __future__ import annotations
 
 import ctypes
-import functools
-import inspect
 from dataclasses import dataclass
 from typing import Optional
 
@@ -20,6 +18,10 @@ import torch
 
 from . import _abi
 from ._abi import SaCache, SaError, SaNewTokens, SaQuery, check
+
+# (a torch without CUDA has neither; nor has it tensors that get this far)
+_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 _TORCH_RAW = {np.dtype(np.uint8): torch.uint8, np.dtype(np.uint16): torch.int16,
               np.dtype(np.float32): torch.float32, np.dtype(np.int32): torch.int32}
@@ -84,58 +86,50 @@ def _need_sums(t, name: str, batch: int, min_cols: int) -> int:
     return int(t.shape[1])
 
 
-def _need_here(where: str, *tensors) -> None:
+def _need_here(where: str, *tensors) -> int:
     """The kernels run on the current device, which is that of the entry point's
-    first argument (see _entry): refuse tensors of another one."""
-    here = torch._C._cuda_getDevice()
+    first argument (see _there): refuse tensors of another one.  Returns the raw
+    handle of its current stream (a Stream object costs 3 us)."""
+    here = _device()
     for t in tensors:
         if t is not None and t.get_device() != here:
             raise SaError(_abi.SA_ERR_INVALID_ARG, f"{where}: a tensor is on {t.device}, the "
                                                    f"call runs on cuda:{here}")
+    return _raw_stream(here)
 
 
-def _entry(f):
-    """An entry point runs on the device of its first argument, whichever is
-    current, and on its ``stream``, or that device's current one.  Both are made
+def _away(t) -> bool:
+    """Whether another device than the current one holds an entry point's first argument."""
+    return not isinstance(t, torch.Tensor) or t.get_device() != _device()
+
+
+def _there(f, given: dict):
+    """Entry point `f` with its arguments, on the device of the first one, whichever
+    is current, and on ``stream``, or that device's current one.  Both are made
     current while it runs, so the buffers that the binding makes itself are allocated
     and filled there, and a workspace dropped on return goes back to that stream,
     behind the kernels that use it.  Results that it made may be used on the
     caller's stream, which the allocator is told."""
-    names = list(inspect.signature(f).parameters)
-    at = names.index("stream")
-
-    @functools.wraps(f)
-    def call(*args, **kwargs):
-        first = args[0] if args else kwargs.get(names[0])
-        if isinstance(first, DeviceCache):
-            first = first.page_table
-        device = first.get_device() if isinstance(first, torch.Tensor) else -1
-        stream = args[at] if len(args) > at else kwargs.get("stream")
-        if stream is None:
-            if device < 0 or device == torch._C._cuda_getDevice():
-                return f(*args, **kwargs)
-            with torch.cuda.device(device):
-                return f(*args, **kwargs)
-        if stream.device.index != device >= 0:
-            raise SaError(_abi.SA_ERR_INVALID_ARG, f"{f.__name__}: the stream is on "
-                                                   f"{stream.device}, the tensors on cuda:{device}")
-        caller = torch.cuda.current_stream(stream.device)
-        with torch.cuda.stream(stream):
-            made = f(*args, **kwargs)
-        if caller != stream:
-            given = {id(a) for a in args} | {id(a) for a in kwargs.values()}
-            for t in made if isinstance(made, tuple) else (made,):
-                if isinstance(t, torch.Tensor) and id(t) not in given:
-                    t.record_stream(caller)
-        return made
-
-    return call
-
-
-def _stream(stream) -> int:
-    if stream is None:  # the raw handle: a Stream object costs 3 us
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+    first = next(iter(given.values()))
+    first = first.page_table if isinstance(first, DeviceCache) else first
+    if not isinstance(first, torch.Tensor) or first.get_device() < 0:
+        raise SaError(_abi.SA_ERR_INVALID_ARG, f"{f.__name__}: CUDA tensors only")
+    stream = given.pop("stream")
+    if stream is None:
+        with torch.cuda.device(first.get_device()):
+            return f(**given)
+    if stream.device.index != first.get_device():
+        raise SaError(_abi.SA_ERR_INVALID_ARG, f"{f.__name__}: the stream is on "
+                                               f"{stream.device}, the tensors on {first.device}")
+    caller = torch.cuda.current_stream(stream.device)
+    with torch.cuda.stream(stream):
+        made = f(**given)
+    if caller != stream:
+        own = {id(a) for a in given.values()}
+        for t in made if isinstance(made, tuple) else (made,):
+            if isinstance(t, torch.Tensor) and id(t) not in own:
+                t.record_stream(caller)
+    return made
 
 
 @dataclass
@@ -279,19 +273,22 @@ def workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-@_entry
 def device_status(ws: torch.Tensor, stream=None) -> tuple[int, int]:
     """(status, detail) of the last call that used `ws`; synchronises the stream."""
+    if stream is not None or _away(ws):
+        return _there(device_status, locals())
     detail = ctypes.c_int32(0)
-    st = _abi.lib().sa_device_status(_ptr(ws), ws.numel(), _stream(stream), ctypes.byref(detail))
+    st = _abi.lib().sa_device_status(_ptr(ws), ws.numel(), _raw_stream(_device()),
+                                     ctypes.byref(detail))
     return int(st), int(detail.value)
 
 
 # -------------------------------------------------------------- entry points ---
 
-@_entry
 def indexer_score(cache: DeviceCache, queries: DeviceQueries, scores=None, ws=None,
                   stream=None) -> torch.Tensor:
+    if stream is not None or _away(cache.page_table):
+        return _there(indexer_score, locals())
     dev = queries.q_seq.device
     if scores is None:
         scores = torch.full((queries.n_q, max(1, queries.max_visible)), float("nan"),
@@ -301,16 +298,17 @@ def indexer_score(cache: DeviceCache, queries: DeviceQueries, scores=None, ws=No
     _need_rows(scores, "scores", queries.n_q, queries.max_visible)
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
-    _need_here("indexer_score", cache.k_index, queries.q_index, scores, ws)
+    stream = _need_here("indexer_score", cache.k_index, queries.q_index, scores, ws)
     check(_abi.lib().sa_indexer_score(ctypes.byref(c), ctypes.byref(q), _ptr(scores),
-                                      scores.stride(0), _ptr(ws), ws.numel(), _stream(stream)),
+                                      scores.stride(0), _ptr(ws), ws.numel(), stream),
           "sa_indexer_score")
     return scores
 
 
-@_entry
 def topk(scores: torch.Tensor, valid_len: torch.Tensor, top_k: int, max_valid: int,
          idx=None, ws=None, stream=None) -> torch.Tensor:
+    if stream is not None or _away(scores):
+        return _there(topk, locals())
     n_q = scores.shape[0]
     if idx is None:
         idx = torch.empty((n_q, top_k), dtype=torch.int32, device=scores.device)
@@ -320,9 +318,9 @@ def topk(scores: torch.Tensor, valid_len: torch.Tensor, top_k: int, max_valid: i
     _need(valid_len, "valid_len", torch.int32, (n_q,))
     _need(idx, "idx", torch.int32, (n_q, top_k))
     _need(ws, "ws")
-    _need_here("topk", valid_len, idx, ws)
+    stream = _need_here("topk", valid_len, idx, ws)
     check(_abi.lib().sa_topk(_ptr(scores), scores.stride(0), _ptr(valid_len), n_q, max_valid,
-                             top_k, _ptr(idx), _ptr(ws), ws.numel(), _stream(stream)),
+                             top_k, _ptr(idx), _ptr(ws), ws.numel(), stream),
           "sa_topk")
     return idx
 
@@ -345,33 +343,35 @@ def _to_store(out: torch.Tensor) -> torch.Tensor:
     return out if out.data_ptr() & 15 == 0 else torch.empty_like(out)
 
 
-@_entry
 def sparse_mla_attn(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                     out=None, lse=None, out_dtype: str = "bf16", ws=None, stream=None):
+    if stream is not None or _away(cache.page_table):
+        return _there(sparse_mla_attn, locals())
     out, lse = _outputs(queries, cache.d_latent, out, lse, out_dtype)
     if ws is None:
         ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_ATTN), idx.device)
     _need(idx, "idx", torch.int32, (queries.n_q, top_k))
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
-    _need_here("sparse_mla_attn", cache.kv, queries.q, idx, out, lse, ws)
+    stream = _need_here("sparse_mla_attn", cache.kv, queries.q, idx, out, lse, ws)
     to = _to_store(out)
     check(_abi.lib().sa_sparse_mla_attn(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
                                         _ptr(to), _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws),
-                                        ws.numel(), _stream(stream)),
+                                        ws.numel(), stream),
           "sa_sparse_mla_attn")
     if to is not out:
         out.copy_(to)
     return out, lse
 
 
-@_entry
 def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse=None,
            idx=None, out_dtype: str = "bf16", ws=None, stream=None, phase_events=None):
     """Fused indexer -> top-K -> sparse attention.  Returns (out, lse, idx-or-None).
 
     ``phase_events``: optional list of len(_abi.DECODE_PHASES) + 1 torch.cuda.Event
     objects recorded at the phase boundaries (sa_decode_traced)."""
+    if stream is not None or _away(cache.page_table):
+        return _there(decode, locals())
     out, lse = _outputs(queries, cache.d_latent, out, lse, out_dtype)
     if ws is None:
         ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_DECODE),
@@ -379,10 +379,10 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
     _need(idx, "idx", torch.int32, (queries.n_q, top_k), optional=True)
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
-    _need_here("decode", cache.kv, queries.q, out, lse, idx, ws)
+    stream = _need_here("decode", cache.kv, queries.q, out, lse, idx, ws)
     to = _to_store(out)
     args = (ctypes.byref(c), ctypes.byref(q), top_k, _ptr(idx), _ptr(to),
-            _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), _stream(stream))
+            _abi.DTYPES[out_dtype], _ptr(lse), _ptr(ws), ws.numel(), stream)
     if phase_events is None:
         check(_abi.lib().sa_decode(*args), "sa_decode")
     else:
@@ -390,7 +390,7 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
             raise ValueError("need one event per phase boundary")
         for e in phase_events:
             if e.cuda_event == 0:       # torch creates the CUDA event on first record
-                e.record(stream if stream is not None else torch.cuda.current_stream())
+                e.record(torch.cuda.current_stream())
         handles = (ctypes.c_void_p * len(phase_events))(*[e.cuda_event for e in phase_events])
         check(_abi.lib().sa_decode_traced(*args, handles), "sa_decode_traced")
     if to is not out:
@@ -400,11 +400,12 @@ def decode(cache: DeviceCache, queries: DeviceQueries, top_k: int, out=None, lse
 
 # -------------------------------------------- context-parallel decode steps ---
 
-@_entry
 def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
                      offset: torch.Tensor, score=None, pos=None, ws=None, stream=None):
     """This GPU's top_k of its context shard as (score fp32, position + offset
     int32), both [n_q, top_k], ascending positions, (-inf, -1) padding."""
+    if stream is not None or _away(cache.page_table):
+        return _there(local_candidates, locals())
     dev = queries.q_seq.device
     n_q = queries.n_q
     if score is None:
@@ -418,19 +419,19 @@ def local_candidates(cache: DeviceCache, queries: DeviceQueries, top_k: int,
     _need(pos, "pos", torch.int32, (n_q, top_k))
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
-    _need_here("local_candidates", cache.kv, queries.q, offset, score, pos, ws)
+    stream = _need_here("local_candidates", cache.kv, queries.q, offset, score, pos, ws)
     check(_abi.lib().sa_local_candidates(ctypes.byref(c), ctypes.byref(q), top_k, _ptr(offset),
-                                         _ptr(score), _ptr(pos), _ptr(ws), ws.numel(),
-                                         _stream(stream)),
+                                         _ptr(score), _ptr(pos), _ptr(ws), ws.numel(), stream),
           "sa_local_candidates")
     return score, pos, ws
 
 
-@_entry
 def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: torch.Tensor,
                      hi: torch.Tensor, idx_global=None, idx_local=None, stream=None):
     """All ranks' candidates [n_ranks, n_q, top_k] -> (global top-K positions,
     the ones in [lo, hi) as local positions), both int32 [n_q, top_k]."""
+    if stream is not None or _away(score):
+        return _there(merge_candidates, locals())
     n_ranks, n_q, k = score.shape
     if k != top_k:
         raise SaError(_abi.SA_ERR_INVALID_ARG, "merge_candidates: candidate rows of top_k")
@@ -444,19 +445,19 @@ def merge_candidates(score: torch.Tensor, pos: torch.Tensor, top_k: int, lo: tor
         idx_local = torch.empty((n_q, top_k), dtype=torch.int32, device=score.device)
     _need(idx_global, "idx_global", torch.int32, (n_q, top_k))
     _need(idx_local, "idx_local", torch.int32, (n_q, top_k))
-    _need_here("merge_candidates", pos, lo, hi, idx_global, idx_local)
+    stream = _need_here("merge_candidates", pos, lo, hi, idx_global, idx_local)
     check(_abi.lib().sa_merge_candidates(_ptr(score), _ptr(pos), n_ranks, n_q, top_k, _ptr(lo),
-                                         _ptr(hi), _ptr(idx_global), _ptr(idx_local),
-                                         _stream(stream)),
+                                         _ptr(hi), _ptr(idx_global), _ptr(idx_local), stream),
           "sa_merge_candidates")
     return idx_global, idx_local
 
 
-@_entry
 def combine_partials(o_part: torch.Tensor, lse_part: torch.Tensor, out=None, lse=None,
                      out_dtype: str = "bf16", stream=None):
     """Partial outputs [n_parts, n_q, heads, d] (fp32) with their lse [n_parts,
     n_q, heads] -> (out [n_q, heads, d], lse [n_q, heads])."""
+    if stream is not None or _away(o_part):
+        return _there(combine_partials, locals())
     n_parts, n_q, heads, d = o_part.shape
     _need(o_part, "o_part", torch.float32, (n_parts, n_q, heads, d))
     _need(lse_part, "lse_part", torch.float32, (n_parts, n_q, heads))
@@ -467,10 +468,9 @@ def combine_partials(o_part: torch.Tensor, lse_part: torch.Tensor, out=None, lse
         lse = torch.empty((n_q, heads), dtype=torch.float32, device=o_part.device)
     _need(out, "out", dt, (n_q, heads, d))
     _need(lse, "lse", torch.float32, (n_q, heads))
-    _need_here("combine_partials", lse_part, out, lse)
+    stream = _need_here("combine_partials", lse_part, out, lse)
     check(_abi.lib().sa_combine_partials(_ptr(o_part), _ptr(lse_part), n_parts, n_q, heads, d,
-                                         _ptr(out), _abi.DTYPES[out_dtype], _ptr(lse),
-                                         _stream(stream)),
+                                         _ptr(out), _abi.DTYPES[out_dtype], _ptr(lse), stream),
           "sa_combine_partials")
     return out, lse
 
@@ -486,10 +486,11 @@ def _in_dtype(t: torch.Tensor) -> int:
     return _abi.DTYPES[_IN_DTYPES[t.dtype]]
 
 
-@_entry
 def quantize_index_query(q: torch.Tensor, out=None, scale=None, stream=None):
     """Indexer query [n_q, h_index, d_index] (bfloat16 or float32) -> (e4m3 codes
     uint8 [n_q, h_index, d_index], fp32 scales [n_q, h_index])."""
+    if stream is not None or _away(q):
+        return _there(quantize_index_query, locals())
     _need(q, "q", (torch.bfloat16, torch.float32))
     n_q, h, d = q.shape
     if out is None:
@@ -498,14 +499,13 @@ def quantize_index_query(q: torch.Tensor, out=None, scale=None, stream=None):
         scale = torch.empty((n_q, h), dtype=torch.float32, device=q.device)
     _need(out, "out", torch.uint8, (n_q, h, d))
     _need(scale, "scale", torch.float32, (n_q, h))
-    _need_here("quantize_index_query", out, scale)
+    stream = _need_here("quantize_index_query", out, scale)
     check(_abi.lib().sa_quantize_index_query(_ptr(q), _in_dtype(q), n_q, h, d, _ptr(out),
-                                             _ptr(scale), _stream(stream)),
+                                             _ptr(scale), stream),
           "sa_quantize_index_query")
     return out, scale
 
 
-@_entry
 def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
                   k_index: Optional[torch.Tensor] = None, kv: Optional[torch.Tensor] = None,
                   ws=None, stream=None) -> torch.Tensor:
@@ -513,6 +513,8 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
     index keys [n_new, d_index] and latent + rope rows [n_new, d_latent + d_rope],
     both bfloat16 or both float32 (either may be None).  Returns the workspace,
     whose status word records skipped tokens (see device_status)."""
+    if stream is not None or _away(cache.page_table):
+        return _there(append_tokens, locals())
     if k_index is not None and kv is not None and k_index.dtype != kv.dtype:
         raise SaError(_abi.SA_ERR_INVALID_ARG, "append_tokens: k_index and kv dtypes differ")
     n_new = int(seq.numel())
@@ -531,21 +533,22 @@ def append_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor,
             raise SaError(_abi.SA_ERR_INVALID_ARG, "sa_workspace_size")
         ws = workspace(n, seq.device)
     _need(ws, "ws")
-    _need_here("append_tokens", cache.kv, seq, pos, k_index, kv, ws)
+    stream = _need_here("append_tokens", cache.kv, seq, pos, k_index, kv, ws)
     t = SaNewTokens(n_new, _ptr(seq), _ptr(pos), dt, _ptr(k_index), _ptr(kv))
     check(_abi.lib().sa_append_tokens(ctypes.byref(c), ctypes.byref(t), _ptr(ws), ws.numel(),
-                                      _stream(stream)),
+                                      stream),
           "sa_append_tokens")
     return ws
 
 
-@_entry
 def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=None,
                 out_dtype: str = "bf16", ws=None, stream=None):
     """Latent + rope rows of tokens (sequence, position) as the values the pool
     stands for: [n, d_latent + d_rope] in ``out_dtype`` ("bf16" or "f32"; taken
     from ``out`` when given).  Returns (out, ws): the workspace's status word
     records tokens that do not exist, whose rows are zero."""
+    if stream is not None or _away(cache.page_table):
+        return _there(read_tokens, locals())
     n = int(seq.numel())
     _need(seq, "seq", torch.int32, (n,))
     _need(pos, "pos", torch.int32, (n,))
@@ -556,17 +559,16 @@ def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=No
     if ws is None:
         ws = workspace(workspace_size(cache, None, 0, _abi.SA_WS_APPEND), seq.device)
     _need(ws, "ws")
-    _need_here("read_tokens", cache.kv, seq, pos, out, ws)
+    stream = _need_here("read_tokens", cache.kv, seq, pos, out, ws)
     c = cache.struct()
     check(_abi.lib().sa_read_tokens(ctypes.byref(c), n, _ptr(seq), _ptr(pos), _ptr(out),
-                                    _in_dtype(out), _ptr(ws), ws.numel(), _stream(stream)),
+                                    _in_dtype(out), _ptr(ws), ws.numel(), stream),
           "sa_read_tokens")
     return out, ws
 
 
 # -------------------------------------- shrinking a cache by its attention ---
 
-@_entry
 def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Tensor, top_k: int,
                        lse: torch.Tensor, acc: Optional[torch.Tensor], decay: float = 1.0,
                        out=None, ws=None, stream=None, return_ws: bool = False):
@@ -578,6 +580,8 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
     same length; only positions below each sequence's length are written.
     ``return_ws``: return (out, ws) instead of out; the workspace's status word
     records skipped entries and sequences longer than the rows (see device_status)."""
+    if stream is not None or _away(cache.page_table):
+        return _there(accumulate_weights, locals())
     batch = int(cache.page_table.shape[0])
     if out is None:
         out = acc if acc is not None else torch.zeros(
@@ -591,15 +595,14 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
         ws = workspace(workspace_size(cache, queries, top_k, _abi.SA_WS_WEIGHTS), idx.device)
     _need(ws, "ws")
     c, q = cache.struct(), queries.struct()
-    _need_here("accumulate_weights", cache.kv, queries.q, idx, lse, acc, out, ws)
+    stream = _need_here("accumulate_weights", cache.kv, queries.q, idx, lse, acc, out, ws)
     check(_abi.lib().sa_accumulate_weights(ctypes.byref(c), ctypes.byref(q), _ptr(idx), top_k,
                                            _ptr(lse), _ptr(acc), decay, _ptr(out), ld, _ptr(ws),
-                                           ws.numel(), _stream(stream)),
+                                           ws.numel(), stream),
           "sa_accumulate_weights")
     return (out, ws) if return_ws else out
 
 
-@_entry
 def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: DeviceCache,
                  keep_first: int = 0, keep_last: int = 0, acc_out=None, src_pos=None, ws=None,
                  stream=None, return_ws: bool = False):
@@ -612,6 +615,8 @@ def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: Device
     int32 [batch, budget], ascending, padded with -1.  ``return_ws``: return
     (positions, ws) instead; the workspace's status word records sequences that were
     skipped whole (see device_status)."""
+    if stream is not None or _away(cache.page_table):
+        return _there(evict_tokens, locals())
     batch = int(cache.page_table.shape[0])
     ld = _need_sums(acc, "acc", batch, 1)
     if src_pos is None:
@@ -622,9 +627,9 @@ def evict_tokens(cache: DeviceCache, acc: torch.Tensor, budget: int, dst: Device
         ws = workspace(workspace_size(cache, None, budget, _abi.SA_WS_EVICT), acc.device)
     _need(ws, "ws")
     c, d = cache.struct(), dst.struct()
-    _need_here("evict_tokens", cache.kv, dst.kv, dst.seq_len, acc, acc_out, src_pos, ws)
+    stream = _need_here("evict_tokens", cache.kv, dst.kv, dst.seq_len, acc, acc_out, src_pos, ws)
     check(_abi.lib().sa_evict_tokens(
         ctypes.byref(c), _ptr(acc), ld, budget, keep_first, keep_last, ctypes.byref(d),
-        _ptr(acc_out), ld_out, _ptr(src_pos), _ptr(ws), ws.numel(), _stream(stream)),
+        _ptr(acc_out), ld_out, _ptr(src_pos), _ptr(ws), ws.numel(), stream),
         "sa_evict_tokens")
     return (src_pos, ws) if return_ws else src_pos

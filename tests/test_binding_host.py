@@ -75,12 +75,12 @@ class World:
         lib = Lib()
         monkeypatch.setattr(torch.cuda, "stream", On)
         monkeypatch.setattr(torch.cuda, "device", On)
-        monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: world.device, raising=False)
+        monkeypatch.setattr(api, "_device", lambda: world.device)
+        monkeypatch.setattr(api, "_raw_stream", lambda device: world.current.cuda_stream)
         monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: world.current)
         monkeypatch.setattr(_abi, "lib", lambda: lib)
         monkeypatch.setattr(api, "_need", lambda *a, **k: None)
         monkeypatch.setattr(api, "_need_rows", lambda *a, **k: None)
-        monkeypatch.setattr(api, "_stream", lambda s: (s or world.current).cuda_stream)
         for name in ("empty", "zeros", "full"):
             monkeypatch.setattr(torch, name, making(getattr(torch, name)))
 
@@ -172,7 +172,7 @@ def test_a_call_runs_on_the_device_of_its_tensors(name, monkeypatch):
 def test_a_status_is_read_on_the_device_of_its_workspace(monkeypatch):
     ws = placed(torch.zeros(256), 1)
     world = World(monkeypatch)
-    monkeypatch.setattr(api, "_stream", lambda s: 100 + world.device)
+    monkeypatch.setattr(api, "_raw_stream", lambda device: 100 + device)
 
     class Lib:
         def sa_device_status(self, p, n, stream, detail):
