@@ -99,8 +99,9 @@ def _need_here(where: str, *tensors) -> int:
 
 
 def _away(t) -> bool:
-    """Whether another device than the current one holds an entry point's first argument."""
-    return not isinstance(t, torch.Tensor) or t.get_device() != _device()
+    """Whether an entry point's first argument is not on the current device."""
+    d = t.get_device() if isinstance(t, torch.Tensor) else -1   # -1: the host
+    return d < 0 or d != _device()
 
 
 def _there(f, given: dict):
