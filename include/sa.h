@@ -347,7 +347,10 @@ SA_API sa_status sa_combine_partials(const float *o_part, const float *lse_part,
  *     even (1 for an all-zero group); where that rounds to 0 every code is +0;
  *   code = e2m1(x / scale) with an IEEE round-to-nearest division, rounded to
  *     nearest (ties to the even code) and saturated to +-6.
- * Inputs must be finite: a NaN or infinity gives unspecified codes. */
+ *   A group that holds a NaN or an infinity, which e2m1 has not, takes the scale
+ *   byte that is NaN (SA_MXFP4: 255, SA_NVFP4: 0x7F) and codes of +0, so that
+ *   all of it reads back, and enters an attention, as NaN.
+ * FP8 inputs must be finite: a NaN or infinity gives unspecified codes. */
 
 /* Indexer query -> e4m3 codes + one fp32 scale per (token, head): the form
  * sa_query.q_index / q_index_scale take for an SA_E4M3 index cache.

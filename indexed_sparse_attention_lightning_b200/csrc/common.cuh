@@ -124,6 +124,13 @@ __device__ __forceinline__ float relu_keep_nan(float x) {
     return y;
 }
 
+// max(a, b), NaN if either is.
+__device__ __forceinline__ float max_keep_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
 // ---------------------------------------------------------------------------
 // Paged addressing: physical row of logical position s of sequence seq, or -1
 // when the page id is outside [0, num_pages) or the slot is past max_pages.

@@ -11,11 +11,15 @@
 //
 // A 4-bit latent takes, per group of 32 (MXFP4) or 16 values (NVFP4), a scale
 // byte that puts the largest magnitude near e2m1's 6: 2^(floor(log2 amax) - 2),
-// or e4m3(amax / 6); code = e2m1(x / scale), nearest even, saturated to +-6.
+// or e4m3(amax / 6); code = e2m1(x / scale), nearest even, saturated to +-6.  e2m1
+// has neither infinity nor NaN, so a group that holds one takes the scale byte that
+// is NaN: the whole group reads back as NaN.
 //
 // The kernels are memory-bound: one warp per quantised row of the query
 // (d_index values), per token of a 4-bit cache and per row read back, one CTA
 // per other appended token.
+#include <cfloat>
+
 #include "common.cuh"
 #include "internal.h"
 #include "prep.h"
@@ -152,8 +156,12 @@ __device__ void quantize_groups(const void *src, int64_t s0, bool bf16, int32_t 
     __syncthreads();  // gmax is reused by the next call
 }
 
-// amax of a group -> its scale byte of a 4-bit latent and that byte's value.
+// The scale bytes that are NaN.
+constexpr uint32_t kE8m0Nan = 255u, kE4m3Nan = 0x7Fu;
+
+// amax of a group (NaN if one of its values is) -> its scale byte of a 4-bit latent.
 __device__ __forceinline__ uint32_t fp4_scale_byte(int32_t dtype, float amax) {
+    if (!(amax <= FLT_MAX)) return dtype == SA_MXFP4 ? kE8m0Nan : kE4m3Nan;
     if (dtype == SA_MXFP4) {
         if (!(amax > 0.0f)) return 127u;
         // floor(log2 amax): the exponent field of a normal number; of a subnormal
@@ -173,11 +181,12 @@ __device__ __forceinline__ uint32_t fp4_scale_byte(int32_t dtype, float amax) {
 // with fp32's 1 / s, within 2^-23 of x / s and rounded to 16 bits, is m in the
 // one case and on x / s's side of it in the other, and the code is the
 // quotient's (a division per value: 40001 rows appended in 35 us).  A scale
-// that rounded to 0 gives zeros.
+// that rounded to 0, or is NaN, gives zeros.
 template <int kKv, bool kBf16>
 __device__ __forceinline__ uint2 to_fp4x16(const float (&x)[16], uint32_t scale_byte) {
     float q[16];
     if constexpr (kKv == SA_MXFP4) {
+        if (scale_byte == kE8m0Nan) return make_uint2(0u, 0u);
         // 2^(127 - byte): byte <= 252, so neither end leaves the normal range
         const float inv = __uint_as_float((254u - scale_byte) << 23);
 #pragma unroll
@@ -426,10 +435,10 @@ append_fp4_kernel(const AppendParams p, int32_t block) {
                 float x[16], amax = 0.0f;
                 raw[u].values(x);
 #pragma unroll
-                for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));
+                for (int i = 0; i < 16; ++i) amax = max_keep_nan(amax, fabsf(x[i]));
                 if (kKv == SA_MXFP4) {
                     const uint32_t lanes = 0xffffffffu >> (32 - chunks);
-                    amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
+                    amax = max_keep_nan(amax, __shfl_xor_sync(lanes, amax, 1));
                 }
                 const uint32_t byte = fp4_scale_byte(kKv, amax);
                 codes[lane] = to_fp4x16<kKv, kBf16>(x, byte);

@@ -283,18 +283,19 @@ def to_e2m1_codes(x: np.ndarray) -> np.ndarray:
 
 
 def quantize_fp4(x: np.ndarray, kv_dtype: str):
-    """Rows of the last axis -> (bytes of two codes, scale bytes) of a 4-bit latent."""
+    """Rows of the last axis -> (bytes of two codes, scale bytes) of a 4-bit latent.
+    A group with a NaN or an infinity: a NaN scale over codes of 0."""
     grp = FP4_GROUP[kv_dtype]
     g = x.reshape(x.shape[:-1] + (x.shape[-1] // grp, grp)).astype(np.float32)
     amax = np.abs(g).max(axis=-1)
     if kv_dtype == "mxfp4":
         _, ex = np.frexp(amax)
         byte = np.where(amax > 0, np.clip(ex.astype(np.int64) - 1 - 2 + 127, 0, 254), 127)
-        byte = byte.astype(np.uint8)
-        scale = np.ldexp(np.float32(1.0), byte.astype(np.int64) - 127).astype(np.float32)
+        byte = np.where(np.isfinite(amax), byte, 255).astype(np.uint8)
+        scale = e8m0_value(byte)
     else:
         s = np.where(amax > 0, amax / np.float32(6.0), np.float32(1.0)).astype(np.float32)
-        byte = to_e4m3_codes(s)
+        byte = np.where(np.isfinite(amax), to_e4m3_codes(s), E4M3_NAN).astype(np.uint8)
         scale = torch.from_numpy(byte).view(torch.float8_e4m3fn).float().numpy()
     s = scale[..., None]
     codes = to_e2m1_codes(np.where(s > 0, g / np.where(s > 0, s, np.float32(1.0)),

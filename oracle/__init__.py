@@ -135,11 +135,14 @@ def fp4_decode(kv_dtype: str, codes: np.ndarray, scales: np.ndarray) -> np.ndarr
 
 def quantize_fp4(x: np.ndarray, kv_dtype: str):
     """fp32 rows -> (bytes of two codes, scale bytes): the quotients are taken in
-    fp32 and the nearest e2m1 value is found by search, ties to the even code."""
+    fp32 and the nearest e2m1 value is found by search, ties to the even code.  A
+    group with a NaN or an infinity: the scale byte that is NaN, codes 0."""
     x = np.ascontiguousarray(x, dtype=np.float32)
     g = x.reshape(x.shape[:-1] + (-1, FP4_GROUP[kv_dtype]))
     amax = np.abs(g).max(axis=-1)
     byte = np.full(amax.shape, 127, dtype=np.uint8)
+    lost = ~np.isfinite(amax)
+    amax = np.where(lost, np.float32(0), amax)
     if kv_dtype == "mxfp4":
         some = amax > 0
         e = np.floor(np.log2(amax[some].astype(np.float64))) - 2
@@ -147,6 +150,7 @@ def quantize_fp4(x: np.ndarray, kv_dtype: str):
     else:
         s = np.where(amax > 0, amax / np.float32(6), np.float32(1)).astype(np.float32)
         byte = e4m3_encode(np.minimum(s, np.float32(448)))
+    byte[lost] = 255 if kv_dtype == "mxfp4" else 0x7F
     sc = fp4_scale_decode(kv_dtype, byte).astype(np.float32)[..., None]
     quot = np.where(sc > 0, g / np.where(sc > 0, sc, np.float32(1)), np.float32(0))
     # (past 8 everything is nearest to 6; the cut keeps the differences exact)

@@ -205,3 +205,36 @@ def test_attention_refuses_an_output_its_stores_cannot_reach(L, fmt):
 def test_new_names_are_bound():
     assert _abi.DTYPES["mxfp4"] == 4 and _abi.DTYPES["nvfp4"] == 5
     assert torch.uint8 is not None and len(set(_abi.EXPORTS)) == len(_abi.EXPORTS)
+
+
+# ------------------------------------------------- values that are not finite ---
+
+def rows_not_finite(d=64):
+    """(rows, which groups of 16 hold a NaN or an infinity)."""
+    x = _rows(9, n=12, d=d)
+    bad = [(0, 3, np.nan), (1, 20, -np.nan), (2, 40, np.inf), (3, 63, -np.inf), (4, 0, np.nan),
+           (4, 1, np.inf), (8, 15, np.nan), (8, 16, np.nan)]
+    for r, c, v in bad:
+        x[r, c] = v
+    x[9, 16:32] = np.nan                                  # nothing else in the group
+    x[10, 32:48] = -np.inf
+    return x, ~np.isfinite(x).reshape(12, d // 16, 16).all(axis=-1)
+
+
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_a_group_that_is_not_finite_reads_back_as_nan(fmt):
+    x, bad = rows_not_finite()
+    if fmt == "mxfp4":
+        bad = np.repeat(bad.reshape(12, -1, 2).any(axis=-1), 2, axis=1)
+    for quantize in (W.quantize_fp4, oracle.quantize_fp4):
+        codes, scales = quantize(x, fmt)
+        v = oracle.fp4_decode(fmt, codes, scales)
+        assert np.array_equal(np.isnan(v).reshape(12, -1, 16).any(axis=-1), bad)
+        assert np.array_equal(np.isnan(v).reshape(12, -1, 16).all(axis=-1), bad)
+        clean = np.where(np.repeat(bad, 16, axis=1), np.float32(0), x)
+        want_codes, want_scales = quantize(clean, fmt)     # the other groups as ever
+        at = np.repeat(bad, 8, axis=1)
+        assert np.array_equal(codes[~at], want_codes[~at]) and np.all(codes[at] == 0)
+        group_bad = bad if fmt == "nvfp4" else bad[:, ::2]
+        assert np.array_equal(scales[~group_bad], want_scales[~group_bad])
+        assert np.all(scales[group_bad] == (255 if fmt == "mxfp4" else 0x7F))

@@ -22,7 +22,7 @@ import oracle
 from indexed_sparse_attention_lightning_b200 import _abi, api
 from indexed_sparse_attention_lightning_b200 import workloads as W
 from tests import parity
-from tests.test_cache_ops_host import _rows
+from tests.test_cache_ops_host import _rows, rows_not_finite
 
 pytestmark = pytest.mark.gpu
 
@@ -1003,3 +1003,47 @@ def test_binding_refuses_what_the_library_would_misread():
     refused(api.read_tokens, cache, pos, pos, out=torch.zeros((2, 576), device="cuda",
                                                               dtype=torch.float16))
     refused(api.read_tokens, cache, pos, pos[:1])
+
+
+# ------------------------------------------------- values that are not finite ---
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_values_that_are_not_finite_stay_visible(fmt, inp):
+    wl = make(fmt, (12, 12), d_latent=64, d_rope=8, heads=16)
+    cache, _ = api.upload(wl)
+    x = torch.from_numpy(np.concatenate([rows_not_finite()[0], np.ones((12, 8), np.float32)],
+                                        axis=1))
+    x = x.to(torch.bfloat16 if inp == "bf16" else torch.float32)
+    seq, pos = np.zeros(12, np.int32), np.arange(12, dtype=np.int32)
+    seq_t, pos_t = torch.from_numpy(seq).cuda(), torch.from_numpy(pos).cuda()
+    ws = api.append_tokens(cache, seq_t, pos_t, kv=x.cuda())
+    assert api.device_status(ws) == OK
+    want, _ = oracle.append_tokens(_pools(wl), _layout(wl), seq, pos, None, x.float().numpy())
+    same_bytes(_device_pools(cache), want)
+    rows = values(dataclasses.replace(wl, **want))[row_of(wl, 0, pos)]
+    assert np.isnan(rows).any() and not np.isnan(rows).all(axis=1).any()
+    for out_dtype in ("bf16", "f32"):
+        back, _ = api.read_tokens(cache, seq_t, pos_t, out_dtype=out_dtype)
+        exp = torch.from_numpy(rows).to(back.dtype)
+        assert torch.equal(torch.isnan(back.cpu()), torch.isnan(exp))
+        assert torch.equal(torch.nan_to_num(back.cpu()), torch.nan_to_num(exp))
+
+
+@pytest.mark.parametrize("inp", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", ["mxfp4", "nvfp4"])
+def test_a_poisoned_token_poisons_the_attention_that_selects_it(fmt, inp):
+    wl = make(fmt, (70, 70), heads=128)
+    idx = selection(wl, 70, 4)
+    cache, queries, idx_t = upload(wl, idx)
+    before, _ = api.sparse_mla_attn(cache, queries, idx_t, 70)
+    x = torch.ones((1, 576), dtype=torch.bfloat16 if inp == "bf16" else torch.float32,
+                   device="cuda")
+    x[0, 77] = float("nan")
+    at = torch.tensor([1], dtype=torch.int32, device="cuda")
+    api.append_tokens(cache, at, at + 65, kv=x)
+    out, _ = api.sparse_mla_attn(cache, queries, idx_t, 70)
+    assert torch.isnan(out[1]).all() and torch.equal(out[0], before[0])
+    idx_t[1][idx_t[1] == 66] = -1                          # not selected: not seen
+    out, _ = api.sparse_mla_attn(cache, queries, idx_t, 70)
+    assert torch.isfinite(out.float()).all()
