@@ -430,20 +430,21 @@ evict_move_kernel(const EvictArgs a, const EvictFields fields, int32_t pieces, i
     }
     const int32_t *row_of = a.src_row + (int64_t)b * a.budget;
     const int32_t *table = a.dst_table + (int64_t)b * a.dst_max_pages;
-    const int32_t step = gridDim.x * (kMoveThreads / 32) * rows;
+    // kept places are below 2^31, those that a step leads to may be above
+    const uint32_t end = kept, step = gridDim.x * (kMoveThreads / 32) * rows;
     // lane r looks token r of a group up
-    auto places = [&](int32_t i0, int32_t &from, int32_t &to) {
-        const int32_t i = i0 + lane;
+    auto places = [&](uint32_t i0, int32_t &from, int32_t &to) {
+        const uint32_t i = i0 + lane;
         from = to = 0;
-        if (lane >= rows || i >= kept) return;
+        if (lane >= rows || i >= end) return;
         from = row_of[i];
         to = table[i >> 6] * 64 + (i & 63);
     };
     int32_t from, to;
-    int32_t i0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * rows;
+    uint32_t i0 = (blockIdx.x * (kMoveThreads / 32) + (threadIdx.x >> 5)) * rows;
     places(i0, from, to);
-    for (; i0 < kept; i0 += step) {
-        const int32_t n = min(rows, kept - i0);
+    for (; i0 < end; i0 += step) {
+        const int32_t n = min((uint32_t)rows, end - i0);
         uint4 x[kMovePieces];
 #pragma unroll
         for (int j = 0; j < kMovePieces; ++j) {
