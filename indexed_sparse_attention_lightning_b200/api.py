@@ -161,6 +161,9 @@ class DeviceCache:
         _need(self.kv, "kv", optional=True)
         _need(self.kv_rope, "kv_rope", optional=True)
         _need(self.kv_scale, "kv_scale", optional=True)
+        if self.page_table.dim() != 2 or self.seq_len.numel() < self.page_table.shape[0]:
+            raise SaError(_abi.SA_ERR_INVALID_ARG, "page_table must be [batch, max_pages] and "
+                                                   "seq_len have an entry per sequence")
         # in the order of the struct's fields: by keyword the construction takes twice as long
         batch, max_pages = self.page_table.shape
         return SaCache(
@@ -197,6 +200,8 @@ class DeviceQueries:
     def struct(self) -> SaQuery:
         _need(self.q_seq, "q_seq", torch.int32)
         _need(self.q_pos, "q_pos", torch.int32)
+        if self.q_pos.numel() < self.n_q:
+            raise SaError(_abi.SA_ERR_INVALID_ARG, "q_pos must have an entry per query")
         for name in ("q_index", "q_index_scale", "w", "q"):
             _need(getattr(self, name), name, optional=True)
         return SaQuery(
@@ -554,6 +559,8 @@ def read_tokens(cache: DeviceCache, seq: torch.Tensor, pos: torch.Tensor, out=No
     _need(seq, "seq", torch.int32, (n,))
     _need(pos, "pos", torch.int32, (n,))
     if out is None:
+        if out_dtype not in _IN_DTYPES.values():
+            raise SaError(_abi.SA_ERR_UNSUPPORTED, "read_tokens: out_dtype (bf16 or f32)")
         dt = torch.bfloat16 if out_dtype == "bf16" else torch.float32
         out = torch.empty((n, cache.d_latent + cache.d_rope), dtype=dt, device=seq.device)
     _need(out, "out", (torch.bfloat16, torch.float32), (n, cache.d_latent + cache.d_rope))

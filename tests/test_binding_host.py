@@ -1,6 +1,7 @@
 """The Python binding's own part, with the library and CUDA replaced by
 stand-ins: which stream its buffers are made on, which device a call runs on
 (no GPU)."""
+import dataclasses
 import types
 
 import pytest
@@ -181,3 +182,28 @@ def test_a_status_is_read_on_the_device_of_its_workspace(monkeypatch):
 
     monkeypatch.setattr(_abi, "lib", lambda: Lib())
     assert api.device_status(ws) == (0, 0) and world.device == 0
+
+
+def test_arrays_that_are_too_short_are_refused(monkeypatch):
+    """The kernels read an entry of seq_len per sequence (an eviction writes the
+    destination's) and one of q_pos per query."""
+    args = given()
+    short = placed(torch.zeros(1, dtype=torch.int32))
+    flat = placed(torch.zeros(8, dtype=torch.int32))
+    World(monkeypatch)
+    cache, queries, idx, _, lse, _ = args["accumulate_weights"]
+    sums = args["evict_tokens"][1]
+    cut = dataclasses.replace(cache, seq_len=short)
+    wrong = dataclasses.replace(cache, page_table=flat)
+    for call in (lambda: api.evict_tokens(cache, sums, 64, cut),
+                 lambda: api.evict_tokens(cut, sums, 64, cache),
+                 lambda: api.evict_tokens(cache, sums, 64, wrong),
+                 lambda: api.accumulate_weights(cut, queries, idx, 8, lse, None),
+                 lambda: api.accumulate_weights(
+                     cache, dataclasses.replace(queries, q_pos=short), idx, 8, lse, None),
+                 lambda: api.read_tokens(wrong, flat, flat),
+                 lambda: api.read_tokens(cache, flat, flat, out_dtype="f16")):
+        with pytest.raises(api.SaError):
+            call()
+    # buffers of a larger capacity are fine
+    api.evict_tokens(cache, sums, 64, dataclasses.replace(cache, seq_len=flat))
