@@ -158,12 +158,14 @@ cudaError_t launch_sfa_mma(const PathParams &p, const int32_t *idx, int32_t top_
                            cudaStream_t s);
 
 // Accumulated attention weights (weights.cu).  Each query's selection is compacted
-// into physical rows (one list per CTA: n_q * weights_splits of them) and kept
+// into physical rows (n_q * weights_lists of them: one per query or per CTA) and kept
 // positions (n_valid of them), `starts` notes where each range of positions begins
 // in them, w [n_q, weights_ld] takes one weight per kept entry, and the sum kernel
 // adds those to the sequences' rows.  Leading dimension of rows, kept and w:
 // weights_ld(K); of starts: weights_starts_ld(n_q, batch, max_visible).
 int32_t weights_splits(int32_t n_q, int32_t top_k, int32_t kv_dtype);
+int32_t weights_lists(int32_t n_q, int32_t top_k, int32_t kv_dtype);
+bool weights_rows_first(int32_t n_q, int32_t top_k, int32_t kv_dtype);
 int32_t weights_ld(int32_t top_k);
 int32_t weights_starts_ld(int32_t n_q, int32_t batch, int32_t max_visible);
 cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, int32_t top_k,

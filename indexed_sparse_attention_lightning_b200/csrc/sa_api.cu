@@ -160,7 +160,7 @@ struct Layout {
         lse_part;
     size_t indexer_total, decode_total;
     size_t attn_o_part, attn_lse_part, attn_total;
-    // accumulated weights: status | rows [n_q, weights_splits, weights_ld] | kept and w
+    // accumulated weights: status | rows [n_q, weights_lists, weights_ld] | kept and w
     // [n_q, weights_ld] each | n_valid [n_q] | starts [n_q, weights_starts_ld]
     size_t wt_rows, wt_kept, wt_w, wt_n_valid, wt_starts, wt_total;
 };
@@ -197,9 +197,9 @@ Layout make_layout(const sa_query *q, int32_t top_k, const sa_cache *c) {
     l.attn_lse_part = align_up(l.attn_o_part + o_bytes);
     l.attn_total = align_up(l.attn_lse_part + lse_bytes);
     const size_t wt_bytes = 4 * nq * (size_t)weights_ld(top_k);
-    const size_t wt_splits = (size_t)weights_splits(q->n_q, top_k, c->kv_dtype);
+    const size_t wt_lists = (size_t)weights_lists(q->n_q, top_k, c->kv_dtype);
     l.wt_rows = align_up(kStatusBytes);
-    l.wt_kept = align_up(l.wt_rows + wt_splits * wt_bytes);
+    l.wt_kept = align_up(l.wt_rows + wt_lists * wt_bytes);
     l.wt_w = align_up(l.wt_kept + wt_bytes);
     l.wt_n_valid = align_up(l.wt_w + wt_bytes);
     l.wt_starts = align_up(l.wt_n_valid + sizeof(int32_t) * nq);

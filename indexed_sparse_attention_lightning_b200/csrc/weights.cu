@@ -6,8 +6,9 @@
 //     acc_out[b,s] = decay * acc_in[b,s] + sum_{t of b} w[t,s]
 // For the attention's production shape two kernels: weights (each query's
 // selection as physical rows and positions, then one fp32 w per selected entry, on
-// the tensor cores) and sum; for other shapes a rows kernel in front of a weights
-// kernel on CUDA cores.  Sums over queries are taken in the order of t without
+// the tensor cores) and sum; a rows kernel in front makes rows and positions for
+// very long selections (weights_rows_first) and for the CUDA-core weights kernel
+// of other shapes.  Sums over queries are taken in the order of t without
 // atomics between CTAs, so results are reproducible: in the sum kernel each warp
 // owns a range of one sequence's positions, keeps its sums in shared memory and
 // walks the queries in order.
@@ -54,7 +55,6 @@ __device__ __forceinline__ void write_starts(const int32_t *pos, int32_t n, int3
     }
 }
 
-// For the CUDA-core kernel; the tensor-core one compacts its selection itself.
 constexpr int kRowsThreads = 512;
 __global__ void __launch_bounds__(kRowsThreads)
 weights_rows_kernel(const PathParams p, const int32_t *__restrict__ idx, int32_t K, int32_t ld,
@@ -152,7 +152,8 @@ cudaError_t launch_weights_simt(const PathParams &p, const float *lse, int32_t l
 // once per query, and a stage is free again as soon as its S is done.
 //   all         turn the query's selection into rows, each CTA for itself while Q
 //               is on its way (64 queries 51.6 us, with a kernel in front 53.7; 256
-//               queries, two CTAs after one another, 128 and 126.5);
+//               queries, two CTAs after one another, 128 and 126.5), unless the rows
+//               kernel has (see weights_rows_first);
 //   warp 0      lane 0 loads Q by TMA (its halves into ring stages 1 and 2), then
 //               the warp issues the MMAs;
 //   warps 1-7   gather the rows (sfa_gather.cuh; with warp 12 for a 4-bit latent);
@@ -300,10 +301,15 @@ constexpr int kProducers = is_fp4(kKv) ? kFp4Warps : kProducerWarps;
 template <int kKv>
 constexpr int kCtaThreads = 32 * (5 + kProducers<kKv>);
 
+// Entries of a selection that a thread looks up in one step of a CTA.
+constexpr int kEntries = 6;
+
+// rows_ready: the rows kernel has made rows (one list per query), kept, n_valid and
+// starts; otherwise each CTA makes its own list, and the query's first the others.
 template <int kKv>  // sa_dtype of the latent cache
 __global__ void __launch_bounds__(kCtaThreads<kKv>, 1)
 weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
-                   const int32_t *__restrict__ idx, int32_t K, int32_t splits,
+                   const int32_t *__restrict__ idx, int32_t K, int32_t splits, bool rows_ready,
                    const float *__restrict__ lse, int32_t ld, int32_t ld_starts,
                    int32_t range_log2, int32_t *rows_of, int32_t *kept, int32_t *n_valid_of,
                    int32_t *starts_of, float *__restrict__ w) {
@@ -312,11 +318,11 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
     const int t = blockIdx.x / splits, split = blockIdx.x % splits;
     const int warp = warp_id(), lane = lane_id();
     const int32_t *sel = idx + (int64_t)t * K;
-    int32_t *rows = rows_of + (int64_t)blockIdx.x * ld;  // this CTA's own
+    int32_t *rows = rows_of + (int64_t)(rows_ready ? t : blockIdx.x) * ld;
     int32_t *pos = kept + (int64_t)t * ld, *starts = starts_of + (int64_t)t * ld_starts;
-    int32_t entries[6];
+    int32_t entries[kEntries];
     pdl_wait();
-    load_entries(sel, K, 0, entries);
+    if (!rows_ready) load_entries(sel, K, 0, entries);
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -345,9 +351,13 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
                 tma_load_2d(sm.kv[1 + half] + b * (64 * 128), &tm_q, 64 * b,
                             t * kHeads + 64 * half, &sm.q_full);
     }
-    if (threadIdx.x == 0 && split == 0) starts[0] = 0;
-    compact_selection(p, t, sel, K, kTile, rows, &sm.n_valid, sm.scratch, entries,
-                      split == 0 ? pos : nullptr);
+    if (rows_ready) {
+        if (threadIdx.x == 0) sm.n_valid = n_valid_of[t];
+    } else {
+        if (threadIdx.x == 0 && split == 0) starts[0] = 0;
+        compact_selection(p, t, sel, K, kTile, rows, &sm.n_valid, sm.scratch, entries,
+                          split == 0 ? pos : nullptr);
+    }
     __syncthreads();
     const uint32_t tmem = sm.tmem_base;
     volatile int *abort_flag = &sm.abort;
@@ -457,7 +467,7 @@ weights_mma_kernel(const __grid_constant__ CUtensorMap tm_q, const PathParams p,
         else
             produce_rows<kKv>(p, tile_rows, T, producer_index(warp), sm.kv, sm.kv_full,
                               sm.kv_empty, &sm.q_ready, 1, abort_flag, status);
-        if (split == 0) {
+        if (split == 0 && !rows_ready) {
             const int32_t thread = 32 * producer_index(warp) + lane;
             write_starts(pos, n_valid, starts, ld_starts, range_log2, thread,
                          32 * kProducers<kKv>);
@@ -534,8 +544,8 @@ cudaError_t launch_weights_mma(const PathParams &p, const int32_t *idx, int32_t 
     const int threads = is_fp4(p.kv_dtype) ? kCtaThreads<SA_MXFP4> : kCtaThreads<SA_BF16>;
     count_launch();
     return launch_pdl(kernel, dim3((unsigned)((int64_t)p.n_q * splits)), dim3(threads), smem,
-                      s, tq, p, idx, top_k, splits, lse, ld, ld_starts, range_log2, rows, kept,
-                      n_valid, starts, w);
+                      s, tq, p, idx, top_k, splits, weights_rows_first(p.n_q, top_k, p.kv_dtype),
+                      lse, ld, ld_starts, range_log2, rows, kept, n_valid, starts, w);
 }
 
 // -------------------------------------------------------------------- sum ---
@@ -682,6 +692,21 @@ int32_t weights_splits(int32_t n_q, int32_t top_k, int32_t kv_dtype) {
     return std::max(1, std::min(tiles, num_sms() / n_q));
 }
 
+// Whether the rows kernel runs in front of the tensor-core one: for selections that
+// take a CTA more than four steps, if several CTAs share a query: each would make and
+// store the whole list for its few tiles.  Two queries over e4m3, 5000 entries: 50 us
+// with the kernel in front and 44 without; one query over bf16, 9400 entries: 46 and
+// 53, 300000 entries: 638 and 1140, with 3.6 and 180 MB of workspace.
+bool weights_rows_first(int32_t n_q, int32_t top_k, int32_t kv_dtype) {
+    return top_k > 4 * kEntries * kCtaThreads<SA_BF16> &&
+           weights_splits(n_q, top_k, kv_dtype) > 1;
+}
+
+int32_t weights_lists(int32_t n_q, int32_t top_k, int32_t kv_dtype) {
+    if (weights_rows_first(n_q, top_k, kv_dtype)) return 1;
+    return weights_splits(n_q, top_k, kv_dtype);
+}
+
 int32_t weights_ld(int32_t top_k) { return (int32_t)round_up(top_k > 0 ? top_k : 1, kTile); }
 
 int32_t weights_starts_ld(int32_t n_q, int32_t batch, int32_t max_visible) {
@@ -699,15 +724,17 @@ cudaError_t launch_accumulate_weights(const PathParams &p, const int32_t *idx, i
     const int32_t ld_starts = weights_starts_ld(p.n_q, p.batch, p.max_visible);
     cudaError_t e;
     const int32_t range_log2 = many ? 8 : 10;
-    if (p.n_q > 0 && weights_mma_supported(p)) {
-        e = launch_weights_mma(p, idx, top_k, lse, ld, ld_starts, range_log2, rows, kept, n_valid,
-                               starts, w, s);
-        if (e != cudaSuccess) return e;
-    } else if (p.n_q > 0) {
+    const bool mma = weights_mma_supported(p);
+    if (p.n_q > 0 && (!mma || weights_rows_first(p.n_q, top_k, p.kv_dtype))) {
         count_launch();
         e = launch_pdl(weights_rows_kernel, dim3((unsigned)p.n_q), dim3(kRowsThreads), 0, s, p, idx,
                        top_k, ld, ld_starts, range_log2, rows, kept, n_valid, starts);
-        if (e == cudaSuccess) e = launch_weights_simt(p, lse, ld, rows, n_valid, w, s);
+        if (e != cudaSuccess) return e;
+    }
+    if (p.n_q > 0) {
+        e = mma ? launch_weights_mma(p, idx, top_k, lse, ld, ld_starts, range_log2, rows, kept,
+                                     n_valid, starts, w, s)
+                : launch_weights_simt(p, lse, ld, rows, n_valid, w, s);
         if (e != cudaSuccess) return e;
     }
     return many ? launch_weights_sum<SumMany>(p, ld, ld_starts, kept, n_valid, starts, w, acc_in,

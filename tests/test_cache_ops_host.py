@@ -238,3 +238,21 @@ def test_a_group_that_is_not_finite_reads_back_as_nan(fmt):
         group_bad = bad if fmt == "nvfp4" else bad[:, ::2]
         assert np.array_equal(scales[~group_bad], want_scales[~group_bad])
         assert np.all(scales[group_bad] == (255 if fmt == "mxfp4" else 0x7F))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "mxfp4"])
+@pytest.mark.parametrize("n_q", [1, 3, 74, 75, 300])
+def test_workspace_of_the_weights_follows_the_selections(L, n_q, fmt):
+    """Rows, positions and weights are 12 bytes an entry.  CTAs that share a query make
+    a list of rows each only where that is short: 148 lists of 9216 entries at most
+    (a query whose tiles are split takes at most as many CTAs as there are SMs)."""
+    kv = {"bf16": {}, "e4m3": {"kv_dtype": _abi.SA_E4M3, **FP4, "kv_scale_tokens": 1,
+                               "kv_scale_dims": 128},
+          "mxfp4": {"kv_dtype": _abi.SA_MXFP4, **FP4}}[fmt]
+    c = good_cache(**kv, max_pages=1 << 14, num_pages=1 << 14)
+    for k in (64, 2304, 9216, 9217, 100000, 1 << 20):
+        q = good_query(n_q=n_q, max_visible=1 << 20)
+        need = ws_size(L, c, q, k, _abi.SA_WS_WEIGHTS)
+        starts = n_q * (4 + 4 * ((1 << 20) // 256 + 1))
+        entries = 12 * n_q * (k + 63)
+        assert entries - 12 * n_q * 63 < need <= entries + starts + 148 * 9216 * 4 + 6 * 256

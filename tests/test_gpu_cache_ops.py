@@ -529,6 +529,16 @@ def test_weights_of_long_selections(kv, heads):
     check_weights(wl, selection(wl, 5000, 6, holes=True))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "nvfp4", "e4m3"])
+def test_weights_of_selections_that_take_many_steps(kv):
+    """Longer than the weights kernel looks up itself: a kernel in front does."""
+    wl = make(kv, (10500, 9217, 40), heads=128)
+    idx = selection(wl, 10000, 6, holes=True)
+    idx[1, :300] = idx[1, 300:600]                # repeated entries, and in no order
+    check_weights(wl, idx, decay=0.5)
+    check_weights(wl, selection(wl, 9217, 7), inplace=True)
+
+
 @pytest.mark.parametrize("heads,dl,dr", [(1, 64, 16), (7, 96, 8), (20, 512, 64), (130, 32, 0)])
 def test_weights_of_other_shapes(heads, dl, dr):
     wl = make("nvfp4", (50, 400), heads=heads, d_latent=dl, d_rope=dr)
