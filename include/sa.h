@@ -428,7 +428,11 @@ SA_API sa_status sa_read_tokens(const sa_cache *cache, int32_t n, const int32_t 
  * it was.  idx (device int32 [n_q, top_k]) and lse (device fp32 [n_q, heads])
  * are what sa_sparse_mla_attn or sa_decode took and returned (for a cache
  * split over GPUs: the rank's local positions with the combined lse), so that
- * a query's weights sum to `heads`; -1 entries are skipped, an entry that
+ * a query's weights sum to `heads`.  (SA_E4M3 at 128 heads x (512 + 64) dims: to
+ * that within a factor exp(+-d) a head.  The attention there rounds a value, code
+ * x scale, to bf16 and its lse belongs to the rounded rows, while the weights take
+ * the value itself to 2^-16; d is at most 2^-8 sm_scale sum |q[d] kv[s,d]| over the
+ * latent dims of a selected row.)  -1 entries are skipped, an entry that
  * occurs twice counts twice, as it does in the attention, and a head with
  * lse = -inf (nothing selected) adds nothing.  acc_in may be NULL (zeros) or
  * equal to acc_out; otherwise the two must not overlap.  decay must be finite.

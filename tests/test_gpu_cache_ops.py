@@ -583,6 +583,34 @@ def test_weights_of_one_query_sum_to_the_heads():
     assert torch.all(out[1, 1:] == 0)
 
 
+@pytest.mark.parametrize("K", [1, 700])
+@pytest.mark.parametrize("heads", [128, 16])
+@pytest.mark.parametrize("kv,tile", [("bf16", (0, 0)), ("nvfp4", (0, 0)), ("e4m3", (0, 0)),
+                                     ("e4m3", (1, 128))])
+def test_weights_of_a_query_against_the_attentions_lse(kv, tile, heads, K):
+    """With the attention's own lse a query's weights sum to `heads`.  The tensor-core
+    attention rounds an e4m3 value (code times scale) to bf16, 2^-8 of it, and its lse
+    belongs to the rounded rows, so there a head's sum is off by a factor within
+    exp(+-d), d the largest 2^-8 sm sum |q_d k_d| over the latent dims of its rows.
+    Both sides' own errors as in check_attention and weights_ref."""
+    wl = make(kv, (2500, 900), heads=heads, kv_scale_tile=tile, sm_scale=0.1)
+    idx = selection(wl, K, 5)
+    cache, queries, idx_t = upload(wl, idx)
+    _, lse = api.sparse_mla_attn(cache, queries, idx_t, K)
+    got = api.accumulate_weights(cache, queries, idx_t, K, lse, None).double().sum(1).cpu().numpy()
+    l = lse.double().cpu().numpy()
+    for t in range(2):
+        sel = idx[t][idx[t] >= 0]
+        _, dz, kv_rows = logits(wl, t, sel)
+        dl = wl.spec.d_latent
+        size = (np.abs(q_values(wl)[t][:, :dl]) @ np.abs(kv_rows[:, :dl]).T) * 0.1
+        d = 2.0 ** -8 * size.max(axis=1) if kv == "e4m3" and heads == 128 else 0.0
+        own = dz.max(axis=1) + 2.0 ** -21 + 2 * EPS * (sel.size + np.abs(l[t])) + 1e-6   # the lse's
+        own = own + dz.max(axis=1) + 2.0 ** -21 + 4 * EPS * np.abs(l[t])         # the weights'
+        room = np.expm1(d + own).sum() + 4 * EPS * heads * heads
+        assert abs(got[t] - heads) <= room
+
+
 def test_weights_with_infinite_lse_and_no_queries():
     wl = make("bf16", (128, 128), heads=128)
     idx = selection(wl, 40, 3)
