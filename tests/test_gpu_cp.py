@@ -16,6 +16,7 @@ import oracle
 from indexed_sparse_attention_lightning_b200 import _abi, api, cp
 from indexed_sparse_attention_lightning_b200 import workloads as W
 from tests import parity
+from tests.test_gpu_cache_ops import make, selection, upload, weights_ref
 
 pytestmark = pytest.mark.gpu
 
@@ -105,3 +106,44 @@ def test_combine_weights_parts_by_lse_and_skips_empty_parts():
     ref = (w[..., None] * o).sum(0) / w.sum(0)[..., None]
     np.testing.assert_allclose(out.cpu().numpy(), ref, rtol=1e-5, atol=1e-6)
     np.testing.assert_allclose(lse.cpu().numpy(), m + np.log(w.sum(0)), rtol=1e-6, atol=1e-6)
+
+
+@pytest.mark.parametrize("world", [2, 3])
+@pytest.mark.parametrize("kv,heads", [("bf16", 128), ("nvfp4", 128), ("bf16", 16)])
+def test_weights_of_a_split_cache(kv, heads, world):
+    """Each rank weighs its part of the selection, local positions with the combined
+    lse: together its sums are those of the whole cache."""
+    wl = make(kv, (900, 2000, 300), heads=heads)
+    K = 400
+    idx = selection(wl, K, 5)
+    idx[2] = np.where(idx[2] >= 100, -1, idx[2])            # nothing on the last rank
+    shards = cp.partition(wl.seq_len, world)
+    ranks, o, lse = [], [], []
+    for sh in shards:
+        lo, hi = sh.lo[wl.q_seq][:, None], sh.hi[wl.q_seq][:, None]
+        local = np.where((idx >= lo) & (idx < hi), idx - lo, -1).astype(np.int32)
+        cache, queries, idx_t = upload(W.shard_workload(wl, sh.lo, sh.hi), local)
+        ranks.append((cache, queries, idx_t))
+        part = api.sparse_mla_attn(cache, queries, idx_t, K, out_dtype="f32")
+        o.append(part[0])
+        lse.append(part[1])
+    _, lse = api.combine_partials(torch.stack(o), torch.stack(lse))
+    rng = np.random.default_rng(3)
+    acc = rng.random((3, 2000)).astype(np.float32)
+    ref, tol = weights_ref(wl, idx, lse.cpu().numpy(), acc, 0.75)
+    for sh, (cache, queries, idx_t) in zip(shards, ranks):
+        width = int((sh.hi - sh.lo).max())
+        mine = np.zeros((3, width), np.float32)
+        for b in range(3):
+            n = sh.hi[b] - sh.lo[b]
+            mine[b, :n] = acc[b, sh.lo[b]:sh.hi[b]]
+        out, ws = api.accumulate_weights(cache, queries, idx_t, K, lse,
+                                         torch.from_numpy(mine).cuda(), decay=0.75,
+                                         return_ws=True)
+        assert api.device_status(ws) == (_abi.SA_OK, 0)
+        out = out.double().cpu().numpy()
+        for b in range(3):
+            at = slice(sh.lo[b], sh.hi[b])
+            n = sh.hi[b] - sh.lo[b]
+            assert np.all(np.abs(out[b, :n] - ref[b, at]) <= tol[b, at])
+            assert np.all(out[b, n:] == 0)
