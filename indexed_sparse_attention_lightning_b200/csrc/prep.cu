@@ -275,31 +275,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AppendPara
 constexpr int kWarpThreads = 256;
 constexpr int kWarpTokens = kWarpThreads / 32;
 
-// N consecutive values starting at element i of src (16-byte pieces).
-template <int N>
-__device__ __forceinline__ void load_values(const void *src, int64_t i, bool bf16, float (&x)[N]) {
-    if (bf16) {
-        const uint4 *s = reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(src) + i);
-#pragma unroll
-        for (int j = 0; j < N / 8; ++j) {
-            const uint4 u = __ldg(s + j);
-            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                x[8 * j + 2 * k] = __uint_as_float(w[k] << 16);
-                x[8 * j + 2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
-            }
-        }
-    } else {
-        const float4 *s = reinterpret_cast<const float4 *>(static_cast<const float *>(src) + i);
-#pragma unroll
-        for (int j = 0; j < N / 4; ++j) {
-            const float4 f = __ldg(s + j);
-            x[4 * j] = f.x, x[4 * j + 1] = f.y, x[4 * j + 2] = f.z, x[4 * j + 3] = f.w;
-        }
-    }
-}
-
 // N values to element i of dst, rounded to nearest even for bf16.
 template <int N>
 __device__ __forceinline__ void store_values(void *dst, int64_t i, bool bf16,
