@@ -20,10 +20,9 @@
  * as e4m3 with one fp32 scale per tile of tokens x latent dims (a whole page
  * by default; rope stays bf16).  Input preparation quantises the query and
  * appends new tokens in these formats.  The latent may also be held in 4 bits
- * (e2m1 codes with one small scale per 32 or 16 dims): a row then takes about
- * a third of its bf16 size ("Long-Context LLM Inference Optimization": a cache
- * footprint below a quarter of the original).  A cache that outgrows its
- * memory is shrunk by the attention its positions received: see
+ * (e2m1 codes with one small scale per 32 or 16 dims): a row of 512 + 64 dims
+ * then takes 400 or 416 bytes, 35 % of its 1152 in bf16.  A cache that outgrows
+ * its memory is shrunk by the attention its positions received: see
  * sa_accumulate_weights and sa_evict_tokens.
  *
  * Conventions for every entry point
@@ -80,7 +79,8 @@ typedef enum sa_dtype {
     SA_MXFP4 = 4,             /* latent cache only: e2m1 codes, two to a byte (dim 2i in the
                                * low half of byte i), with one E8M0 scale byte per 32 dims */
     SA_NVFP4 = 5              /* latent cache only: e2m1 codes as above with one e4m3fn scale
-                               * byte per 16 dims */
+                               * byte per 16 dims: NVFP4's blocks without its fp32 scale per
+                               * tensor (see the 4-bit rules at sa_append_tokens) */
 } sa_dtype;
 
 /* Paged caches of one attention layer.
@@ -347,6 +347,13 @@ SA_API sa_status sa_combine_partials(const float *o_part, const float *lse_part,
  *     even (1 for an all-zero group); where that rounds to 0 every code is +0;
  *   code = e2m1(x / scale) with an IEEE round-to-nearest division, rounded to
  *     nearest (ties to the even code) and saturated to +-6.
+ *   An SA_NVFP4 row holds what its e4m3 scales reach, as no fp32 scale per tensor
+ *   stands above them: a group of amax <= 6 * 2^-10 (0.0059) becomes zero, one below
+ *   6 * 2^-6 (0.094) has a subnormal scale of fewer bits, and values past 2688
+ *   saturate.  A caller with latents of another size applies a tensor scale T
+ *   itself: append kv / T (latent only), multiply the latent dims of the attention
+ *   query by T, and the output (and rows read back) by T; lse and accumulated
+ *   weights are then those of the unscaled rows.
  *   A group that holds a NaN or an infinity, which e2m1 has not, takes the scale
  *   byte that is NaN (SA_MXFP4: 255, SA_NVFP4: 0x7F) and codes of +0, so that
  *   all of it reads back, and enters an attention, as NaN.
@@ -458,9 +465,9 @@ SA_API sa_status sa_accumulate_weights(const sa_cache *cache, const sa_query *qu
  * its index key and scale, its latent row, rope and scales, byte for byte.
  * dst has src's batch, formats, dims and page size and its own page table
  * (dst->max_pages * page_size >= budget); its pools may be src's own, with
- * the destination pages disjoint from every page that src reads -- except
- * that a sequence which keeps all its tokens may keep its own pages, in the
- * same order.  src's seq_len and page table are not changed: afterwards the
+ * the destination pages disjoint from one another and from every page that src
+ * reads -- except that a sequence which keeps all its tokens may keep its own
+ * pages, in the same order.  src's seq_len and page table are not changed: afterwards the
  * caller frees the old pages.  src and dst must not share seq_len.
  * Written besides the pools:
  *   dst->seq_len[b]  the kept count;

@@ -585,7 +585,8 @@ def accumulate_weights(cache: DeviceCache, queries: DeviceQueries, idx: torch.Te
     >= max_visible] per sequence.  ``idx`` and ``lse`` are the attention's own.
     ``acc`` may be None (zeros); ``out`` defaults to ``acc`` (in place), or to a
     new zero-filled [batch, max_visible].  Both are contiguous, with rows of the
-    same length; only positions below each sequence's length are written.
+    same length; only positions below each sequence's length are written (bring
+    ``out`` for sequences longer than max_visible, whose rest is reported otherwise).
     ``return_ws``: return (out, ws) instead of out; the workspace's status word
     records skipped entries and sequences longer than the rows (see device_status)."""
     if stream is not None or _away(cache.page_table):

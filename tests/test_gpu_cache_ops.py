@@ -1085,3 +1085,37 @@ def test_a_poisoned_token_poisons_the_attention_that_selects_it(fmt, inp):
     idx_t[1][idx_t[1] == 66] = -1                          # not selected: not seen
     out, _ = api.sparse_mla_attn(cache, queries, idx_t, 70)
     assert torch.isfinite(out.float()).all()
+
+
+@pytest.mark.parametrize("log2_t", [-4, 2])
+def test_a_tensor_scale_is_folded_into_query_and_output(log2_t):
+    """NVFP4 rows of another size: the latent is appended times 1 / T, the query's
+    latent dims and the output are multiplied by T.  T is a power of two and the e4m3
+    scales stay normal (amax / 6 of 16 values N(0, 1) lies above 2^-4), so every step
+    is the same but for exponents."""
+    wl = make("nvfp4", (300, 200), heads=128)
+    idx = selection(wl, 120, 5)
+    cache, queries, idx_t = upload(wl, idx)
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(3)
+    x = torch.randn((500, 576), device="cuda", generator=gen).bfloat16()
+    seq = torch.tensor([0] * 300 + [1] * 200, dtype=torch.int32, device="cuda")
+    pos = torch.cat([torch.arange(300), torch.arange(200)]).int().cuda()
+    t = 2.0 ** log2_t
+    got = []
+    for stored, query, back in ((1.0, 1.0, 1.0), (1.0, 1.0, 1.0), (t, 1.0, 1.0), (t, t, t)):
+        kv, q = x.clone(), queries.q.view(torch.bfloat16).clone()
+        kv[:, :512] /= stored                       # times 1 / T and back: both exact
+        q[..., :512] *= query
+        api.append_tokens(cache, seq, pos, kv=kv)
+        mine = dataclasses.replace(queries, q=q)
+        out, lse = api.sparse_mla_attn(cache, mine, idx_t, 120)
+        sums = api.accumulate_weights(cache, mine, idx_t, 120, lse, None)
+        rows, _ = api.read_tokens(cache, seq, pos)
+        rows[:, :512] *= back
+        got.append((out * back, lse, sums, rows))
+    for a, b in zip(got[0], got[1]):
+        assert torch.equal(a, b)
+    for a, b in zip(got[0], got[3]):
+        assert torch.equal(a, b)
+    assert not torch.equal(got[0][1], got[2][1])
