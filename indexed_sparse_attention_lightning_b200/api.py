@@ -112,7 +112,7 @@ def _there(f, given: dict):
     behind the kernels that use it.  Results that it made may be used on the
     caller's stream, which the allocator is told."""
     first = next(iter(given.values()))
-    first = first.page_table if isinstance(first, DeviceCache) else first
+    first = getattr(first, "page_table", first)
     if not isinstance(first, torch.Tensor) or first.get_device() < 0:
         raise SaError(_abi.SA_ERR_INVALID_ARG, f"{f.__name__}: CUDA tensors only")
     stream = given.pop("stream")

@@ -207,3 +207,13 @@ def test_arrays_that_are_too_short_are_refused(monkeypatch):
             call()
     # buffers of a larger capacity are fine
     api.evict_tokens(cache, sums, 64, dataclasses.replace(cache, seq_len=flat))
+
+
+def test_a_cache_need_only_look_like_one(monkeypatch):
+    """Any object with a cache's fields and struct(), on another stream too."""
+    cache, seq, pos = given()["read_tokens"]
+    like = types.SimpleNamespace(**vars(cache), struct=cache.struct)
+    World(monkeypatch)
+    for stream in (None, SIDE):
+        out, _ = api.read_tokens(like, seq, pos, stream=stream)
+        assert out.shape == (2, 576)
