@@ -356,7 +356,9 @@ SA_API sa_status sa_combine_partials(const float *o_part, const float *lse_part,
  *   weights are then those of the unscaled rows.
  *   A group that holds a NaN or an infinity, which e2m1 has not, takes the scale
  *   byte that is NaN (SA_MXFP4: 255, SA_NVFP4: 0x7F) and codes of +0, so that
- *   all of it reads back, and enters an attention, as NaN.
+ *   all of it reads back as NaN.  (A query that selects such a row gets NaN from
+ *   the tensor-core attention; the CUDA-core one gives out = 0 and lse = -inf for
+ *   logits that are NaN, over every pool.)
  * FP8 inputs must be finite: a NaN or infinity gives unspecified codes. */
 
 /* Indexer query -> e4m3 codes + one fp32 scale per (token, head): the form
